@@ -27,7 +27,9 @@ __all__ = ["MsqError", "PackedWeight", "plan", "quantize_pack", "allocate_packed
            "OPTION_FIELDS", "gemm_noalloc", "NOALLOC_SCRATCH_BYTES",
            "gemm_group", "group_workspace_bytes", "GROUP_MAX",
            "library_path", "load_library", "KERNELS", "FORMAT_VERSION", "GEMV_MAX_M",
-           "allocate_bits", "alloc_workspace_bytes", "ALLOC_LEVELS", "reorder_channels"]
+           "allocate_bits", "alloc_workspace_bytes", "ALLOC_LEVELS", "reorder_channels",
+           "KVCache", "allocate_kv_cache", "kv_write", "kv_read", "kv_attention",
+           "kv_attention_workspace_bytes", "KV_HEAD_DIMS", "KV_BLOCK_TOKENS"]
 
 FORMAT_VERSION = 2
 GEMV_MAX_M = 64
@@ -86,6 +88,29 @@ class _Weight(ctypes.Structure):
                 ("tile16_blocks", ctypes.c_int64)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("num_blocks", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_tokens", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _KvSeqs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("offset", ctypes.c_void_p),
+                ("total", ctypes.c_int64), ("max_count", ctypes.c_int32)]
+
+
+class _KvAttn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("q_dtype", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("kv_len", ctypes.c_void_p),
+                ("max_kv_len", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int32),
+                ("lse", ctypes.c_void_p)]
+
+
 def load_library():
     """Load libmsq.so once; raises OSError with the path if it is not built."""
     global _lib
@@ -132,6 +157,17 @@ def load_library():
     lib.msq_reorder_channels.restype = ctypes.c_int
     lib.msq_gemm_noalloc.argtypes = [vp, i64, ctypes.POINTER(_Weight), vp, vp]
     lib.msq_gemm_noalloc.restype = ctypes.c_int
+    cache_p, seqs_p = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvSeqs)
+    attn_p = ctypes.POINTER(_KvAttn)
+    lib.msq_kv_write.argtypes = [cache_p, seqs_p, vp, vp, i64, i64, vp, i64, i64, ctypes.c_int32,
+                                 vp]
+    lib.msq_kv_write.restype = ctypes.c_int
+    lib.msq_kv_read.argtypes = [cache_p, seqs_p, vp, vp, vp, ctypes.c_int32, vp]
+    lib.msq_kv_read.restype = ctypes.c_int
+    lib.msq_kv_attention_workspace_bytes.argtypes = [cache_p, seqs_p, attn_p]
+    lib.msq_kv_attention_workspace_bytes.restype = sz
+    lib.msq_kv_attention.argtypes = [cache_p, seqs_p, attn_p, vp, sz, vp]
+    lib.msq_kv_attention.restype = ctypes.c_int
     lib.msq_status_string.argtypes = [ctypes.c_int]
     lib.msq_status_string.restype = ctypes.c_char_p
     lib.msq_format_version.argtypes = []
@@ -465,3 +501,250 @@ def reorder_channels(saliency, reorder_rows: bool = True, workspace=None, stream
                                     pc.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                     _stream_handle(stream)), "msq_reorder_channels")
     return pr, pc
+
+
+# ---- 8-bit key/value cache ---------------------------------------------------------
+KV_HEAD_DIMS = (64, 128, 256)
+KV_BLOCK_TOKENS = (32, 64, 128, 256)
+
+
+@dataclass
+class KVCache:
+    """Device buffers of an 8-bit key/value cache: blocks of block_tokens tokens, one fp32
+    scale per block and head (layout and quantiser: include/msq.h).  Block tables say which
+    blocks a sequence has; handing blocks out is the caller's."""
+    num_blocks: int
+    kv_heads: int
+    head_dim: int
+    block_tokens: int
+    k_codes: "object"   # uint8 [num_blocks][kv_heads][block_tokens * head_dim]
+    v_codes: "object"
+    k_scale: "object"   # float32 [num_blocks][kv_heads]
+    v_scale: "object"
+
+    def __post_init__(self):
+        d = _KvCache()
+        d.num_blocks, d.kv_heads = self.num_blocks, self.kv_heads
+        d.head_dim, d.block_tokens = self.head_dim, self.block_tokens
+        d.k_codes, d.v_codes = self.k_codes.data_ptr(), self.v_codes.data_ptr()
+        d.k_scale, d.v_scale = self.k_scale.data_ptr(), self.v_scale.data_ptr()
+        self._desc = d
+
+    def descriptor(self) -> _KvCache:
+        return self._desc
+
+    @property
+    def device(self):
+        return self.k_codes.device
+
+    @property
+    def nbytes(self) -> int:
+        """Device bytes of the codes and scales."""
+        return 2 * int(self.k_codes.numel()) + 8 * int(self.k_scale.numel())
+
+
+def allocate_kv_cache(num_blocks: int, kv_heads: int, head_dim: int, block_tokens: int = 64,
+                      device="cuda") -> KVCache:
+    """An empty cache.  head_dim from KV_HEAD_DIMS, block_tokens from KV_BLOCK_TOKENS.  Codes
+    start undefined (no call uses slots that were never written); scales start at 0."""
+    torch = _torch()
+    if head_dim not in KV_HEAD_DIMS or block_tokens not in KV_BLOCK_TOKENS:
+        raise ValueError(f"head_dim must be one of {KV_HEAD_DIMS}, block_tokens of {KV_BLOCK_TOKENS}")
+    if num_blocks < 1 or kv_heads < 1:
+        raise ValueError("num_blocks and kv_heads must be positive")
+    dev = torch.device(device)
+    codes = [torch.empty((num_blocks, kv_heads, block_tokens * head_dim), dtype=torch.uint8,
+                         device=dev) for _ in range(2)]
+    scale = [torch.zeros((num_blocks, kv_heads), dtype=torch.float32, device=dev) for _ in range(2)]
+    return KVCache(num_blocks, kv_heads, head_dim, block_tokens, *codes, *scale)
+
+
+def _kv_dtype(dtype) -> int:
+    torch = _torch()
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float32:
+        return 1
+    raise TypeError(f"expected bfloat16 or float32, got {dtype}")
+
+
+def _kv_rows(t, name, heads, dim, device):
+    """t as [rows][heads][dim] the kernels can read: any token and head strides that are
+    multiples of 16 bytes with contiguous dims; anything else is copied."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [rows][{heads}][{dim}]")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the cache's device {device}")
+    per16 = 8 if _kv_dtype(t.dtype) == 0 else 4
+    st, sh, sd = t.stride()
+    if sd != 1 or st % per16 or sh % per16 or t.data_ptr() % 16:
+        t = t.clone(memory_format=_torch().contiguous_format)
+    return t
+
+
+def _kv_index(t, name, shape, device):
+    torch = _torch()
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be int32 {list(shape)} on {device}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+class _OnStream:
+    """Allocations inside belong to the stream the launch goes to, on the cache's device.
+    Tensors handed to use() are marked as used on that stream when it is not the current one."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        cur = torch.cuda.current_stream(device)
+        self.stream = cur if stream is None else stream
+        self.other = self.stream.cuda_stream != cur.cuda_stream
+        self.guard = (torch.cuda.stream(self.stream)
+                      if self.other or torch.cuda.current_device() != device.index else None)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def use(self, *tensors):
+        if self.other:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    @property
+    def handle(self) -> int:
+        return int(self.stream.cuda_stream)
+
+
+def _kv_seqs(cache: KVCache, block_table, offset, total: int, max_count: int):
+    batch = int(block_table.shape[0]) if block_table.dim() == 2 else -1
+    if batch < 0 or block_table.shape[1] < 1:
+        raise ValueError("block_table must be int32 [batch][entries]")
+    block_table = _kv_index(block_table, "block_table", tuple(block_table.shape), cache.device)
+    if offset is not None:
+        offset = _kv_index(offset, "offset", (batch + 1,), cache.device)
+    elif total % max(batch, 1) or (batch == 0 and total):
+        raise ValueError("without offset every sequence has the same number of rows")
+    s = _KvSeqs()
+    s.batch, s.table_width = batch, int(block_table.shape[1])
+    s.block_table = block_table.data_ptr()
+    s.offset = offset.data_ptr() if offset is not None else None
+    s.total, s.max_count = total, int(max_count)
+    return s, block_table, offset
+
+
+def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: int = 0,
+             stream=None) -> None:
+    """Quantise new tokens' keys and values into the cache (msq_kv_write).
+
+    k, v: [rows][kv_heads][head_dim] bf16 or fp32 (one type for both).  block_table: int32
+    [batch][entries].  first: int32 [batch], the position of each sequence's first new token,
+    which is the number of tokens it has in the cache (negative: leave the sequence out).
+    offset: int32 [batch + 1], sequence b's rows are offset[b] .. offset[b + 1] - 1; None:
+    rows / batch each.  max_count: the largest sequence's rows, if known (else all rows)."""
+    lib = load_library()
+    dev = cache.device
+    with _OnStream(dev, stream) as on:
+        kd = _kv_rows(k, "k", cache.kv_heads, cache.head_dim, dev)
+        vd = _kv_rows(v, "v", cache.kv_heads, cache.head_dim, dev)
+        if kd.shape[0] != vd.shape[0] or kd.dtype != vd.dtype:
+            raise ValueError("k and v must have the same rows and type")
+        s, table, offset = _kv_seqs(cache, block_table, offset, int(kd.shape[0]), max_count)
+        first = _kv_index(first, "first", (s.batch,), dev)
+        on.use(kd, vd, table, first, offset, cache.k_codes, cache.v_codes, cache.k_scale,
+               cache.v_scale)
+        _check(lib.msq_kv_write(cache.descriptor(), s, first.data_ptr(), kd.data_ptr(),
+                                kd.stride(0), kd.stride(1), vd.data_ptr(), vd.stride(0),
+                                vd.stride(1), _kv_dtype(kd.dtype), on.handle), "msq_kv_write")
+
+
+def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int] = None,
+            max_count: int = 0, dtype=None, stream=None):
+    """Read positions first[b] .. first[b] + rows - 1 of every sequence back (msq_kv_read):
+    (k, v), [total][kv_heads][head_dim] of dtype (bf16 unless given; or fp32), code * scale.
+    offset as in kv_write, total its last entry; with offset None, total / batch rows each."""
+    torch = _torch()
+    lib = load_library()
+    dev = cache.device
+    if total is None:
+        raise ValueError("total: the number of rows to read")
+    with _OnStream(dev, stream) as on:
+        s, table, offset = _kv_seqs(cache, block_table, offset, int(total), max_count)
+        first = _kv_index(first, "first", (s.batch,), dev)
+        shape = (s.total, cache.kv_heads, cache.head_dim)
+        dtype = torch.bfloat16 if dtype is None else dtype
+        code = _kv_dtype(dtype)
+        k = torch.empty(shape, dtype=dtype, device=dev)
+        v = torch.empty(shape, dtype=dtype, device=dev)
+        on.use(table, first, offset, cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale)
+        _check(lib.msq_kv_read(cache.descriptor(), s, first.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               code, on.handle), "msq_kv_read")
+    return k, v
+
+
+def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch: int,
+                                 max_count: int, max_kv_len: int, causal: bool = True,
+                                 window: int = 0) -> int:
+    """Workspace of kv_attention for calls of these sizes (rows: query rows of all sequences)
+    whose block tables have no more entries than max_kv_len tokens need."""
+    s, a = _KvSeqs(), _KvAttn()
+    s.batch, s.total, s.max_count = batch, rows, max_count
+    s.table_width = max(1, -(-max_kv_len // cache.block_tokens))
+    s.offset = 1  # only asked whether it is there
+    a.q_heads, a.max_kv_len, a.causal, a.window = q_heads, max_kv_len, int(causal), window
+    return int(load_library().msq_kv_attention_workspace_bytes(cache.descriptor(), s, a))
+
+
+def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count: int = 0,
+                 max_kv_len: int = 0, scale: float = 0.0, causal: bool = True, window: int = 0,
+                 out=None, out_dtype=None, return_lse: bool = False, workspace=None, stream=None):
+    """Attention of new tokens' queries over the cache (msq_kv_attention).
+
+    q: [rows][q_heads][head_dim] bf16 or fp32, q_heads a multiple of kv_heads.  kv_len: int32
+    [batch], the tokens each sequence has in the cache, the queries' own among them: with
+    causal, query i of n stands at position kv_len - n + i and sees positions up to its own,
+    the last `window` of them if window > 0.  offset, max_count as in kv_write.  max_kv_len:
+    about the largest kv_len, for the split of the work (0: the block table's length).
+    scale: of the scores (0: 1 / sqrt(head_dim)).  Returns out [rows][q_heads][head_dim] (bf16
+    unless out or out_dtype says fp32), with return_lse also the fp32 [rows][q_heads] natural
+    log of each row's softmax denominator.  A query that sees nothing gives zeros and -inf.
+    workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
+    torch = _torch()
+    lib = load_library()
+    dev = cache.device
+    if q.dim() != 3:
+        raise ValueError("q must be [rows][q_heads][head_dim]")
+    with _OnStream(dev, stream) as on:
+        heads = int(q.shape[1])
+        qd = _kv_rows(q, "q", heads, cache.head_dim, dev)
+        rows = int(qd.shape[0])
+        s, table, offset = _kv_seqs(cache, block_table, offset, rows, max_count)
+        kv_len = _kv_index(kv_len, "kv_len", (s.batch,), dev)
+        if out is None:
+            out = torch.empty((rows, heads, cache.head_dim), dtype=out_dtype or torch.bfloat16,
+                              device=dev)
+        elif tuple(out.shape) != (rows, heads, cache.head_dim) or not out.is_contiguous() or \
+                out.device != dev or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError("out must be contiguous, [rows][q_heads][head_dim], on the cache's device")
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
+        a = _KvAttn()
+        a.q, a.q_token_stride, a.q_head_stride = qd.data_ptr(), qd.stride(0), qd.stride(1)
+        a.q_dtype, a.q_heads = _kv_dtype(qd.dtype), heads
+        a.kv_len, a.max_kv_len = kv_len.data_ptr(), int(max_kv_len)
+        a.scale, a.causal, a.window = float(scale), int(bool(causal)), int(window)
+        a.out, a.out_dtype = out.data_ptr(), _kv_dtype(out.dtype)
+        a.lse = lse.data_ptr() if lse is not None else None
+        if workspace is None:
+            need = int(lib.msq_kv_attention_workspace_bytes(cache.descriptor(), s, a))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        on.use(qd, table, kv_len, offset, out, workspace, cache.k_codes, cache.v_codes,
+               cache.k_scale, cache.v_scale)
+        _check(lib.msq_kv_attention(cache.descriptor(), s, a, workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), on.handle),
+               "msq_kv_attention")
+    return (out, lse) if return_lse else out

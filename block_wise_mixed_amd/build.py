@@ -23,7 +23,7 @@ PROBE_SOURCES = ["msq_probe.hip"]
 ARCH = "gfx950"
 
 SOURCES = ["msq_host.cpp", "msq_pack.hip", "msq_gemv.hip", "msq_gemm.hip", "msq_alloc.hip",
-           "msq_reorder.hip", "msq_tile16.hip"]
+           "msq_reorder.hip", "msq_tile16.hip", "msq_kv.hip", "msq_kv_attn.hip"]
 
 # Device code: O3, no fast-math (correctly rounded division, denormals kept),
 # no packed-fp32 instructions.

@@ -1,0 +1,538 @@
+// Attention over the 8-bit key/value cache (msq_kv_attention).
+//
+// For a query row with scores x_t = c q.k_t (base-2 logarithms, c = scale *
+// log2 e) over the tokens it sees, o = sum 2^x_t v_t / sum 2^x_t.  One pass
+// keeps a reference exponent M, the weighted sum O = sum w_t code(v_t) and
+// the denominator L.  The scale s of a block's values is a factor of its
+// tokens' weights, w_t = 2^(x_t + log2 s - M), so no product with s is left
+// for O, and L = sum w_t / s.  M follows the largest weighted exponent: w is
+// rounded to f16, and this way its error is relative to the largest
+// contribution to O whatever the blocks' scales are.
+//
+// M is only moved when some weight would pass 2^14 (f16 ends at 2^16), and
+// then to 6 below the maximum: most tiles need neither the cross-lane maximum
+// nor a rescale, and weights down to 2^-20 of the largest stay normal f16
+// numbers.
+//
+// Codes become f16 exactly: the bytes code + 128 under the exponent byte 0x64
+// are the f16 numbers 1024 + byte, and one packed subtraction of 1152 leaves
+// the code.  A query row is scaled by the power of two that puts its largest
+// value in [2^14, 2^15), so bf16 queries are exact down to 2^-21 of it.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "msq.h"
+#include "msq_kv.h"
+
+namespace msq {
+namespace {
+
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kNone = -1e30f;    // M before any token
+constexpr float kTop = 14.f;       // weights stay below 2^kTop
+constexpr float kPlace = 6.f;      // a moved M puts the largest weight at 2^kPlace
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
+constexpr int kSpan = 32;          // tokens of one tile
+
+struct AttnArgs {
+  KvCacheView c;
+  KvSeqsView s;
+  const void* q;
+  int64_t qts, qhs;
+  const int32_t* kv_len;
+  void* out;
+  float* lse;
+  float* part_o;   // [nsplit][total * Hq][D], null for one split
+  float2* part_ml; // [nsplit][total * Hq]: M, L
+  int Hq, G, q_f32, out_f32, causal, window;
+  int nsplit;      // workgroups along a row tile's tokens
+  int span_tiles;  // tiles of one such part (more where nsplit parts cannot cover the range)
+  int row_tiles;
+  float c2;        // scale * log2 e
+};
+
+__device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ inline float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
+
+// Four bytes code + 128 -> four f16 codes.
+__device__ inline void codes_f16(uint32_t w, half2v& a, half2v& b) {
+  const half2v off = {(_Float16)(-1152.f), (_Float16)(-1152.f)};
+  a = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + off;
+  b = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + off;
+}
+__device__ inline half8 codes_f16x8(uint32_t w0, uint32_t w1) {
+  union {
+    half2v p[4];
+    half8 h;
+  } r;
+  codes_f16(w0, r.p[0], r.p[1]);
+  codes_f16(w1, r.p[2], r.p[3]);
+  return r.h;
+}
+
+// Eight query values as fp32.
+__device__ inline void load8(const void* q, int f32, int64_t at, float* x) {
+  if (f32) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(q) + at);
+    const float4 a = p[0], b = p[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(q) + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// The power of two 2^e that the row is multiplied by, from its largest
+// magnitude (NaN if the row has a non-finite value), and its inverse.
+__device__ inline void row_scale(float amax, bool bad, float& up, float& down) {
+  int e = 0;
+  if (amax > 0.f) {
+    (void)frexpf(amax, &e);  // amax = m 2^e, 1/2 <= m < 1
+    e = 15 - e;
+  }
+  e = min(max(e, -126), 126);
+  up = bad ? __uint_as_float(0x7FC00000u) : ldexpf(1.f, e);
+  down = ldexpf(1.f, -e);
+}
+
+// The positions lo <= t < hi that row i of n of a sequence with len tokens sees.
+__device__ inline void row_range(int len, int n, int i, int causal, int window, int& lo, int& hi) {
+  lo = 0;
+  hi = len;
+  if (causal) {
+    const int64_t pos = (int64_t)len - n + i;
+    hi = (int)max(min(pos + 1, (int64_t)len), (int64_t)0);
+    if (window > 0) lo = (int)max(pos - window + 1, (int64_t)0);
+  }
+}
+
+__device__ inline int clamped_len(const AttnArgs& a, int b) {
+  return min(max(a.kv_len[b], 0), a.s.width << a.c.shift);
+}
+
+__device__ inline void write_row(const AttnArgs& a, int64_t at, int n, const float* x) {
+  if (a.out_f32) {
+    float* p = reinterpret_cast<float*>(a.out) + at;
+    for (int i = 0; i < n; ++i) p[i] = x[i];
+  } else {
+    __bf16* p = reinterpret_cast<__bf16*>(a.out) + at;
+    for (int i = 0; i < n; ++i) p[i] = (__bf16)x[i];
+  }
+}
+
+extern __shared__ __align__(16) unsigned char smem_kv[];
+
+// ---- few query rows --------------------------------------------------------
+// Workgroup: 16 query rows (new tokens x the heads of one kv head) and one
+// part of their tokens; its four wavefronts take the part's tiles of 32
+// tokens in turn, straight from HBM into registers (the cache order is the
+// operand order), the next tile's loads in flight during the current one's
+// products.  S^T = K Q^T (16 x 16 x 32, tokens down, rows across), whose
+// result registers are the B operand of O^T = V^T P^T: no LDS in the loop.
+// Bound by HBM: 2 D bytes a token and kv head.
+template <int D>
+struct Tile {
+  uint4 k[D / 32];  // [16-token half][64-dim chunk]
+  uint4 v[D / 32];  // [32-dim chunk]
+};
+
+template <int D>
+__device__ inline void load_tile(Tile<D>& t, const KvCacheView& c, int id, int h, int tile,
+                                 int lane) {
+  const int P = 1 << c.shift;
+  const int64_t at = ((int64_t)max(id, 0) * c.H + h) * P * D +
+                     (int64_t)((tile * kSpan) & (P - 1)) * D;
+  const uint4* k = reinterpret_cast<const uint4*>(c.kc + at) + lane;
+  const uint4* v = reinterpret_cast<const uint4*>(c.vc + at) + lane;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) t.k[i] = k[64 * i];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) t.v[i] = v[64 * i];
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
+  constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
+  constexpr int kStride = D + 4;
+  int64_t wg = blockIdx.x;
+  const int h = (int)(wg % a.c.H);
+  wg /= a.c.H;
+  const int sp = (int)(wg % a.nsplit);
+  wg /= a.nsplit;
+  const int tile_row = (int)(wg % a.row_tiles), b = (int)(wg / a.row_tiles);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  int row0, n;
+  kv_rows(a.s, b, row0, n);
+  const int64_t rows = (int64_t)n * a.G;
+  const int64_t r0 = (int64_t)tile_row * 16;
+  if (r0 >= rows) return;
+  const int len = clamped_len(a, b);
+  // the tile's rows: their tokens' range, and where no mask is needed
+  const int i0 = (int)(r0 / a.G), i1 = (int)(min(r0 + 15, rows - 1) / a.G);
+  int lo, hi, lo1, hi0;
+  row_range(len, n, i0, a.causal, a.window, lo, hi0);
+  row_range(len, n, i1, a.causal, a.window, lo1, hi);
+  const int t_first = lo / kSpan, t_end = (hi + kSpan - 1) / kSpan;
+  const int span = max(a.span_tiles, (t_end - t_first + a.nsplit - 1) / a.nsplit);
+  const int t0 = t_first + sp * span, t1 = min(t0 + span, t_end);
+  if (t0 >= t1 && a.nsplit > 1) return;  // the join looks at the parts that have tiles only
+
+  const int64_t r = min(r0 + col, rows - 1);
+  const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
+  int my_lo, my_hi;
+  row_range(len, n, i, a.causal, a.window, my_lo, my_hi);
+
+  // query fragments: slots (g, e) of step 2c + u are dims 64c + 16g + 8u + e
+  half8 q[kSteps];
+  float down;
+  {
+    float x[kSteps][8], amax = 0.f;
+    bool bad = false;
+    const int64_t at = (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      load8(a.q, a.q_f32, at + 64 * (s >> 1) + 16 * g + 8 * (s & 1), x[s]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        amax = fmaxf(amax, fabsf(x[s][e]));
+        bad |= !(fabsf(x[s][e]) <= 3.402823466e38f);
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor(amax, 16));
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    int nb = bad;
+    nb |= __shfl_xor(nb, 16);
+    nb |= __shfl_xor(nb, 32);
+    float up;
+    row_scale(amax, nb != 0, up, down);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(x[s][e] * up);
+  }
+  const float cq = a.c2 * down;
+
+  f32x4 o[kTiles];
+#pragma unroll
+  for (int d = 0; d < kTiles; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float M = kNone, L = 0.f;
+
+  const int shift = a.c.shift - 5;  // tiles per block, as a shift
+  auto block_of = [&](int t) {
+    return __builtin_amdgcn_readfirstlane(kv_block(a.c, a.s, b, t >> shift));
+  };
+  Tile<D> cur, nxt;
+  int t = t0 + wave, id = -1, id_n = -1;
+  if (t < t1) {
+    id = block_of(t);
+    load_tile<D>(cur, a.c, id, h, t, lane);
+  }
+  if (t + kWaves < t1) id_n = block_of(t + kWaves);
+  for (; t < t1; t += kWaves) {
+    const bool more = t + kWaves < t1;
+    if (more) load_tile<D>(nxt, a.c, id_n, h, t + kWaves, lane);
+    const int id_nn = t + 2 * kWaves < t1 ? block_of(t + 2 * kWaves) : -1;
+    if (id >= 0) {
+      const int64_t hb = (int64_t)id * a.c.H + h;
+      const float sk = a.c.ks[hb], sv = a.c.vs[hb];
+      f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const uint4 k0 = cur.k[c], k1 = cur.k[D / 64 + c];
+        s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.x, k0.y), q[2 * c], s0, 0, 0, 0);
+        s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.x, k1.y), q[2 * c], s1, 0, 0, 0);
+        s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.z, k0.w), q[2 * c + 1], s0, 0, 0, 0);
+        s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.z, k1.w), q[2 * c + 1], s1, 0, 0, 0);
+      }
+      // lane (col, g): scores of row col at tokens 4g + 0..3 and 16 + 4g + 0..3
+      const float f = cq * sk;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = s0[e] * f;
+        x[4 + e] = s1[e] * f;
+      }
+      const int tok = t * kSpan;
+      if (tok < lo1 || tok + kSpan > hi0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int p = tok + 4 * g + (e & 3) + 16 * (e >> 2);
+          if (p < my_lo || p >= my_hi) x[e] = -INFINITY;
+        }
+      }
+      // a block of zeros takes no part in placing M: any scale stands for it
+      const float s = fmaxf(sv, kTiny);
+      const float lam = sv > 0.f ? log2_fast(s) : 0.f;
+      const float inv = sv > 0.f ? 1.f / s : 1.f;
+      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      if (__any(top + lam > M + kTop)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (top + lam > M + kTop) {
+          const float m = top + lam - kPlace;
+          const float al = exp2_fast(M - m);
+          L *= al;
+#pragma unroll
+          for (int d = 0; d < kTiles; ++d) o[d] *= al;
+          M = m;
+        }
+      }
+      const float add = lam - M;
+      float sum = 0.f;
+      half8 p;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float w = exp2_fast(x[e] + add);
+        sum += w;
+        p[e] = (_Float16)w;
+      }
+      L += sum * inv;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint4 v = cur.v[c];
+        o[2 * c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.x, v.y), p, o[2 * c], 0, 0, 0);
+        o[2 * c + 1] =
+            __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.z, v.w), p, o[2 * c + 1], 0, 0, 0);
+      }
+    }
+    cur = nxt;
+    id = id_n;
+    id_n = id_nn;
+  }
+
+  // join the wavefronts: M and L per row, then the weighted sum of O
+  L += __shfl_xor(L, 16);
+  L += __shfl_xor(L, 32);
+  float* lo_o = reinterpret_cast<float*>(smem_kv);           // [wave][16][kStride]
+  float* lo_m = lo_o + kWaves * 16 * kStride;                 // [wave][16]
+  float* lo_l = lo_m + kWaves * 16;
+#pragma unroll
+  for (int d = 0; d < kTiles; ++d)
+    *reinterpret_cast<f32x4*>(lo_o + (wave * 16 + col) * kStride + 16 * d + 4 * g) = o[d];
+  if (g == 0) {
+    lo_m[wave * 16 + col] = M;
+    lo_l[wave * 16 + col] = L;
+  }
+  __syncthreads();
+  constexpr int kPer = D / 16;  // outputs per thread: 16 threads a row
+  const int rr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kPer;
+  if (r0 + rr >= rows) return;
+  float m = kNone;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, lo_m[w * 16 + rr]);
+  float x[kPer], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const float f = exp2_fast(lo_m[w * 16 + rr] - m);
+    l += f * lo_l[w * 16 + rr];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] += f * lo_o[(w * 16 + rr) * kStride + d0 + e];
+  }
+  const int64_t ro = r0 + rr;
+  const int io = (int)(ro / a.G);
+  const int64_t orow = (int64_t)(row0 + io) * a.Hq + h * a.G + (int)(ro - (int64_t)io * a.G);
+  if (a.nsplit > 1) {
+    const int64_t pr = (int64_t)sp * a.s.total * a.Hq + orow;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) a.part_o[pr * D + d0 + e] = x[e];
+    if (d0 == 0) a.part_ml[pr] = make_float2(m, l);
+    return;
+  }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = l == 0.f ? 0.f : x[e] * f;
+  write_row(a, orow * D + d0, kPer, x);
+  if (a.lse && d0 == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
+}
+
+// ---- the join of a split call ----------------------------------------------
+// One wavefront a query row and head: the parts that have tiles, in order.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows_per_tile, int64_t most) {
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // (b, i, head)
+  const int per = a.s.max_count;
+  if (w >= most) return;
+  const int hq = (int)(w % a.Hq);
+  const int i = (int)(w / a.Hq % per), b = (int)(w / a.Hq / per);
+  int row0, n;
+  kv_rows(a.s, b, row0, n);
+  if (i >= n) return;
+  const int len = clamped_len(a, b);
+  // the row tile this row was in, as the split kernel saw it
+  const int64_t rows = (int64_t)n * a.G, r = (int64_t)i * a.G + hq % a.G;
+  const int64_t r0 = r / rows_per_tile * rows_per_tile;
+  const int i0 = (int)(r0 / a.G), i1 = (int)(min(r0 + rows_per_tile - 1, rows - 1) / a.G);
+  int lo, hi, x0, x1;
+  row_range(len, n, i0, a.causal, a.window, lo, x1);
+  row_range(len, n, i1, a.causal, a.window, x0, hi);
+  const int t_first = lo / kSpan, t_end = (hi + kSpan - 1) / kSpan;
+  const int tiles = max(t_end - t_first, 0);
+  const int span = max(a.span_tiles, (tiles + a.nsplit - 1) / a.nsplit);
+  const int parts = (tiles + span - 1) / span;
+  const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq, step = (int64_t)a.s.total * a.Hq;
+  float m = kNone;
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[p * step + orow].x);
+  float l = 0.f, x[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) x[e] = 0.f;
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = a.part_ml[p * step + orow];
+    const float f = exp2_fast(ml.x - m);
+    l += f * ml.y;
+    const float* po = a.part_o + (p * step + orow) * D + lane * (D / 64);
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) x[e] += f * po[e];
+  }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) x[e] = l == 0.f ? 0.f : x[e] * f;
+  write_row(a, orow * D + lane * (D / 64), D / 64, x);
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
+}
+
+// ---- host ------------------------------------------------------------------
+struct AttnPlan {
+  int rows_per_tile, row_tiles, nsplit, span_tiles;
+  int64_t blocks;     // workgroups of the attention launch
+  size_t workspace, ml_at;
+};
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Sizes only; MSQ_OK with blocks == 0 for an empty call.
+msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_attn& t, int D,
+                     AttnPlan& p) {
+  p = AttnPlan{};
+  if (t.q_heads < 1 || t.q_heads % c.H != 0 || t.window < 0 || t.max_kv_len < 0)
+    return MSQ_ERR_SHAPE;
+  if (t.window > 0 && !t.causal) return MSQ_ERR_INVALID_ARG;
+  if (s.batch == 0 || s.total == 0) return MSQ_OK;
+  const int64_t G = t.q_heads / c.H;
+  if ((int64_t)s.total * t.q_heads > (int64_t)0x7FFFFFFF ||
+      (int64_t)s.max_count * G > (int64_t)0x7FFFFFFF - 256)
+    return MSQ_ERR_SHAPE;
+  int64_t longest = (int64_t)s.width << c.shift;
+  if (t.max_kv_len > 0) longest = std::min(longest, t.max_kv_len);
+  if (t.window > 0) longest = std::min<int64_t>(longest, (int64_t)t.window + s.max_count + kSpan);
+  const int64_t tiles = std::max<int64_t>(1, (longest + kSpan - 1) / kSpan);
+  p.rows_per_tile = 16;
+  p.row_tiles = (int)((s.max_count * G + p.rows_per_tile - 1) / p.rows_per_tile);
+  const int64_t items = (int64_t)s.batch * c.H * p.row_tiles;
+  // parts: about four workgroups a compute unit, each at least 8 tiles
+  const int64_t want = std::max<int64_t>(1, 1024 / items);
+  int64_t span = std::max<int64_t>(8, (tiles + want - 1) / want);
+  span = std::min<int64_t>(span, 64);
+  p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, 256);
+  p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
+  p.blocks = items * p.nsplit;
+  if (p.blocks > (int64_t)0x7FFFFFFF) return MSQ_ERR_SHAPE;
+  if (p.nsplit > 1) {
+    // the join's grid: four (sequence, row, head) a workgroup
+    if ((int64_t)s.batch * s.max_count * G > (int64_t)0x7FFFFFFF * 4 / c.H) return MSQ_ERR_SHAPE;
+    const size_t rows = (size_t)s.total * t.q_heads * p.nsplit;
+    p.ml_at = (rows * D * 4 + 255) / 256 * 256;
+    p.workspace = p.ml_at + rows * 8;
+  }
+  return MSQ_OK;
+}
+
+template <int D>
+hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  const size_t lds = 4 * 16 * (D + 4) * 4 + 2 * 4 * 16 * 4;
+  hipLaunchKernelGGL((k_kv_decode<D>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
+  if (p.nsplit > 1) {
+    const int64_t most = (int64_t)a.s.batch * a.s.max_count * a.Hq;
+    hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)((most + 3) / 4)), dim3(256), 0, stream, a,
+                       p.rows_per_tile, most);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace msq
+
+using namespace msq;
+
+extern "C" size_t msq_kv_attention_workspace_bytes(const msq_kv_cache* cache,
+                                                   const msq_kv_seqs* seqs,
+                                                   const msq_kv_attn* attn) {
+  KvCacheView c;
+  KvSeqsView s;
+  AttnPlan p;
+  if (!attn || kv_views(cache, seqs, c, s) != MSQ_OK) return 0;
+  if (plan_attn(c, s, *attn, cache->head_dim, p) != MSQ_OK) return 0;
+  return p.workspace;
+}
+
+extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
+                                       const msq_kv_attn* attn, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+  if (!attn) return MSQ_ERR_INVALID_ARG;
+  AttnArgs a{};
+  msq_status st = kv_views(cache, seqs, a.c, a.s);
+  if (st != MSQ_OK) return st;
+  const msq_kv_attn& t = *attn;
+  const int D = cache->head_dim;
+  if ((t.q_dtype != MSQ_DTYPE_BF16 && t.q_dtype != MSQ_DTYPE_F32) ||
+      (t.out_dtype != MSQ_DTYPE_BF16 && t.out_dtype != MSQ_DTYPE_F32) ||
+      !(t.scale >= 0.f) || !std::isfinite(t.scale))
+    return MSQ_ERR_INVALID_ARG;
+  AttnPlan p;
+  st = plan_attn(a.c, a.s, t, D, p);
+  if (st != MSQ_OK || p.blocks == 0) return st;
+  st = kv_pointers(cache, seqs);
+  if (st != MSQ_OK) return st;
+  const int64_t per16 = t.q_dtype == MSQ_DTYPE_F32 ? 4 : 8;
+  if (!t.q || !t.kv_len || !t.out || !aligned_to(t.q, 16) || !aligned_to(t.out, 16) ||
+      !aligned_to(t.kv_len, 4) || !aligned_to(t.lse, 4) || t.q_token_stride % per16 ||
+      t.q_head_stride % per16)
+    return MSQ_ERR_INVALID_ARG;
+  if (p.workspace > 0) {
+    if (workspace_bytes < p.workspace) return MSQ_ERR_BUFFER_TOO_SMALL;
+    if (!workspace || !aligned_to(workspace, 256)) return MSQ_ERR_INVALID_ARG;
+    a.part_o = reinterpret_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(workspace) + p.ml_at);
+  }
+  a.q = t.q;
+  a.qts = t.q_token_stride;
+  a.qhs = t.q_head_stride;
+  a.kv_len = t.kv_len;
+  a.out = t.out;
+  a.lse = t.lse;
+  a.Hq = t.q_heads;
+  a.G = t.q_heads / a.c.H;
+  a.q_f32 = t.q_dtype == MSQ_DTYPE_F32;
+  a.out_f32 = t.out_dtype == MSQ_DTYPE_F32;
+  a.causal = t.causal != 0;
+  a.window = t.window;
+  a.nsplit = p.nsplit;
+  a.span_tiles = p.span_tiles;
+  a.row_tiles = p.row_tiles;
+  a.c2 = (t.scale > 0.f ? t.scale : 1.f / std::sqrt((float)D)) * kLog2e;
+  hipError_t e;
+  switch (D) {
+    case 64: e = launch_attn<64>(a, p, stream); break;
+    case 128: e = launch_attn<128>(a, p, stream); break;
+    default: e = launch_attn<256>(a, p, stream); break;
+  }
+  return e == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
+}

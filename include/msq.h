@@ -360,6 +360,133 @@ msq_status msq_reorder_channels(const float *saliency, int64_t N, int64_t K, int
                                 int32_t *perm_row, int32_t *perm_col, void *workspace,
                                 size_t workspace_bytes, hipStream_t stream);
 
+/* ---- 8-bit key/value cache ------------------------------------------------
+ * Between the q, k, v products of a decoder layer and its o product stands
+ * attention over the keys and values of all tokens so far.  The cache holds
+ * them as 8-bit integers: blocks of block_tokens tokens x head_dim values
+ * for every key/value head, one fp32 scale per (block, head), keys and
+ * values apart.  A block table strings blocks together per sequence:
+ * position t of sequence b is slot t % block_tokens of block
+ * block_table[b][t / block_tokens].
+ *
+ * Quantiser, in IEEE fp32 rounded after every operation, for the new tokens
+ * that one call puts into one block, per head, keys and values apart:
+ *     a = max |x| over their finite values,  s = a / 127
+ *     if the block already holds earlier tokens of the sequence: s = max(s, its scale)
+ *     new code     = clamp(rint(x / s), -127, 127)   (0 if s == 0 or x is NaN)
+ *     earlier code = unchanged, or rint((code * old) / s) where s > old
+ * so infinite values take the code +-127.  A block counts as holding earlier
+ * tokens when the call's first position lies inside it past its slot 0; a
+ * call that writes slot 0 begins the block anew.  The value a code stands
+ * for is code * s.  (Writing a run of tokens in several calls can give other
+ * codes than one call, since a scale that grows rounds earlier codes again.)
+ *
+ * Codes are stored as uint8 code + 128, in the order in which a wavefront
+ * feeds them to the matrix instructions, so that every load is 16 contiguous
+ * bytes a lane (1 KiB a wavefront).  Inside the block_tokens * head_dim bytes
+ * of (block, head), for slot t and dim d:
+ *   keys:   byte 16*D*(t / 16) + 1024*(d / 64) + 16*((t % 16) + 16*((d / 16) % 4)) + d % 16
+ *   values: byte 32*D*(t / 32) + 1024*(d / 32) + 16*((d % 16) + 16*((t % 16) / 4))
+ *                + 8*((d / 16) % 2) + 4*((t / 16) % 2) + t % 4
+ * Slots that were never written hold unspecified codes; no call uses them
+ * beyond a sequence's length.
+ *
+ * All pointers inside the structs are device pointers.  The kernels read
+ * lengths, offsets and the table on the device (no host synchronization) and
+ * never leave the buffers the structs size, whatever these hold: table
+ * entries outside 0 .. num_blocks - 1 mark absent blocks (writes to them are
+ * dropped, their tokens are not seen, reads give 0), positions outside the
+ * table likewise, and offsets are clamped to 0 .. total. */
+#define MSQ_DTYPE_BF16 0
+#define MSQ_DTYPE_F32 1
+
+typedef struct {
+  int64_t num_blocks;   /* blocks in the cache, 1 .. 2^31 - 1 */
+  int32_t kv_heads;     /* key/value heads, >= 1 */
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t block_tokens; /* 32, 64, 128 or 256 */
+  uint8_t *k_codes;     /* [num_blocks][kv_heads][block_tokens * head_dim], 16-byte aligned */
+  uint8_t *v_codes;     /* the same for the values */
+  float *k_scale;       /* [num_blocks][kv_heads] */
+  float *v_scale;       /* [num_blocks][kv_heads] */
+} msq_kv_cache;
+
+/* The sequences of one call and their rows in its ragged [total][heads][dim]
+ * tensors: sequence b has rows offset[b] .. offset[b + 1] - 1, or, with a
+ * null offset, total / batch rows each (total must then be a multiple of
+ * batch). */
+typedef struct {
+  int32_t batch;              /* sequences, >= 0 */
+  int32_t table_width;        /* block-table entries per sequence, >= 1;
+                                 table_width * block_tokens < 2^31 */
+  const int32_t *block_table; /* [batch][table_width] */
+  const int32_t *offset;      /* [batch + 1], non-decreasing, or null */
+  int64_t total;              /* rows of all sequences, 0 .. 2^31 - 1 */
+  int32_t max_count;          /* at least the largest sequence's rows; rows past it are not
+                                 processed.  0: total.  Ignored with a null offset */
+} msq_kv_seqs;
+
+/* Quantises k and v rows into the cache: row i of sequence b goes to position
+ * first[b] + i; a sequence with first[b] < 0 is left out.  A block may be
+ * written for one sequence only per call.  k, v: [total][kv_heads][head_dim]
+ * of dtype, with token and head strides in elements (dims contiguous; 16-byte
+ * aligned pointers and byte strides).  One launch, asynchronous.
+ * Errors: MSQ_ERR_INVALID_ARG (null or misaligned pointer, unknown dtype),
+ * MSQ_ERR_SHAPE (a size outside the ranges above), MSQ_ERR_UNSUPPORTED
+ * (head_dim or block_tokens not listed above), MSQ_ERR_HIP. */
+msq_status msq_kv_write(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
+                        const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                        const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                        int32_t dtype, hipStream_t stream);
+
+/* Reads positions first[b] .. first[b] + count - 1 of every sequence back
+ * into k and v ([total][kv_heads][head_dim] of dtype, contiguous, 16-byte
+ * aligned): code * scale in fp32, rounded once more for bf16.  Errors as
+ * msq_kv_write. */
+msq_status msq_kv_read(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
+                       void *k, void *v, int32_t dtype, hipStream_t stream);
+
+/* One attention call over the cache. */
+typedef struct {
+  const void *q;           /* [total][q_heads][head_dim] of q_dtype, 16-byte aligned */
+  int64_t q_token_stride;  /* in elements; byte strides multiples of 16 */
+  int64_t q_head_stride;
+  int32_t q_dtype;
+  int32_t q_heads;         /* a multiple of kv_heads; query head h reads kv head
+                              h / (q_heads / kv_heads) */
+  const int32_t *kv_len;   /* [batch]: tokens of each sequence in the cache */
+  int64_t max_kv_len;      /* about the largest kv_len, for the split of the work (any value
+                              gives right results); 0: table_width * block_tokens */
+  float scale;             /* of the scores, finite and > 0; 0: 1 / sqrt(head_dim) */
+  int32_t causal;          /* nonzero: row i of n stands at position kv_len - n + i and sees
+                              positions up to its own; 0: every row sees all kv_len */
+  int32_t window;          /* > 0: of those only the last window positions (causal only); 0: all */
+  void *out;               /* [total][q_heads][head_dim] of out_dtype, contiguous, 16-byte aligned */
+  int32_t out_dtype;
+  float *lse;              /* [total][q_heads] or null: natural log of the softmax denominator,
+                              -inf for a row that sees nothing */
+} msq_kv_attn;
+
+/* Bytes of device workspace msq_kv_attention needs (0 for arguments it
+ * refuses and for calls that need none).  Only sizes are looked at: batch,
+ * table_width, total, max_count, whether offset is null, q_heads, max_kv_len, causal and
+ * window. */
+size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
+                                        const msq_kv_attn *attn);
+
+/* out = softmax(scale * q . k) . v over the cached tokens each query row
+ * sees; a row that sees nothing gives zeros, a row with a non-finite query
+ * value gives NaN.  Products run on the f16 matrix instructions: codes are
+ * exact there, the query row is scaled by a power of two and the softmax
+ * weights are rounded to f16; scores, softmax statistics and sums are fp32.
+ * workspace: msq_kv_attention_workspace_bytes, 256-byte aligned; calls that
+ * share one must be ordered on one stream.  One launch, and one more to join
+ * the parts where a sequence's tokens are split over workgroups.  Errors as
+ * msq_kv_write, plus MSQ_ERR_BUFFER_TOO_SMALL. */
+msq_status msq_kv_attention(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
+                            const msq_kv_attn *attn, void *workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
 /* Static English text for a status code; never NULL.  Takes an int so that
  * any value a caller holds, including one outside the enum, is defined input
  * ("unknown status"). */
