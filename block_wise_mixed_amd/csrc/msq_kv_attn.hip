@@ -33,6 +33,7 @@ namespace {
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kNone = -1e30f;    // M before any token
 constexpr float kTop = 14.f;       // weights stay below 2^kTop
@@ -40,7 +41,10 @@ constexpr float kPlace = 6.f;      // a moved M puts the largest weight at 2^kPl
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
-constexpr int kSpan = 32;          // tokens of one tile
+constexpr int kSpan = 32;          // tokens of a tile of k_kv_decode
+constexpr int kRowTile = 16;       // and its query rows
+constexpr int kStage = 64;         // tokens of a tile of k_kv_prefill
+constexpr float kTinyStep = 1e-37f;  // keeps -inf * step from being NaN where a step is 0
 
 struct AttnArgs {
   KvCacheView c;
@@ -55,7 +59,7 @@ struct AttnArgs {
   int Hq, G, q_f32, out_f32, causal, window;
   int nsplit;      // workgroups along a row tile's tokens
   int span_tiles;  // tiles of one such part (more where nsplit parts cannot cover the range)
-  int row_tiles;
+  int row_tiles, tile_rows, tile_tokens;
   float c2;        // scale * log2 e
 };
 
@@ -134,6 +138,50 @@ __device__ inline void write_row(const AttnArgs& a, int64_t at, int n, const flo
   }
 }
 
+__device__ inline void write4(const AttnArgs& a, int64_t at, const float* x) {
+  if (a.out_f32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    union {
+      __bf16 b[4];
+      uint2 u;
+    } o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.b[i] = (__bf16)x[i];
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) = o.u;
+  }
+}
+
+// The tiles of a part: query rows r0 .. of a sequence with n * G rows see the
+// tokens lo .. hi - 1 between them, cut into tiles of tile_tokens and those
+// into parts of the same number of tiles.
+struct Parts {
+  int lo, hi;          // of all rows together
+  int lo_last, hi_first;  // tokens from lo_last to hi_first are seen by every row
+  int first, end;      // tiles
+  int span;            // tiles per part
+};
+__device__ inline Parts parts_of(const AttnArgs& a, int len, int n, int64_t r0) {
+  Parts p;
+  const int64_t rows = (int64_t)n * a.G;
+  const int i0 = (int)(r0 / a.G), i1 = (int)(min(r0 + a.tile_rows, rows) - 1) / a.G;
+  row_range(len, n, i0, a.causal, a.window, p.lo, p.hi_first);
+  row_range(len, n, i1, a.causal, a.window, p.lo_last, p.hi);
+  p.first = p.lo / a.tile_tokens;
+  p.end = max(p.first, (int)(((int64_t)p.hi + a.tile_tokens - 1) / a.tile_tokens));
+  p.span = max(a.span_tiles, (p.end - p.first + a.nsplit - 1) / a.nsplit);
+  return p;
+}
+
+// Workgroup barrier that waits for the wavefront's LDS operations only (global
+// loads stay in flight).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 extern __shared__ __align__(16) unsigned char smem_kv[];
 
 // ---- few query rows --------------------------------------------------------
@@ -179,17 +227,12 @@ __global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
   int row0, n;
   kv_rows(a.s, b, row0, n);
   const int64_t rows = (int64_t)n * a.G;
-  const int64_t r0 = (int64_t)tile_row * 16;
+  const int64_t r0 = (int64_t)tile_row * kRowTile;
   if (r0 >= rows) return;
   const int len = clamped_len(a, b);
-  // the tile's rows: their tokens' range, and where no mask is needed
-  const int i0 = (int)(r0 / a.G), i1 = (int)(min(r0 + 15, rows - 1) / a.G);
-  int lo, hi, lo1, hi0;
-  row_range(len, n, i0, a.causal, a.window, lo, hi0);
-  row_range(len, n, i1, a.causal, a.window, lo1, hi);
-  const int t_first = lo / kSpan, t_end = (hi + kSpan - 1) / kSpan;
-  const int span = max(a.span_tiles, (t_end - t_first + a.nsplit - 1) / a.nsplit);
-  const int t0 = t_first + sp * span, t1 = min(t0 + span, t_end);
+  const Parts pt = parts_of(a, len, n, r0);
+  const int lo1 = pt.lo_last, hi0 = pt.hi_first;
+  const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   if (t0 >= t1 && a.nsplit > 1) return;  // the join looks at the parts that have tiles only
 
   const int64_t r = min(r0 + col, rows - 1);
@@ -363,10 +406,267 @@ __global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
   if (a.lse && d0 == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
 }
 
+// ---- many query rows -------------------------------------------------------
+// Workgroup: 32 kWaves query rows of one kv head and one part of their
+// tokens, 64 tokens at a time.  The workgroup turns each tile's codes into f16
+// once, in LDS, in operand order (two buffers; the next tile's codes are
+// loaded during the current one's products and converted before its barrier);
+// each wavefront holds 32 rows: S^T = K Q^T (32 x 32 x 16), softmax in
+// registers, O^T += V^T P^T with the score registers as operand.  Inside 32
+// tokens the key rows are placed so that those registers hold the weights in
+// the order of the value codes: token t is row t with bits 3 and 4 swapped.
+template <int D, int kWaves>
+struct Stage {
+  uint4 k[D * kStage / 16 / (64 * kWaves)], v[D * kStage / 16 / (64 * kWaves)];
+};
+
+template <int D, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
+  constexpr int kThreads = 64 * kWaves, kSteps = D / 16, kTiles = D / 32;
+  constexpr int kUnits = D * kStage / 16 / kThreads;  // 16-byte pieces of K (and of V) a thread
+  constexpr int kBuf = 2 * kStage * D * 2;            // bytes of one K and V buffer
+  int64_t wg = blockIdx.x;
+  const int h = (int)(wg % a.c.H);
+  wg /= a.c.H;
+  const int sp = (int)(wg % a.nsplit);
+  wg /= a.nsplit;
+  const int b = (int)(wg % a.s.batch);
+  const int tile_row = a.row_tiles - 1 - (int)(wg / a.s.batch);  // the longest rows first
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  int row0, n;
+  kv_rows(a.s, b, row0, n);
+  const int64_t rows = (int64_t)n * a.G;
+  const int64_t r0 = (int64_t)tile_row * (32 * kWaves);
+  if (r0 >= rows) return;
+  const int len = clamped_len(a, b);
+  const Parts pt = parts_of(a, len, n, r0);
+  const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
+  if (t0 >= t1 && a.nsplit > 1) return;
+
+  // this wavefront's rows (past the end: the last row again, never written)
+  const int64_t w0 = r0 + 32 * wave;
+  const int64_t r = min(w0 + col, rows - 1);
+  const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
+  int my_lo, my_hi;
+  row_range(len, n, i, a.causal, a.window, my_lo, my_hi);
+  int w_lo, w_hi, w_lo_last, w_hi_first;
+  row_range(len, n, (int)(min(w0, rows - 1) / a.G), a.causal, a.window, w_lo, w_hi_first);
+  row_range(len, n, (int)(min(w0 + 31, rows - 1) / a.G), a.causal, a.window, w_lo_last, w_hi);
+  if (w0 >= rows) w_hi = 0;
+
+  half8 q[kSteps];  // slots (half, e) of step s are dims 16 s + 8 half + e
+  float cq;
+  {
+    const int64_t at = (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs + 8 * half;
+    float amax = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float x[8];
+      load8(a.q, a.q_f32, at + 16 * s, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        amax = fmaxf(amax, fabsf(x[e]));
+        bad |= !(fabsf(x[e]) <= 3.402823466e38f);
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    int nb = bad;
+    nb |= __shfl_xor(nb, 32);
+    float up, down;
+    row_scale(amax, nb != 0, up, down);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      float x[8];
+      load8(a.q, a.q_f32, at + 16 * s, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(x[e] * up);
+    }
+    cq = a.c2 * down;
+  }
+
+  f32x16 o[kTiles];
+#pragma unroll
+  for (int d = 0; d < kTiles; ++d) o[d] = f32x16{};
+  float M = kNone, L = 0.f;
+
+  // blocks, key and value scales of a tile's two halves of 32 tokens
+  struct Meta {
+    int id[2];
+    float sk[2], sv[2];
+  };
+  const int P = 1 << a.c.shift;
+  auto meta_of = [&](int t, Meta& m) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t tok = (int64_t)t * kStage + 32 * u;
+      m.id[u] = __builtin_amdgcn_readfirstlane(kv_block(a.c, a.s, b, tok >> a.c.shift));
+      // a half without tokens: its block may be absent or never written, whose
+      // scales may be anything
+      const bool none = m.id[u] < 0 || tok >= len;
+      const int64_t hb = (int64_t)max(m.id[u], 0) * a.c.H + h;
+      m.sk[u] = none ? 0.f : a.c.ks[hb];
+      m.sv[u] = none ? 0.f : a.c.vs[hb];
+    }
+  };
+  auto load = [&](int t, const Meta& m, Stage<D, kWaves>& st) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int hf = __builtin_amdgcn_readfirstlane((64 * wave + kThreads * u) / (2 * D));
+      const int tok = (t * kStage + 32 * hf) & (P - 1);
+      const int64_t at = ((int64_t)max(hf ? m.id[1] : m.id[0], 0) * a.c.H + h) * P * D +
+                         (int64_t)tok * D + 16 * ((int)threadIdx.x + kThreads * u - 2 * D * hf);
+      st.k[u] = *reinterpret_cast<const uint4*>(a.c.kc + at);
+      st.v[u] = *reinterpret_cast<const uint4*>(a.c.vc + at);
+    }
+  };
+  auto convert = [&](const Stage<D, kWaves>& st, int buf) {
+    half8* kl = reinterpret_cast<half8*>(smem_kv + buf * kBuf);  // [32 tokens][step][half][row]
+    half8* vl = kl + kStage * D / 8;                             // [32 tokens][d tile][step][half][d]
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int nn = threadIdx.x + kThreads * u;
+      {
+        const int tt = nn / D, c = nn % D / 64, g = nn % 64 / 16;
+        const int tk = 16 * (tt & 1) + (nn & 15);  // token inside its 32
+        const int m = (tk & 7) | (tk & 8) << 1 | (tk & 16) >> 1;
+        half8* at = kl + ((tt >> 1) * kSteps + 4 * c + g) * 64 + m;
+        at[0] = codes_f16x8(st.k[u].x, st.k[u].y);
+        at[32] = codes_f16x8(st.k[u].z, st.k[u].w);
+      }
+      {
+        const int hf = nn / (2 * D), c = nn % (2 * D) / 64, g = nn % 64 / 16;
+        half8* at = vl + (((hf * kTiles + c) * 2 + (g >> 1)) * 2 + (g & 1)) * 32 + (nn & 15);
+        at[0] = codes_f16x8(st.v[u].x, st.v[u].y);
+        at[16] = codes_f16x8(st.v[u].z, st.v[u].w);
+      }
+    }
+  };
+
+  Stage<D, kWaves> st;
+  Meta now, next;
+  if (t0 < t1) {
+    meta_of(t0, now);
+    load(t0, now, st);
+    convert(st, 0);
+    if (t0 + 1 < t1) {
+      meta_of(t0 + 1, next);
+      load(t0 + 1, next, st);
+    }
+    lds_barrier();
+  }
+  for (int t = t0; t < t1; ++t) {
+    const int buf = (t - t0) & 1;
+    Meta later = next;
+    if (t + 1 < t1) {
+      convert(st, buf ^ 1);
+      if (t + 2 < t1) {
+        meta_of(t + 2, later);
+        load(t + 2, later, st);
+      }
+    }
+    const int tok = t * kStage;
+    if (tok < w_hi && tok + kStage > w_lo) {
+      const half8* kl = reinterpret_cast<const half8*>(smem_kv + buf * kBuf) + lane;
+      const half8* vl = kl + kStage * D / 8;
+      f32x16 s[2] = {f32x16{}, f32x16{}};
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(u * kSteps + k) * 64], q[k], s[u], 0, 0, 0);
+      // lane (col, half), register e: row col, token 8 (e / 8) + 4 half + e % 4 + 16 (e / 4 % 2)
+      if (tok < w_lo_last || tok + kStage > w_hi_first || now.id[0] < 0 || now.id[1] < 0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int p = tok + 32 * u + 8 * (e >> 3) + 4 * half + (e & 3) + 16 * ((e >> 2) & 1);
+            if (p < my_lo || p >= my_hi || now.id[u] < 0) s[u][e] = -INFINITY;
+          }
+      }
+      float f[2], lam[2], inv[2], top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        f[u] = fmaxf(cq * now.sk[u], kTinyStep);
+        const float sv = fmaxf(now.sv[u], kTiny);
+        lam[u] = now.sv[u] > 0.f ? log2_fast(sv) : 0.f;
+        inv[u] = now.sv[u] > 0.f ? 1.f / sv : 1.f;
+        float m = s[u][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) m = fmaxf(m, s[u][e]);
+        top = fmaxf(top, fmaf(m, f[u], lam[u]));
+      }
+      if (__any(top > M + kTop)) {
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (top > M + kTop) {
+          const float m = top - kPlace;
+          const float al = exp2_fast(M - m);
+          L *= al;
+#pragma unroll
+          for (int d = 0; d < kTiles; ++d) o[d] *= al;
+          M = m;
+        }
+      }
+      half8 p[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float add = lam[u] - M;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float w = exp2_fast(fmaf(s[u][e], f[u], add));
+          sum += w;
+          p[u][e >> 3][e & 7] = (_Float16)w;
+        }
+        L += sum * inv[u];
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int d = 0; d < kTiles; ++d)
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[((u * kTiles + d) * 2 + k) * 64],
+                                                          p[u][k], o[d], 0, 0, 0);
+    }
+    now = next;
+    next = later;
+    lds_barrier();
+  }
+
+  L += __shfl_xor(L, 32);
+  if (w0 + col >= rows) return;
+  const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq;
+  const int64_t pr = (int64_t)sp * a.s.total * a.Hq + orow;
+  const float f = a.nsplit > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L;
+  // register e of tile d: dim 32 d + 8 (e / 4) + 4 half + e % 4
+#pragma unroll
+  for (int d = 0; d < kTiles; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float x[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = L == 0.f ? 0.f : o[d][e + c] * f;
+      const int dim = 32 * d + 2 * e + 4 * half;
+      if (a.nsplit > 1)
+        *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = make_float4(x[0], x[1], x[2], x[3]);
+      else
+        write4(a, orow * D + dim, x);
+    }
+  if (half == 0) {
+    if (a.nsplit > 1)
+      a.part_ml[pr] = make_float2(M, L);
+    else if (a.lse)
+      a.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M + log2_fast(L));
+  }
+}
+
 // ---- the join of a split call ----------------------------------------------
 // One wavefront a query row and head: the parts that have tiles, in order.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows_per_tile, int64_t most) {
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int64_t most) {
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // (b, i, head)
   const int per = a.s.max_count;
@@ -378,16 +678,9 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows_per_tile, 
   if (i >= n) return;
   const int len = clamped_len(a, b);
   // the row tile this row was in, as the split kernel saw it
-  const int64_t rows = (int64_t)n * a.G, r = (int64_t)i * a.G + hq % a.G;
-  const int64_t r0 = r / rows_per_tile * rows_per_tile;
-  const int i0 = (int)(r0 / a.G), i1 = (int)(min(r0 + rows_per_tile - 1, rows - 1) / a.G);
-  int lo, hi, x0, x1;
-  row_range(len, n, i0, a.causal, a.window, lo, x1);
-  row_range(len, n, i1, a.causal, a.window, x0, hi);
-  const int t_first = lo / kSpan, t_end = (hi + kSpan - 1) / kSpan;
-  const int tiles = max(t_end - t_first, 0);
-  const int span = max(a.span_tiles, (tiles + a.nsplit - 1) / a.nsplit);
-  const int parts = (tiles + span - 1) / span;
+  const int64_t r = (int64_t)i * a.G + hq % a.G;
+  const Parts pt = parts_of(a, len, n, r / a.tile_rows * a.tile_rows);
+  const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;
   const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq, step = (int64_t)a.s.total * a.Hq;
   float m = kNone;
   for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[p * step + orow].x);
@@ -411,10 +704,12 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows_per_tile, 
 
 // ---- host ------------------------------------------------------------------
 struct AttnPlan {
-  int rows_per_tile, row_tiles, nsplit, span_tiles;
+  bool prefill;
+  int tile_rows, tile_tokens, row_tiles, nsplit, span_tiles;
   int64_t blocks;     // workgroups of the attention launch
   size_t workspace, ml_at;
 };
+constexpr int kPrefillWaves = 4;
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -433,14 +728,22 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   int64_t longest = (int64_t)s.width << c.shift;
   if (t.max_kv_len > 0) longest = std::min(longest, t.max_kv_len);
   if (t.window > 0) longest = std::min<int64_t>(longest, (int64_t)t.window + s.max_count + kSpan);
-  const int64_t tiles = std::max<int64_t>(1, (longest + kSpan - 1) / kSpan);
-  p.rows_per_tile = 16;
-  p.row_tiles = (int)((s.max_count * G + p.rows_per_tile - 1) / p.rows_per_tile);
+  p.prefill = s.max_count * G > 2 * kRowTile;
+  p.tile_rows = p.prefill ? 32 * kPrefillWaves : kRowTile;
+  p.tile_tokens = p.prefill ? kStage : kSpan;
+  p.row_tiles = (int)((s.max_count * G + p.tile_rows - 1) / p.tile_rows);
   const int64_t items = (int64_t)s.batch * c.H * p.row_tiles;
-  // parts: about four workgroups a compute unit, each at least 8 tiles
-  const int64_t want = std::max<int64_t>(1, 1024 / items);
-  int64_t span = std::max<int64_t>(8, (tiles + want - 1) / want);
-  span = std::min<int64_t>(span, 64);
+  const int64_t tiles = std::max<int64_t>(1, (longest + p.tile_tokens - 1) / p.tile_tokens);
+  int64_t span;
+  if (p.prefill) {
+    // parts: two workgroups a compute unit, each at least 8 tiles
+    const int64_t want = std::max<int64_t>(1, 512 / items);
+    span = std::max<int64_t>(8, (tiles + want - 1) / want);
+  } else {
+    // parts: about four workgroups a compute unit, each 8 to 64 tiles
+    const int64_t want = std::max<int64_t>(1, 1024 / items);
+    span = std::min<int64_t>(std::max<int64_t>(8, (tiles + want - 1) / want), 64);
+  }
   p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, 256);
   p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
   p.blocks = items * p.nsplit;
@@ -457,12 +760,18 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
 
 template <int D>
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  const size_t lds = 4 * 16 * (D + 4) * 4 + 2 * 4 * 16 * 4;
-  hipLaunchKernelGGL((k_kv_decode<D>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
+  if (p.prefill) {
+    const size_t lds = 2 * 2 * kStage * D * 2;
+    hipLaunchKernelGGL((k_kv_prefill<D, kPrefillWaves>), dim3((unsigned)p.blocks),
+                       dim3(64 * kPrefillWaves), lds, stream, a);
+  } else {
+    const size_t lds = 4 * kRowTile * (D + 4) * 4 + 2 * 4 * kRowTile * 4;
+    hipLaunchKernelGGL((k_kv_decode<D>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
+  }
   if (p.nsplit > 1) {
     const int64_t most = (int64_t)a.s.batch * a.s.max_count * a.Hq;
     hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)((most + 3) / 4)), dim3(256), 0, stream, a,
-                       p.rows_per_tile, most);
+                       most);
   }
   return hipGetLastError();
 }
@@ -527,6 +836,8 @@ extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_s
   a.nsplit = p.nsplit;
   a.span_tiles = p.span_tiles;
   a.row_tiles = p.row_tiles;
+  a.tile_rows = p.tile_rows;
+  a.tile_tokens = p.tile_tokens;
   a.c2 = (t.scale > 0.f ? t.scale : 1.f / std::sqrt((float)D)) * kLog2e;
   hipError_t e;
   switch (D) {
