@@ -16,6 +16,7 @@ blocks with a bitwidth from {0,1,2,3,4,8} each, and every block row-group of
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -205,6 +206,7 @@ def plan(N: int, K: int, bits, perm_row, perm_col) -> dict:
                 mean_bits=out.mean_bits)
 
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -529,13 +531,11 @@ class KVCache:
         d.k_codes, d.v_codes = self.k_codes.data_ptr(), self.v_codes.data_ptr()
         d.k_scale, d.v_scale = self.k_scale.data_ptr(), self.v_scale.data_ptr()
         self._desc = d
+        self._index = self.k_codes.get_device()
+        self.device = self.k_codes.device
 
     def descriptor(self) -> _KvCache:
         return self._desc
-
-    @property
-    def device(self):
-        return self.k_codes.device
 
     @property
     def nbytes(self) -> int:
@@ -559,83 +559,82 @@ def allocate_kv_cache(num_blocks: int, kv_heads: int, head_dim: int, block_token
     return KVCache(num_blocks, kv_heads, head_dim, block_tokens, *codes, *scale)
 
 
+_KV_DTYPE: dict = {}
+
+
 def _kv_dtype(dtype) -> int:
-    torch = _torch()
-    if dtype == torch.bfloat16:
-        return 0
-    if dtype == torch.float32:
-        return 1
-    raise TypeError(f"expected bfloat16 or float32, got {dtype}")
+    code = _KV_DTYPE.get(dtype)
+    if code is None:
+        torch = _torch()
+        _KV_DTYPE.update({torch.bfloat16: 0, torch.float32: 1})
+        if dtype not in _KV_DTYPE:
+            raise TypeError(f"expected bfloat16 or float32, got {dtype}")
+        code = _KV_DTYPE[dtype]
+    return code
 
 
-def _kv_rows(t, name, heads, dim, device):
-    """t as [rows][heads][dim] the kernels can read: any token and head strides that are
-    multiples of 16 bytes with contiguous dims; anything else is copied."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+def _kv_rows(t, name, heads, dim, index):
+    """t as (tensor, address, token stride, head stride, type) of [rows][heads][dim] the kernels
+    can read: any token and head strides that are multiples of 16 bytes with contiguous dims;
+    anything else is copied."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [rows][{heads}][{dim}]")
-    if t.device != device:
-        raise ValueError(f"{name} must be on the cache's device {device}")
-    per16 = 8 if _kv_dtype(t.dtype) == 0 else 4
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's device")
+    code = _kv_dtype(t.dtype)
     st, sh, sd = t.stride()
-    if sd != 1 or st % per16 or sh % per16 or t.data_ptr() % 16:
+    at = t.data_ptr()
+    per16 = 4 if code else 8
+    if sd != 1 or st % per16 or sh % per16 or at % 16:
         t = t.clone(memory_format=_torch().contiguous_format)
-    return t
+        at, st, sh = t.data_ptr(), heads * dim, dim
+    return t, at, st, sh, code
 
 
-def _kv_index(t, name, shape, device):
-    torch = _torch()
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device:
-        raise ValueError(f"{name} must be int32 {list(shape)} on {device}")
+def _kv_index(t, name, shape, index):
+    if t.dtype != _torch().int32 or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be int32 {list(shape)} on the cache's device")
     return t if t.is_contiguous() else t.contiguous()
 
 
-class _OnStream:
-    """Allocations inside belong to the stream the launch goes to, on the cache's device.
-    Tensors handed to use() are marked as used on that stream when it is not the current one."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        cur = torch.cuda.current_stream(device)
-        self.stream = cur if stream is None else stream
-        self.other = self.stream.cuda_stream != cur.cuda_stream
-        self.guard = (torch.cuda.stream(self.stream)
-                      if self.other or torch.cuda.current_device() != device.index else None)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def use(self, *tensors):
-        if self.other:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-
-    @property
-    def handle(self) -> int:
-        return int(self.stream.cuda_stream)
-
-
 def _kv_seqs(cache: KVCache, block_table, offset, total: int, max_count: int):
-    batch = int(block_table.shape[0]) if block_table.dim() == 2 else -1
-    if batch < 0 or block_table.shape[1] < 1:
+    """(sequences struct, the tensors it points into)."""
+    shape = block_table.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("block_table must be int32 [batch][entries]")
-    block_table = _kv_index(block_table, "block_table", tuple(block_table.shape), cache.device)
+    batch, width = shape
+    block_table = _kv_index(block_table, "block_table", shape, cache._index)
     if offset is not None:
-        offset = _kv_index(offset, "offset", (batch + 1,), cache.device)
+        offset = _kv_index(offset, "offset", (batch + 1,), cache._index)
     elif total % max(batch, 1) or (batch == 0 and total):
         raise ValueError("without offset every sequence has the same number of rows")
-    s = _KvSeqs()
-    s.batch, s.table_width = batch, int(block_table.shape[1])
-    s.block_table = block_table.data_ptr()
-    s.offset = offset.data_ptr() if offset is not None else None
-    s.total, s.max_count = total, int(max_count)
-    return s, block_table, offset
+    return (_KvSeqs(batch, width, block_table.data_ptr(),
+                    None if offset is None else offset.data_ptr(), total, max_count),
+            (block_table, offset))
+
+
+def _kv_here(index: int, stream) -> bool:
+    """Whether a call can go to the current stream of the current device as it is."""
+    return stream is None and _torch().cuda.current_device() == index
+
+
+def _kv_on(cache: KVCache, stream, tensors, call):
+    """call() with the cache's device and the given stream current, so that what it allocates
+    belongs to that stream; the tensors it was given are marked as used there."""
+    torch = _torch()
+    with torch.cuda.device(cache._index):
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream) as _:
+            used = torch.cuda.current_stream()
+            result = call()
+    for t in (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, *tensors):
+        if t is not None and t.is_cuda:
+            t.record_stream(used)
+    return result
+
+
+def _kv_stream(index: int) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: int = 0,
@@ -647,20 +646,20 @@ def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: i
     which is the number of tokens it has in the cache (negative: leave the sequence out).
     offset: int32 [batch + 1], sequence b's rows are offset[b] .. offset[b + 1] - 1; None:
     rows / batch each.  max_count: the largest sequence's rows, if known (else all rows)."""
+    index = cache._index
+    if not _kv_here(index, stream):
+        return _kv_on(cache, stream, (k, v, block_table, first, offset),
+                      lambda: kv_write(cache, k, v, block_table, first, offset, max_count))
     lib = load_library()
-    dev = cache.device
-    with _OnStream(dev, stream) as on:
-        kd = _kv_rows(k, "k", cache.kv_heads, cache.head_dim, dev)
-        vd = _kv_rows(v, "v", cache.kv_heads, cache.head_dim, dev)
-        if kd.shape[0] != vd.shape[0] or kd.dtype != vd.dtype:
-            raise ValueError("k and v must have the same rows and type")
-        s, table, offset = _kv_seqs(cache, block_table, offset, int(kd.shape[0]), max_count)
-        first = _kv_index(first, "first", (s.batch,), dev)
-        on.use(kd, vd, table, first, offset, cache.k_codes, cache.v_codes, cache.k_scale,
-               cache.v_scale)
-        _check(lib.msq_kv_write(cache.descriptor(), s, first.data_ptr(), kd.data_ptr(),
-                                kd.stride(0), kd.stride(1), vd.data_ptr(), vd.stride(0),
-                                vd.stride(1), _kv_dtype(kd.dtype), on.handle), "msq_kv_write")
+    k, k_at, k_st, k_sh, code = _kv_rows(k, "k", cache.kv_heads, cache.head_dim, index)
+    v, v_at, v_st, v_sh, v_code = _kv_rows(v, "v", cache.kv_heads, cache.head_dim, index)
+    rows = k.shape[0]
+    if v.shape[0] != rows or v_code != code:
+        raise ValueError("k and v must have the same rows and type")
+    s, keep = _kv_seqs(cache, block_table, offset, rows, max_count)
+    first = _kv_index(first, "first", (s.batch,), index)
+    _check(lib.msq_kv_write(cache._desc, s, first.data_ptr(), k_at, k_st, k_sh, v_at, v_st, v_sh,
+                            code, _kv_stream(index)), "msq_kv_write")
 
 
 def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int] = None,
@@ -668,22 +667,22 @@ def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int
     """Read positions first[b] .. first[b] + rows - 1 of every sequence back (msq_kv_read):
     (k, v), [total][kv_heads][head_dim] of dtype (bf16 unless given; or fp32), code * scale.
     offset as in kv_write, total its last entry; with offset None, total / batch rows each."""
+    index = cache._index
+    if not _kv_here(index, stream):
+        return _kv_on(cache, stream, (block_table, first, offset),
+                      lambda: kv_read(cache, block_table, first, offset, total, max_count, dtype))
     torch = _torch()
     lib = load_library()
-    dev = cache.device
-    if total is None:
+    if total is None or total < 0:
         raise ValueError("total: the number of rows to read")
-    with _OnStream(dev, stream) as on:
-        s, table, offset = _kv_seqs(cache, block_table, offset, int(total), max_count)
-        first = _kv_index(first, "first", (s.batch,), dev)
-        shape = (s.total, cache.kv_heads, cache.head_dim)
-        dtype = torch.bfloat16 if dtype is None else dtype
-        code = _kv_dtype(dtype)
-        k = torch.empty(shape, dtype=dtype, device=dev)
-        v = torch.empty(shape, dtype=dtype, device=dev)
-        on.use(table, first, offset, cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale)
-        _check(lib.msq_kv_read(cache.descriptor(), s, first.data_ptr(), k.data_ptr(), v.data_ptr(),
-                               code, on.handle), "msq_kv_read")
+    s, keep = _kv_seqs(cache, block_table, offset, total, max_count)
+    first = _kv_index(first, "first", (s.batch,), index)
+    dtype = dtype or torch.bfloat16
+    code = _kv_dtype(dtype)
+    both = torch.empty((2, total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
+    k, v = both.unbind(0)
+    _check(lib.msq_kv_read(cache._desc, s, first.data_ptr(), k.data_ptr(), v.data_ptr(), code,
+                           _kv_stream(index)), "msq_kv_read")
     return k, v
 
 
@@ -692,12 +691,11 @@ def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch:
                                  window: int = 0) -> int:
     """Workspace of kv_attention for calls of these sizes (rows: query rows of all sequences)
     whose block tables have no more entries than max_kv_len tokens need."""
-    s, a = _KvSeqs(), _KvAttn()
-    s.batch, s.total, s.max_count = batch, rows, max_count
-    s.table_width = max(1, -(-max_kv_len // cache.block_tokens))
-    s.offset = 1  # only asked whether it is there
+    width = max(1, -(-max_kv_len // cache.block_tokens))
+    s = _KvSeqs(batch, width, None, 1, rows, max_count)  # of offset only whether it is there
+    a = _KvAttn()
     a.q_heads, a.max_kv_len, a.causal, a.window = q_heads, max_kv_len, int(causal), window
-    return int(load_library().msq_kv_attention_workspace_bytes(cache.descriptor(), s, a))
+    return int(load_library().msq_kv_attention_workspace_bytes(cache._desc, s, a))
 
 
 def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count: int = 0,
@@ -714,37 +712,36 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     unless out or out_dtype says fp32), with return_lse also the fp32 [rows][q_heads] natural
     log of each row's softmax denominator.  A query that sees nothing gives zeros and -inf.
     workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
+    index = cache._index
+    if not _kv_here(index, stream):
+        return _kv_on(cache, stream, (q, block_table, kv_len, offset, out, workspace),
+                      lambda: kv_attention(q, cache, block_table, kv_len, offset, max_count,
+                                           max_kv_len, scale, causal, window, out, out_dtype,
+                                           return_lse, workspace))
     torch = _torch()
     lib = load_library()
-    dev = cache.device
     if q.dim() != 3:
         raise ValueError("q must be [rows][q_heads][head_dim]")
-    with _OnStream(dev, stream) as on:
-        heads = int(q.shape[1])
-        qd = _kv_rows(q, "q", heads, cache.head_dim, dev)
-        rows = int(qd.shape[0])
-        s, table, offset = _kv_seqs(cache, block_table, offset, rows, max_count)
-        kv_len = _kv_index(kv_len, "kv_len", (s.batch,), dev)
-        if out is None:
-            out = torch.empty((rows, heads, cache.head_dim), dtype=out_dtype or torch.bfloat16,
-                              device=dev)
-        elif tuple(out.shape) != (rows, heads, cache.head_dim) or not out.is_contiguous() or \
-                out.device != dev or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError("out must be contiguous, [rows][q_heads][head_dim], on the cache's device")
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
-        a = _KvAttn()
-        a.q, a.q_token_stride, a.q_head_stride = qd.data_ptr(), qd.stride(0), qd.stride(1)
-        a.q_dtype, a.q_heads = _kv_dtype(qd.dtype), heads
-        a.kv_len, a.max_kv_len = kv_len.data_ptr(), int(max_kv_len)
-        a.scale, a.causal, a.window = float(scale), int(bool(causal)), int(window)
-        a.out, a.out_dtype = out.data_ptr(), _kv_dtype(out.dtype)
-        a.lse = lse.data_ptr() if lse is not None else None
-        if workspace is None:
-            need = int(lib.msq_kv_attention_workspace_bytes(cache.descriptor(), s, a))
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        on.use(qd, table, kv_len, offset, out, workspace, cache.k_codes, cache.v_codes,
-               cache.k_scale, cache.v_scale)
-        _check(lib.msq_kv_attention(cache.descriptor(), s, a, workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), on.handle),
-               "msq_kv_attention")
+    heads, dim = q.shape[1], cache.head_dim
+    q, q_at, q_st, q_sh, q_code = _kv_rows(q, "q", heads, dim, index)
+    rows = q.shape[0]
+    s, keep = _kv_seqs(cache, block_table, offset, rows, max_count)
+    kv_len = _kv_index(kv_len, "kv_len", (s.batch,), index)
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=out_dtype or torch.bfloat16, device=cache.device)
+    elif out.shape != (rows, heads, dim) or not out.is_contiguous() or out.get_device() != index or \
+            (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be contiguous, [rows][q_heads][head_dim], on the cache's device")
+    lse = torch.empty((rows, heads), dtype=torch.float32, device=cache.device) if return_lse else None
+    a = _KvAttn(q_at, q_st, q_sh, q_code, heads, kv_len.data_ptr(), max_kv_len, scale,
+                1 if causal else 0, window, out.data_ptr(), _kv_dtype(out.dtype),
+                None if lse is None else lse.data_ptr())
+    if workspace is None:
+        need = int(lib.msq_kv_attention_workspace_bytes(cache._desc, s, a))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the cache's device")
+    _check(lib.msq_kv_attention(cache._desc, s, a, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _kv_stream(index)),
+           "msq_kv_attention")
     return (out, lse) if return_lse else out

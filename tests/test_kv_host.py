@@ -142,15 +142,17 @@ def test_binding_refuses(lib):
     c = msq.allocate_kv_cache(4, 2, 64, 32, device="cpu")
     assert c.nbytes == 2 * 4 * 2 * 32 * 64 + 2 * 4 * 2 * 4
     x = torch.zeros(3, 2, 64)
-    dev = c.device
-    assert msq._kv_rows(x, "k", 2, 64, dev) is x
+    dev = -1
+    assert msq._kv_rows(x, "k", 2, 64, dev) == (x, x.data_ptr(), 128, 64, 1)
     for bad in (x[:, :1], x[..., :32], x[0]):
         with pytest.raises(ValueError):
             msq._kv_rows(bad, "k", 2, 64, dev)
     with pytest.raises(TypeError):
         msq._kv_rows(x.double(), "k", 2, 64, dev)
     t = torch.zeros(3, 2, 65)[..., 1:]
-    assert msq._kv_rows(t, "k", 2, 64, dev).is_contiguous()
+    assert msq._kv_rows(t, "k", 2, 64, dev)[0].is_contiguous()
+    with pytest.raises(ValueError):
+        msq._kv_rows(x, "k", 2, 64, 0)                          # another device
     table = torch.zeros(2, 3, dtype=torch.int32)
     with pytest.raises(ValueError):
         msq._kv_seqs(c, table[0], None, 2, 0)
@@ -160,6 +162,6 @@ def test_binding_refuses(lib):
         msq._kv_seqs(c, table.long(), None, 2, 0)
     with pytest.raises(ValueError):
         msq._kv_seqs(c, table, torch.zeros(2, dtype=torch.int32), 2, 0)
-    s, _, _ = msq._kv_seqs(c, table, None, 4, 0)
+    s, keep = msq._kv_seqs(c, table, None, 4, 0)
     assert (s.batch, s.table_width, s.total) == (2, 3, 4)
     assert ctypes.sizeof(msq._KvCache) == 56 and ctypes.sizeof(msq._KvSeqs) == 40
