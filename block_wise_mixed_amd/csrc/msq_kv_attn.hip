@@ -491,23 +491,43 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_prefill(At
   for (int d = 0; d < kTiles; ++d) o[d] = f32x16{};
   float M = kNone, L = 0.f;
 
-  // blocks, key and value scales of a tile's two halves of 32 tokens
+  // Blocks and scales of the tiles: lane j holds those of the j-th half (32
+  // tokens) of a batch of 32 tiles, read with vector loads one batch ahead (the
+  // blocks two ahead, since the scales need them).  Scalar loads would share
+  // their counter with the LDS reads, so that every tile waited for them.
   struct Meta {
     int id[2];
     float sk[2], sv[2];
   };
   const int P = 1 << a.c.shift;
-  auto meta_of = [&](int t, Meta& m) {
+  auto blocks_at = [&](int t) {  // of the batch that begins at tile t
+    return kv_block(a.c, a.s, b, ((int64_t)t * kStage + 32 * lane) >> a.c.shift);
+  };
+  auto scales_at = [&](int t, int id, float& sk, float& sv) {
+    // a half without tokens: its block may be absent or never written, whose
+    // scales may be anything
+    const bool none = id < 0 || (int64_t)t * kStage + 32 * lane >= len;
+    const int64_t hb = (int64_t)max(id, 0) * a.c.H + h;
+    sk = none ? 0.f : a.c.ks[hb];
+    sv = none ? 0.f : a.c.vs[hb];
+  };
+  int id0 = blocks_at(t0), id1 = blocks_at(t0 + 32), id2 = blocks_at(t0 + 64), batch = t0;
+  float sk0, sv0, sk1, sv1;
+  scales_at(t0, id0, sk0, sv0);
+  scales_at(t0 + 32, id1, sk1, sv1);
+  auto meta_of = [&](int t, Meta& m) {  // tiles in order
+    if (t - batch == 32) {
+      batch = t;
+      id0 = id1, sk0 = sk1, sv0 = sv1, id1 = id2;
+      scales_at(t + 32, id1, sk1, sv1);
+      id2 = blocks_at(t + 64);
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t tok = (int64_t)t * kStage + 32 * u;
-      m.id[u] = __builtin_amdgcn_readfirstlane(kv_block(a.c, a.s, b, tok >> a.c.shift));
-      // a half without tokens: its block may be absent or never written, whose
-      // scales may be anything
-      const bool none = m.id[u] < 0 || tok >= len;
-      const int64_t hb = (int64_t)max(m.id[u], 0) * a.c.H + h;
-      m.sk[u] = none ? 0.f : a.c.ks[hb];
-      m.sv[u] = none ? 0.f : a.c.vs[hb];
+      const int j = 2 * (t - batch) + u;
+      m.id[u] = __builtin_amdgcn_readlane(id0, j);
+      m.sk[u] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sk0), j));
+      m.sv[u] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sv0), j));
     }
   };
   auto load = [&](int t, const Meta& m, Stage<D, kWaves>& st) {
@@ -592,7 +612,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_prefill(At
         f[u] = fmaxf(cq * now.sk[u], kTinyStep);
         const float sv = fmaxf(now.sv[u], kTiny);
         lam[u] = now.sv[u] > 0.f ? log2_fast(sv) : 0.f;
-        inv[u] = now.sv[u] > 0.f ? 1.f / sv : 1.f;
+        inv[u] = now.sv[u] > 0.f ? __builtin_amdgcn_rcpf(sv) : 1.f;
         float m = s[u][0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) m = fmaxf(m, s[u][e]);
