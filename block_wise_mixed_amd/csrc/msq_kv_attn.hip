@@ -43,7 +43,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
 constexpr int kSpan = 32;          // tokens of a tile of k_kv_decode
 constexpr int kRowTile = 16;       // and its query rows
-constexpr int kStage = 64;         // tokens of a tile of k_kv_prefill
 constexpr float kTinyStep = 1e-37f;  // keeps -inf * step from being NaN where a step is 0
 
 struct AttnArgs {
@@ -407,24 +406,33 @@ __global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
 }
 
 // ---- many query rows -------------------------------------------------------
-// Workgroup: 32 kWaves query rows of one kv head and one part of their
-// tokens, 64 tokens at a time.  The workgroup turns each tile's codes into f16
-// once, in LDS, in operand order (two buffers; the next tile's codes are
-// loaded during the current one's products and converted before its barrier);
-// each wavefront holds 32 rows: S^T = K Q^T (32 x 32 x 16), softmax in
-// registers, O^T += V^T P^T with the score registers as operand.  Inside 32
+// Workgroup: wavefronts of 32 query rows of one kv head, over one part of their
+// tokens, a stage of 64 tokens at a time.  S^T = K Q^T (32 x 32 x 16), softmax in
+// registers, O^T += V^T P^T with the score registers as operand: inside 32
 // tokens the key rows are placed so that those registers hold the weights in
-// the order of the value codes: token t is row t with bits 3 and 4 swapped.
-template <int D, int kWaves>
-struct Stage {
-  uint4 k[D * kStage / 16 / (64 * kWaves)], v[D * kStage / 16 / (64 * kWaves)];
+// the order of the value codes (token t is row t with bits 3 and 4 swapped).
+//
+// The workgroup turns each stage's codes into f16 once, in LDS, in operand
+// order, from registers loaded a stage before.  Half a stage (32 tokens, a
+// strip) at a time, a wavefront multiplies the values of strip i - 1 and the
+// keys of strip i + 1 while it turns the scores of strip i into weights: the
+// three do not depend on each other, so its vector instructions run between its
+// matrix instructions.  LDS holds four strips of keys and four of values, in
+// turn; one barrier a stage.
+template <int D>
+struct Prefill {
+  static constexpr int kStage = 64;  // tokens: two strips
+  static constexpr int kSteps = D / 16, kTiles = D / 32;
+  static constexpr int kWaves = D == 128 ? 8 : 4;
+  static constexpr int kThreads = 64 * kWaves, kRows = 32 * kWaves;
+  static constexpr int kUnits = 8 * D / kThreads;  // 16-byte pieces of keys and values a thread
+  static constexpr int kStrip = 4 * D;             // 16-byte pieces of a strip in LDS
 };
 
-template <int D, int kWaves>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
-  constexpr int kThreads = 64 * kWaves, kSteps = D / 16, kTiles = D / 32;
-  constexpr int kUnits = D * kStage / 16 / kThreads;  // 16-byte pieces of K (and of V) a thread
-  constexpr int kBuf = 2 * kStage * D * 2;            // bytes of one K and V buffer
+template <int D>
+__global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
+  using C = Prefill<D>;
+  constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
   int64_t wg = blockIdx.x;
   const int h = (int)(wg % a.c.H);
   wg /= a.c.H;
@@ -437,7 +445,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_prefill(At
   int row0, n;
   kv_rows(a.s, b, row0, n);
   const int64_t rows = (int64_t)n * a.G;
-  const int64_t r0 = (int64_t)tile_row * (32 * kWaves);
+  const int64_t r0 = (int64_t)tile_row * C::kRows;
   if (r0 >= rows) return;
   const int len = clamped_len(a, b);
   const Parts pt = parts_of(a, len, n, r0);
@@ -454,6 +462,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_prefill(At
   row_range(len, n, (int)(min(w0, rows - 1) / a.G), a.causal, a.window, w_lo, w_hi_first);
   row_range(len, n, (int)(min(w0 + 31, rows - 1) / a.G), a.causal, a.window, w_lo_last, w_hi);
   if (w0 >= rows) w_hi = 0;
+  // its stages: a0 .. a1 - 1 (none: a0 == a1)
+  const int a0 = min(max(t0, w_lo / kStage), t1);
+  const int a1 = max(a0, min(t1, (int)(((int64_t)w_hi + kStage - 1) / kStage)));
 
   half8 q[kSteps];  // slots (half, e) of step s are dims 16 s + 8 half + e
   float cq;
@@ -491,169 +502,191 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void k_kv_prefill(At
   for (int d = 0; d < kTiles; ++d) o[d] = f32x16{};
   float M = kNone, L = 0.f;
 
-  // Blocks and scales of the tiles: lane j holds those of the j-th half (32
-  // tokens) of a batch of 32 tiles, read with vector loads one batch ahead (the
-  // blocks two ahead, since the scales need them).  Scalar loads would share
-  // their counter with the LDS reads, so that every tile waited for them.
-  struct Meta {
-    int id[2];
-    float sk[2], sv[2];
-  };
+  // Blocks and scales of the strips: lane j holds those of the j-th strip of a
+  // batch of 64, read with vector loads one batch ahead (the blocks two ahead,
+  // since the scales need them).  Scalar loads would share their counter with
+  // the LDS reads, so that every stage waited for them.
   const int P = 1 << a.c.shift;
-  auto blocks_at = [&](int t) {  // of the batch that begins at tile t
+  struct Scales {
+    float sk, lam, inv;  // keys' scale; values': log2 and inverse
+  };
+  auto blocks_at = [&](int t) {  // of the batch that begins at stage t
     return kv_block(a.c, a.s, b, ((int64_t)t * kStage + 32 * lane) >> a.c.shift);
   };
-  auto scales_at = [&](int t, int id, float& sk, float& sv) {
-    // a half without tokens: its block may be absent or never written, whose
+  auto scales_at = [&](int t, int id) {
+    // a strip past the end: its block may be absent or never written, whose
     // scales may be anything
     const bool none = id < 0 || (int64_t)t * kStage + 32 * lane >= len;
     const int64_t hb = (int64_t)max(id, 0) * a.c.H + h;
-    sk = none ? 0.f : a.c.ks[hb];
-    sv = none ? 0.f : a.c.vs[hb];
+    Scales s;
+    s.sk = none ? 0.f : a.c.ks[hb];
+    const float sv = none ? 0.f : a.c.vs[hb];
+    // a block of zeros takes no part in placing M: any scale stands for it
+    const float one = sv > 0.f ? fmaxf(sv, kTiny) : 1.f;
+    s.lam = log2_fast(one);
+    s.inv = __builtin_amdgcn_rcpf(one);
+    return s;
   };
-  int id0 = blocks_at(t0), id1 = blocks_at(t0 + 32), id2 = blocks_at(t0 + 64), batch = t0;
-  float sk0, sv0, sk1, sv1;
-  scales_at(t0, id0, sk0, sv0);
-  scales_at(t0 + 32, id1, sk1, sv1);
-  auto meta_of = [&](int t, Meta& m) {  // tiles in order
-    if (t - batch == 32) {
-      batch = t;
-      id0 = id1, sk0 = sk1, sv0 = sv1, id1 = id2;
-      scales_at(t + 32, id1, sk1, sv1);
-      id2 = blocks_at(t + 64);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int j = 2 * (t - batch) + u;
-      m.id[u] = __builtin_amdgcn_readlane(id0, j);
-      m.sk[u] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sk0), j));
-      m.sv[u] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sv0), j));
-    }
+  int batch = 2 * t0;  // its first strip
+  int id0 = blocks_at(t0), id1 = blocks_at(t0 + 32), id2 = blocks_at(t0 + 64);
+  Scales sc0 = scales_at(t0, id0), sc1 = scales_at(t0 + 32, id1);
+  auto id_of = [&](int i) {  // a strip of this batch, the next one, or just before
+    const int j = i - batch;
+    return __builtin_amdgcn_readlane(j < 64 ? id0 : id1, j & 63);
   };
-  auto load = [&](int t, const Meta& m, Stage<D, kWaves>& st) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int hf = __builtin_amdgcn_readfirstlane((64 * wave + kThreads * u) / (2 * D));
-      const int tok = (t * kStage + 32 * hf) & (P - 1);
-      const int64_t at = ((int64_t)max(hf ? m.id[1] : m.id[0], 0) * a.c.H + h) * P * D +
-                         (int64_t)tok * D + 16 * ((int)threadIdx.x + kThreads * u - 2 * D * hf);
-      st.k[u] = *reinterpret_cast<const uint4*>(a.c.kc + at);
-      st.v[u] = *reinterpret_cast<const uint4*>(a.c.vc + at);
-    }
-  };
-  auto convert = [&](const Stage<D, kWaves>& st, int buf) {
-    half8* kl = reinterpret_cast<half8*>(smem_kv + buf * kBuf);  // [32 tokens][step][half][row]
-    half8* vl = kl + kStage * D / 8;                             // [32 tokens][d tile][step][half][d]
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int nn = threadIdx.x + kThreads * u;
-      {
-        const int tt = nn / D, c = nn % D / 64, g = nn % 64 / 16;
-        const int tk = 16 * (tt & 1) + (nn & 15);  // token inside its 32
-        const int m = (tk & 7) | (tk & 8) << 1 | (tk & 16) >> 1;
-        half8* at = kl + ((tt >> 1) * kSteps + 4 * c + g) * 64 + m;
-        at[0] = codes_f16x8(st.k[u].x, st.k[u].y);
-        at[32] = codes_f16x8(st.k[u].z, st.k[u].w);
-      }
-      {
-        const int hf = nn / (2 * D), c = nn % (2 * D) / 64, g = nn % 64 / 16;
-        half8* at = vl + (((hf * kTiles + c) * 2 + (g >> 1)) * 2 + (g & 1)) * 32 + (nn & 15);
-        at[0] = codes_f16x8(st.v[u].x, st.v[u].y);
-        at[16] = codes_f16x8(st.v[u].z, st.v[u].w);
-      }
-    }
+  auto lane_of = [&](float x, int i) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i - batch));
   };
 
-  Stage<D, kWaves> st;
-  Meta now, next;
+  // this thread's pieces of the keys of strips ik, ik + 1 and of the values of
+  // strips iv, iv + 1, into registers
+  const int64_t block_bytes = (int64_t)a.c.H * P * D;
+  const uint8_t* const kc = a.c.kc + (int64_t)h * P * D;
+  const uint8_t* const vc = a.c.vc + (int64_t)h * P * D;
+  uint4 st[C::kUnits];
+  auto load = [&](int ik, int iv) {
+#pragma unroll
+    for (int u = 0; u < C::kUnits; ++u) {
+      const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
+      const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
+      const int64_t blk = max(id_of(i), 0) * block_bytes;
+      const uint32_t at = (uint32_t)(((32 * i) & (P - 1)) * D + 16 * (n & (2 * D - 1)));
+      st[u] = *reinterpret_cast<const uint4*>((kind ? vc : kc) + blk + at);
+    }
+  };
+  // and from there as f16 into LDS: keys [strip][step][half][row], values
+  // [strip][d tile][step][half][d], 16 bytes each
+  half8* const lds = reinterpret_cast<half8*>(smem_kv);
+  auto convert = [&](int ik, int iv) {
+#pragma unroll
+    for (int u = 0; u < C::kUnits; ++u) {
+      const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
+      const int m = n & (2 * D - 1), g = m % 64 / 16;
+      const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
+      half8* p = lds + (4 * kind + (i & 3)) * C::kStrip;
+      const half8 lo = codes_f16x8(st[u].x, st[u].y), hi = codes_f16x8(st[u].z, st[u].w);
+      if (kind == 0) {
+        const int tok = 16 * (m / D) + (m & 15);
+        p += (4 * (m % D / 64) + g) * 64 + ((tok & 7) | (tok & 8) << 1 | (tok & 16) >> 1);
+        p[0] = lo;
+        p[32] = hi;
+      } else {
+        p += (4 * (m / 64) + g) * 32 + (m & 15);
+        p[0] = lo;
+        p[16] = hi;
+      }
+    }
+  };
+  auto scores = [&](int i, f32x16& s) {
+    const half8* kl = lds + (i & 3) * C::kStrip + lane;
+    s = f32x16{};
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[k * 64], q[k], s, 0, 0, 0);
+  };
+  auto values = [&](int i, const half8 (&p)[2]) {
+    const half8* vl = lds + (4 + (i & 3)) * C::kStrip + lane;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int d = 0; d < kTiles; ++d)
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[(2 * d + k) * 64], p[k], o[d], 0, 0, 0);
+  };
+  auto largest = [](const f32x16& s) {
+    float m = s[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) m = fmaxf(m, s[e]);
+    return m;
+  };
+
+  // Strip i: its scores s, whose largest is top, -> weights p; scores sn of
+  // strip i + 1 and their largest; values of strip i - 1 by their weights pp.
+  // Lane (col, half), register e: row col, token 8 (e / 8) + 4 half + e % 4 +
+  // 16 (e / 4 % 2).
+  auto strip = [&](int i, f32x16& s, f32x16& sn, float& top, half8 (&p)[2], half8 (&pp)[2],
+                   auto&& between) {
+    const int tok = 32 * i;
+    const bool gone = __builtin_amdgcn_readlane(id0, i - batch) < 0;
+    const float f = fmaxf(cq * lane_of(sc0.sk, i), kTinyStep);
+    const float lam = lane_of(sc0.lam, i), inv = lane_of(sc0.inv, i);
+    if (tok < w_lo_last || tok + 32 > w_hi_first || gone) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int at = tok + 8 * (e >> 3) + 4 * half + (e & 3) + 16 * ((e >> 2) & 1);
+        if (at < my_lo || at >= my_hi || gone) s[e] = -INFINITY;
+      }
+      top = largest(s);
+    }
+    float most = fmaf(top, f, lam);
+    if (__any(most > M + kTop)) {
+      most = fmaxf(most, __shfl_xor(most, 32));
+      // a power of two, so that the last strip's weights move exactly
+      const float m = most > M + kTop ? ceilf(most - kPlace) : M;
+      const float al = exp2_fast(M - m);
+      L *= al;
+#pragma unroll
+      for (int d = 0; d < kTiles; ++d) o[d] *= al;
+      pp[0] *= (_Float16)al;
+      pp[1] *= (_Float16)al;
+      M = m;
+    }
+    between();
+    scores(i + 1, sn);
+    values(i - 1, pp);
+    const float add = lam - M;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float w = exp2_fast(fmaf(s[e], f, add));
+      sum += w;
+      p[e >> 3][e & 7] = (_Float16)w;
+    }
+    L = fmaf(sum, inv, L);
+    top = largest(sn);
+    // the weights are made here, between the products, not where they are used
+    asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(L));
+  };
+
   if (t0 < t1) {
-    meta_of(t0, now);
-    load(t0, now, st);
-    convert(st, 0);
-    if (t0 + 1 < t1) {
-      meta_of(t0 + 1, next);
-      load(t0 + 1, next, st);
-    }
+    f32x16 sa, sb;
+    half8 pa[2], pb[2];
+    pa[0] = pa[1] = pb[0] = pb[1] = half8{};
+    // the first three strips of keys and the first of values; the strip of
+    // values before that is multiplied by weights of 0, so it gets finite numbers
+    load(2 * t0 - 1, 2 * t0 - 1);
+    convert(2 * t0 - 1, 2 * t0 - 1);
+    load(2 * t0 + 1, 2 * t0 + 1);
+    convert(2 * t0 + 1, 2 * t0 + 1);
+    load(2 * t0 + 3, 2 * t0 + 1);
     lds_barrier();
-  }
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) & 1;
-    Meta later = next;
-    if (t + 1 < t1) {
-      convert(st, buf ^ 1);
-      if (t + 2 < t1) {
-        meta_of(t + 2, later);
-        load(t + 2, later, st);
+    scores(2 * t0, sa);
+    float top = largest(sa);
+    auto next_batch = [&](int t) {
+      if (2 * t - batch == 64) {
+        batch = 2 * t;
+        id0 = id1, sc0 = sc1, id1 = id2;
+        sc1 = scales_at(t + 32, id1);
+        id2 = blocks_at(t + 64);
       }
+    };
+    auto convert_only = [&](int t) {
+      next_batch(t);
+      convert(2 * t + 3, 2 * t + 1);
+      load(2 * t + 5, 2 * t + 3);
+      lds_barrier();
+    };
+    // outside its own stages a wavefront only converts; the stage before them
+    // and the one after are worked through as masked ones
+    int t = t0;
+    for (; t < a0 - 1; ++t) convert_only(t);
+    for (const int end = min(a1 + 1, t1); t < end; ++t) {
+      next_batch(t);
+      strip(2 * t, sa, sb, top, pa, pb, [&] { convert(2 * t + 3, 2 * t + 1); });
+      strip(2 * t + 1, sb, sa, top, pb, pa, [&] { load(2 * t + 5, 2 * t + 3); });
+      lds_barrier();
     }
-    const int tok = t * kStage;
-    if (tok < w_hi && tok + kStage > w_lo) {
-      const half8* kl = reinterpret_cast<const half8*>(smem_kv + buf * kBuf) + lane;
-      const half8* vl = kl + kStage * D / 8;
-      f32x16 s[2] = {f32x16{}, f32x16{}};
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[(u * kSteps + k) * 64], q[k], s[u], 0, 0, 0);
-      // lane (col, half), register e: row col, token 8 (e / 8) + 4 half + e % 4 + 16 (e / 4 % 2)
-      if (tok < w_lo_last || tok + kStage > w_hi_first || now.id[0] < 0 || now.id[1] < 0) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int p = tok + 32 * u + 8 * (e >> 3) + 4 * half + (e & 3) + 16 * ((e >> 2) & 1);
-            if (p < my_lo || p >= my_hi || now.id[u] < 0) s[u][e] = -INFINITY;
-          }
-      }
-      float f[2], lam[2], inv[2], top = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        f[u] = fmaxf(cq * now.sk[u], kTinyStep);
-        const float sv = fmaxf(now.sv[u], kTiny);
-        lam[u] = now.sv[u] > 0.f ? log2_fast(sv) : 0.f;
-        inv[u] = now.sv[u] > 0.f ? __builtin_amdgcn_rcpf(sv) : 1.f;
-        float m = s[u][0];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) m = fmaxf(m, s[u][e]);
-        top = fmaxf(top, fmaf(m, f[u], lam[u]));
-      }
-      if (__any(top > M + kTop)) {
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (top > M + kTop) {
-          const float m = top - kPlace;
-          const float al = exp2_fast(M - m);
-          L *= al;
-#pragma unroll
-          for (int d = 0; d < kTiles; ++d) o[d] *= al;
-          M = m;
-        }
-      }
-      half8 p[2][2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float add = lam[u] - M;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float w = exp2_fast(fmaf(s[u][e], f[u], add));
-          sum += w;
-          p[u][e >> 3][e & 7] = (_Float16)w;
-        }
-        L += sum * inv[u];
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int d = 0; d < kTiles; ++d)
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[((u * kTiles + d) * 2 + k) * 64],
-                                                          p[u][k], o[d], 0, 0, 0);
-    }
-    now = next;
-    next = later;
-    lds_barrier();
+    if (a1 >= t1) values(2 * t1 - 1, pb);
+    for (; t < t1; ++t) convert_only(t);
   }
 
   L += __shfl_xor(L, 32);
@@ -729,7 +762,6 @@ struct AttnPlan {
   int64_t blocks;     // workgroups of the attention launch
   size_t workspace, ml_at;
 };
-constexpr int kPrefillWaves = 4;
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -749,15 +781,18 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   if (t.max_kv_len > 0) longest = std::min(longest, t.max_kv_len);
   if (t.window > 0) longest = std::min<int64_t>(longest, (int64_t)t.window + s.max_count + kSpan);
   p.prefill = s.max_count * G > 2 * kRowTile;
-  p.tile_rows = p.prefill ? 32 * kPrefillWaves : kRowTile;
-  p.tile_tokens = p.prefill ? kStage : kSpan;
+  p.tile_rows = !p.prefill ? kRowTile
+                : D == 64  ? Prefill<64>::kRows
+                : D == 128 ? Prefill<128>::kRows
+                           : Prefill<256>::kRows;
+  p.tile_tokens = p.prefill ? Prefill<128>::kStage : kSpan;
   p.row_tiles = (int)((s.max_count * G + p.tile_rows - 1) / p.tile_rows);
   const int64_t items = (int64_t)s.batch * c.H * p.row_tiles;
   const int64_t tiles = std::max<int64_t>(1, (longest + p.tile_tokens - 1) / p.tile_tokens);
   int64_t span;
   if (p.prefill) {
-    // parts: two workgroups a compute unit, each at least 8 tiles
-    const int64_t want = std::max<int64_t>(1, 512 / items);
+    // parts: one workgroup a compute unit, each at least 8 stages
+    const int64_t want = std::max<int64_t>(1, 256 / items);
     span = std::max<int64_t>(8, (tiles + want - 1) / want);
   } else {
     // parts: about four workgroups a compute unit, each 8 to 64 tiles
@@ -781,9 +816,8 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
 template <int D>
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if (p.prefill) {
-    const size_t lds = 2 * 2 * kStage * D * 2;
-    hipLaunchKernelGGL((k_kv_prefill<D, kPrefillWaves>), dim3((unsigned)p.blocks),
-                       dim3(64 * kPrefillWaves), lds, stream, a);
+    hipLaunchKernelGGL((k_kv_prefill<D>), dim3((unsigned)p.blocks),
+                       dim3(Prefill<D>::kThreads), 8 * 16 * Prefill<D>::kStrip, stream, a);
   } else {
     const size_t lds = 4 * kRowTile * (D + 4) * 4 + 2 * 4 * kRowTile * 4;
     hipLaunchKernelGGL((k_kv_decode<D>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
