@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "msq.h"
 #include "msq_kv.h"
@@ -427,12 +428,15 @@ struct Prefill {
   static constexpr int kThreads = 64 * kWaves, kRows = 32 * kWaves;
   static constexpr int kUnits = 8 * D / kThreads;  // 16-byte pieces of keys and values a thread
   static constexpr int kStrip = 4 * D;             // 16-byte pieces of a strip in LDS
+  static constexpr int kProducts = kSteps + 2 * kTiles;  // of a strip: keys, then values
+  static constexpr int kAhead = 4;                 // operands read from LDS before their product
 };
 
 template <int D>
 __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
   using C = Prefill<D>;
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
+  constexpr int kProducts = C::kProducts, kAhead = C::kAhead;
   int64_t wg = blockIdx.x;
   const int h = (int)(wg % a.c.H);
   wg /= a.c.H;
@@ -544,53 +548,49 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
   const uint8_t* const kc = a.c.kc + (int64_t)h * P * D;
   const uint8_t* const vc = a.c.vc + (int64_t)h * P * D;
   uint4 st[C::kUnits];
+  auto load_one = [&](int ik, int iv, int u) {
+    const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
+    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
+    const int64_t blk = max(id_of(i), 0) * block_bytes;
+    const uint32_t at = (uint32_t)(((32 * i) & (P - 1)) * D + 16 * (n & (2 * D - 1)));
+    st[u] = *reinterpret_cast<const uint4*>((kind ? vc : kc) + blk + at);
+  };
   auto load = [&](int ik, int iv) {
 #pragma unroll
-    for (int u = 0; u < C::kUnits; ++u) {
-      const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
-      const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
-      const int64_t blk = max(id_of(i), 0) * block_bytes;
-      const uint32_t at = (uint32_t)(((32 * i) & (P - 1)) * D + 16 * (n & (2 * D - 1)));
-      st[u] = *reinterpret_cast<const uint4*>((kind ? vc : kc) + blk + at);
-    }
+    for (int u = 0; u < C::kUnits; ++u) load_one(ik, iv, u);
   };
   // and from there as f16 into LDS: keys [strip][step][half][row], values
   // [strip][d tile][step][half][d], 16 bytes each
   half8* const lds = reinterpret_cast<half8*>(smem_kv);
+  auto convert_half = [&](int ik, int iv, int u, int second) {
+    const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
+    const int m = n & (2 * D - 1), g = m % 64 / 16;
+    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
+    const int tok = 16 * (m / D) + (m & 15);
+    half8* p = lds + (4 * kind + (i & 3)) * C::kStrip +
+               (kind ? (4 * (m / 64) + g) * 32 + (m & 15)
+                     : (4 * (m % D / 64) + g) * 64 + ((tok & 7) | (tok & 8) << 1 | (tok & 16) >> 1));
+    p[second * (kind ? 16 : 32)] =
+        second ? codes_f16x8(st[u].z, st[u].w) : codes_f16x8(st[u].x, st[u].y);
+  };
   auto convert = [&](int ik, int iv) {
 #pragma unroll
-    for (int u = 0; u < C::kUnits; ++u) {
-      const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
-      const int m = n & (2 * D - 1), g = m % 64 / 16;
-      const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
-      half8* p = lds + (4 * kind + (i & 3)) * C::kStrip;
-      const half8 lo = codes_f16x8(st[u].x, st[u].y), hi = codes_f16x8(st[u].z, st[u].w);
-      if (kind == 0) {
-        const int tok = 16 * (m / D) + (m & 15);
-        p += (4 * (m % D / 64) + g) * 64 + ((tok & 7) | (tok & 8) << 1 | (tok & 16) >> 1);
-        p[0] = lo;
-        p[32] = hi;
-      } else {
-        p += (4 * (m / 64) + g) * 32 + (m & 15);
-        p[0] = lo;
-        p[16] = hi;
-      }
-    }
+    for (int j = 0; j < 2 * C::kUnits; ++j) convert_half(ik, iv, j >> 1, j & 1);
   };
-  auto scores = [&](int i, f32x16& s) {
-    const half8* kl = lds + (i & 3) * C::kStrip + lane;
-    s = f32x16{};
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl[k * 64], q[k], s, 0, 0, 0);
+  // operand m of strip i's products: the keys of strip i + 1, then the values
+  // of strip i - 1
+  auto operand = [&](int i, int m) {
+    const half8* kl = lds + ((i + 1) & 3) * C::kStrip + lane;
+    const half8* vl = lds + (4 + ((i - 1) & 3)) * C::kStrip + lane;
+    const int v = m - kSteps;
+    return m < kSteps ? kl[m * 64] : vl[(2 * (v % kTiles) + v / kTiles) * 64];
   };
+  half8 fr[kAhead];
   auto values = [&](int i, const half8 (&p)[2]) {
-    const half8* vl = lds + (4 + (i & 3)) * C::kStrip + lane;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int d = 0; d < kTiles; ++d)
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vl[(2 * d + k) * 64], p[k], o[d], 0, 0, 0);
+    for (int v = 0; v < 2 * kTiles; ++v)
+      o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          operand(i + 1, kSteps + v), p[v / kTiles], o[v % kTiles], 0, 0, 0);
   };
   auto largest = [](const f32x16& s) {
     float m = s[0];
@@ -604,7 +604,8 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
   // Lane (col, half), register e: row col, token 8 (e / 8) + 4 half + e % 4 +
   // 16 (e / 4 % 2).
   auto strip = [&](int i, f32x16& s, f32x16& sn, float& top, half8 (&p)[2], half8 (&pp)[2],
-                   auto&& between) {
+                   auto second) {
+    constexpr bool kSecond = decltype(second)::value;  // of its stage
     const int tok = 32 * i;
     const bool gone = __builtin_amdgcn_readlane(id0, i - batch) < 0;
     const float f = fmaxf(cq * lane_of(sc0.sk, i), kTinyStep);
@@ -630,21 +631,66 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
       pp[1] *= (_Float16)al;
       M = m;
     }
-    between();
-    scores(i + 1, sn);
-    values(i - 1, pp);
     const float add = lam - M;
-    float sum = 0.f;
+    float w[16], sum = 0.f;
+    half2v pairs[8];
+    sn = f32x16{};
+    // (the empty asm statements keep each result at its place in this order)
+    auto use = [&](int e) {
+      sum += w[e];
+      asm volatile("" : "+v"(sum));
+      if (e & 1) {
+        pairs[e >> 1] = half2v{(_Float16)w[e - 1], (_Float16)w[e]};
+        asm volatile("" : "+v"(pairs[e >> 1]));
+      }
+    };
+    // A product, the read of a later one's operand, and a share of the vector
+    // work at a time, in this order: the scheduler left to itself reads operands
+    // right before their products and gathers the vector work at the end.
+    constexpr int kMax = D == 64 ? 2 : 4;  // the last products, beside the search of sn
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float w = exp2_fast(fmaf(s[e], f, add));
-      sum += w;
-      p[e >> 3][e & 7] = (_Float16)w;
+    for (int m = 0; m < kProducts; ++m) {
+      const int v = m - kSteps;
+      if (m < kSteps)
+        sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], q[m], sn, 0, 0, 0);
+      else
+        o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], pp[v / kTiles],
+                                                               o[v % kTiles], 0, 0, 0);
+      if (m + kAhead < kProducts)
+        fr[m % kAhead] = operand(i, m + kAhead);
+      else if (!kSecond)
+        fr[m % kAhead] = operand(i + 1, m + kAhead - kProducts);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (e * kProducts / 16 != m) continue;
+        w[e] = exp2_fast(fmaf(s[e], f, add));
+        if (e >= 2) use(e - 2);
+      }
+      if constexpr (!kSecond) {
+#pragma unroll
+        for (int j = 0; j < 2 * C::kUnits; ++j)
+          if (j * kProducts / (2 * C::kUnits) == m) convert_half(i + 3, i + 1, j >> 1, j & 1);
+      } else {
+#pragma unroll
+        for (int u = 0; u < C::kUnits; ++u)
+          if (u * kProducts / C::kUnits == m) load_one(i + 4, i + 2, u);
+      }
+      if (m >= kProducts - kMax) {
+#pragma unroll
+        for (int e = 0; e < 16 / kMax; ++e) {
+          const float x = sn[16 / kMax * (m - kProducts + kMax) + e];
+          top = m == kProducts - kMax && e == 0 ? x : fmaxf(top, x);
+        }
+        asm volatile("" : "+v"(top));
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    use(14);
+    use(15);
     L = fmaf(sum, inv, L);
-    top = largest(sn);
-    // the weights are made here, between the products, not where they are used
-    asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(L));
+    asm volatile("" : "+v"(L));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) p[e >> 3][e & 7] = pairs[e >> 1][e & 1];
   };
 
   if (t0 < t1) {
@@ -659,7 +705,10 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
     convert(2 * t0 + 1, 2 * t0 + 1);
     load(2 * t0 + 3, 2 * t0 + 1);
     lds_barrier();
-    scores(2 * t0, sa);
+    sa = f32x16{};
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+      sa = __builtin_amdgcn_mfma_f32_32x32x16_f16(operand(2 * t0 - 1, k), q[k], sa, 0, 0, 0);
     float top = largest(sa);
     auto next_batch = [&](int t) {
       if (2 * t - batch == 64) {
@@ -681,8 +730,10 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
     for (; t < a0 - 1; ++t) convert_only(t);
     for (const int end = min(a1 + 1, t1); t < end; ++t) {
       next_batch(t);
-      strip(2 * t, sa, sb, top, pa, pb, [&] { convert(2 * t + 3, 2 * t + 1); });
-      strip(2 * t + 1, sb, sa, top, pb, pa, [&] { load(2 * t + 5, 2 * t + 3); });
+#pragma unroll
+      for (int m = 0; m < kAhead; ++m) fr[m] = operand(2 * t, m);
+      strip(2 * t, sa, sb, top, pa, pb, std::false_type{});
+      strip(2 * t + 1, sb, sa, top, pb, pa, std::true_type{});
       lds_barrier();
     }
     if (a1 >= t1) values(2 * t1 - 1, pb);
