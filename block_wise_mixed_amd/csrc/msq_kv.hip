@@ -5,10 +5,12 @@
 // Both kernels give one workgroup to (sequence, block its rows reach, keys or
 // values, head): it owns everything the call changes in that block and head,
 // so a scale that grows and the earlier codes it moves need no second launch
-// and no atomics.  A wavefront takes 32 slots.  Keys: a lane holds 16 dims of
-// a token, which are 16 contiguous code bytes.  Values: a lane holds 8 tokens
-// x (4 + 4) dims, which are 64 contiguous code bytes (the value order puts 8
-// tokens of a dim together, so the transposition happens in registers).
+// and no atomics.  A wavefront takes 32 slots.  On the tensors' side a lane
+// holds 8 dims of a token (whole rows per instruction).  In the keys' order
+// these are 8 contiguous code bytes; the values' order puts 8 tokens of a dim
+// together, so values pass through LDS and 4 x 4 byte transpositions in
+// registers: a lane there holds 8 tokens x (4 + 4) dims, 64 contiguous code
+// bytes.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -21,31 +23,37 @@ namespace {
 
 constexpr float kFinite = 3.402823466e38f;
 
-__device__ inline float bf16_f32(uint32_t bits) { return __uint_as_float(bits << 16); }
-
-// Four consecutive values as loaded: 8 bytes of bf16, 16 of fp32.
+// Eight consecutive values as loaded.
 template <typename T>
-struct Raw4;
+struct Raw8;
 template <>
-struct Raw4<uint16_t> {
-  uint2 v;
-  __device__ float get(int i) const {
-    const uint32_t w = i < 2 ? v.x : v.y;
-    return i & 1 ? __uint_as_float(w & 0xFFFF0000u) : bf16_f32(w & 0xFFFFu);
+struct Raw8<uint16_t> {
+  uint4 v;
+  __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+  // forget the widened values: they are made again, in half the registers
+  __device__ void narrow() { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+  __device__ void get(float* x) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
   }
 };
 template <>
-struct Raw4<float> {
-  float4 v;
-  __device__ float get(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+struct Raw8<float> {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ void narrow() {}
+  __device__ void get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
 };
-
-template <typename T>
-__device__ inline Raw4<T> load4(const T* p) {
-  Raw4<T> r;
-  r.v = *reinterpret_cast<const decltype(r.v)*>(p);
-  return r;
-}
 
 __device__ inline float finite_abs(float x) {
   const float a = fabsf(x);
@@ -64,6 +72,57 @@ __device__ inline uint32_t kv_code(float x, float s) {
 __device__ inline uint32_t kv_recode(uint32_t u, float old, float s) {
   const float v = (float)((int)u - 128) * old;
   return kv_code(v, s);
+}
+
+// Codes of eight values.  inv > 0: a reciprocal of s (v_rcp_f32, 1 ulp) that
+// may stand in for the division: t = x * inv and fl(x / s) are within 127 *
+// (1.5 * 2^-23 + 2^-24) < 2^-15 of each other, so they round to the same code
+// unless t is within 2^-14 of a half-integer; then, and for a NaN, the lane
+// divides.  The rounding is an addition of 1.5 * 2^23, which leaves code + 128
+// in the low byte.
+__device__ inline uint2 kv_codes8(const float* x, float s, float inv) {
+  constexpr float kMagic = 12582912.f + 128.f;
+  uint32_t m[8], w[2];
+  float off = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = fminf(fmaxf(x[i] * inv, -127.f), 127.f);
+    const float r = t + kMagic;
+    off = fmaxf(off, fabsf(t - (r - kMagic)));
+    nan |= x[i] != x[i];
+    m[i] = __float_as_uint(r);
+  }
+  if (!(inv > 0.f) || nan || off > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = kv_code(x[i], s);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __builtin_amdgcn_perm(m[4 * i + 1], m[4 * i], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(m[4 * i + 3], m[4 * i + 2], 0x04000C0Cu);
+    w[i] = lo | hi;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ inline uint32_t kv_recode4(uint32_t w, float old, float s) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) r |= kv_recode((w >> (8 * n)) & 255u, old, s) << (8 * n);
+  return r;
+}
+
+// 4 x 4 bytes: byte j of out[i] is byte i of in[j].
+__device__ inline void transpose4(const uint32_t* in, uint32_t* out) {
+  const uint32_t ab0 = __builtin_amdgcn_perm(in[1], in[0], 0x05010400u);
+  const uint32_t ab1 = __builtin_amdgcn_perm(in[1], in[0], 0x07030602u);
+  const uint32_t cd0 = __builtin_amdgcn_perm(in[3], in[2], 0x05010400u);
+  const uint32_t cd1 = __builtin_amdgcn_perm(in[3], in[2], 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302u);
 }
 
 __device__ inline float wave_max(float v) {
@@ -87,20 +146,30 @@ __device__ inline Task task_of(int64_t id, int H, int reach) {
   return t;
 }
 
-// Value-order pieces of a wavefront's 32 slots x D dims: lane -> token group
-// g, first dim; kUnits of them per lane (the upper half of the lanes has none
-// at D = 64).
+// Pieces of a wavefront's 32 slots x D dims.
 template <int D>
-struct ValueMap {
-  static constexpr int kPerG = D / 8;               // (dim chunk, quad) pairs: D/32 * 4
-  static constexpr int kLanes = kPerG < 16 ? kPerG : 16;
-  static constexpr int kUnits = kPerG / kLanes;
+struct Map {
+  // rows: a lane holds dims 8 * part .. of slots row(lane, u), u < kRows
+  static constexpr int kParts = D / 8, kRows = D / 16;
+  __device__ static int part(int lane) { return lane % kParts; }
+  __device__ static int row(int lane, int u) { return lane / kParts + 64 / kParts * u; }
+  // byte of that piece in the keys' order, from the first of the 32 slots
+  __device__ static int key_byte(int slot, int part) {
+    return 16 * D * (slot >> 4) + 1024 * (part >> 3) +
+           16 * ((slot & 15) + 16 * ((part >> 1) & 3)) + 8 * (part & 1);
+  }
+  // values' order: a lane holds 8 tokens (group g) x dims 4 q .. and 16 + 4 q
+  // .. of chunk c, cq = 4 c + q; kUnits of them (half the lanes idle at D = 64)
+  static constexpr int kLanes = D / 8 < 16 ? D / 8 : 16, kUnits = D / 8 / kLanes;
   __device__ static bool active(int lane) { return lane < 4 * kLanes; }
   __device__ static int g(int lane) { return lane / kLanes; }
-  // index of unit u: 4 * chunk + quad
   __device__ static int cq(int lane, int u) { return lane % kLanes + kLanes * u; }
+  // LDS image of the codes, [slot][dim]
+  static constexpr int kStride = D + 8, kImage = 32 * kStride;
 };
 __device__ inline int value_slot(int g, int j) { return j < 4 ? 4 * g + j : 12 + 4 * g + j; }
+
+extern __shared__ __align__(16) unsigned char smem_codes[];
 
 struct WriteArgs {
   KvCacheView c;
@@ -116,7 +185,8 @@ struct WriteArgs {
 // coding); a call of single tokens is a chain of four dependent loads.
 template <int D, typename T>
 __global__ __launch_bounds__(512) void k_kv_write(WriteArgs a) {
-  __shared__ float part[8];
+  using Mp = Map<D>;
+  __shared__ float part_max[8];
   const Task tk = task_of(blockIdx.x, a.c.H, a.reach);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -136,125 +206,105 @@ __global__ __launch_bounds__(512) void k_kv_write(WriteArgs a) {
   const int64_t row = (int64_t)row0 + base - f;  // row of slot 0
   const int64_t hb = (int64_t)id * a.c.H + tk.h;
   float* scale = (tk.values ? a.c.vs : a.c.ks) + hb;
-  uint8_t* codes = (tk.values ? a.c.vc : a.c.kc) + hb * P * D;
+  const int s0 = 32 * wave;
+  uint8_t* codes = (tk.values ? a.c.vc : a.c.kc) + (hb * P + s0) * D;
   const T* src = reinterpret_cast<const T*>(tk.values ? a.v : a.k) +
                  tk.h * (tk.values ? a.vhs : a.khs);
   const int64_t ts = tk.values ? a.vts : a.kts;
   const float old = lo > 0 ? *scale : 0.f;
 
-  const int s0 = 32 * wave;
-  constexpr int kKeyUnits = 2 * (D / 64);
-  using VM = ValueMap<D>;
-  constexpr int kRaw = kKeyUnits * 4 > VM::kUnits * 16 ? kKeyUnits * 4 : VM::kUnits * 16;
-  Raw4<T> raw[kRaw];
+  const int part = Mp::part(lane);
+  Raw8<T> raw[Mp::kRows];
+#pragma unroll
+  for (int u = 0; u < Mp::kRows; ++u) {
+    const int slot = s0 + Mp::row(lane, u);
+    if (slot >= lo && slot < hi) raw[u].load(src + (row + slot) * ts + 8 * part);
+  }
   float amax = 0.f;
-  if (!tk.values) {
 #pragma unroll
-    for (int u = 0; u < kKeyUnits; ++u) {
-      const int slot = s0 + 16 * (u & 1) + (lane & 15);
-      if (slot >= lo && slot < hi) {
-        const T* p = src + (row + slot) * ts + 64 * (u >> 1) + 16 * (lane >> 4);
+  for (int u = 0; u < Mp::kRows; ++u) {
+    const int slot = s0 + Mp::row(lane, u);
+    if (slot >= lo && slot < hi) {
+      float x[8];
+      raw[u].get(x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) raw[4 * u + i] = load4(p + 4 * i);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(raw[4 * u + i / 4].get(i & 3)));
-      }
-    }
-  } else if (VM::active(lane)) {
-#pragma unroll
-    for (int u = 0; u < VM::kUnits; ++u) {
-      const int cq = VM::cq(lane, u), d = 32 * (cq >> 2) + 4 * (cq & 3);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int slot = s0 + value_slot(VM::g(lane), j);
-        if (slot >= lo && slot < hi) {
-          const T* p = src + (row + slot) * ts + d;
-          raw[16 * u + 2 * j] = load4(p);
-          raw[16 * u + 2 * j + 1] = load4(p + 16);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            amax = fmaxf(amax, finite_abs(raw[16 * u + 2 * j + i / 4].get(i & 3)));
-        }
-      }
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[i]));
+      raw[u].narrow();
     }
   }
   amax = wave_max(amax);
   if (waves > 1) {
-    if (lane == 0) part[wave] = amax;
+    if (lane == 0) part_max[wave] = amax;
     __syncthreads();
-    for (int w = 0; w < waves; ++w) amax = fmaxf(amax, part[w]);
+    for (int w = 0; w < waves; ++w) amax = fmaxf(amax, part_max[w]);
   }
   float s = amax / 127.0f;
   const bool grown = lo > 0 && s > old;
   if (lo > 0 && !grown) s = old;
   if (threadIdx.x == 0 && (lo == 0 || grown)) *scale = s;
+  const float inv = s > 1e-30f && s < 1e30f ? __builtin_amdgcn_rcpf(s) : 0.f;
 
-  if (!tk.values) {
+  uint8_t* image = smem_codes + wave * Mp::kImage;
 #pragma unroll
-    for (int u = 0; u < kKeyUnits; ++u) {
-      const int slot = s0 + 16 * (u & 1) + (lane & 15);
-      uint4* at = reinterpret_cast<uint4*>(codes + 16 * D * (slot >> 4) + 1024 * (u >> 1)) + lane;
-      if (slot >= lo && slot < hi) {
-        uint32_t w[4];
+  for (int u = 0; u < Mp::kRows; ++u) {
+    const int in = Mp::row(lane, u), slot = s0 + in;
+    uint2* at = reinterpret_cast<uint2*>(codes + Mp::key_byte(in, part));
+    if (slot >= lo && slot < hi) {
+      float x[8];
+      raw[u].get(x);
+      const uint2 q = kv_codes8(x, s, inv);
+      if (tk.values)
+        *reinterpret_cast<uint2*>(image + in * Mp::kStride + 8 * part) = q;
+      else
+        *at = q;
+    } else if (grown && slot < lo && !tk.values) {
+      const uint2 q = *at;
+      *at = make_uint2(kv_recode4(q.x, old, s), kv_recode4(q.y, old, s));
+    }
+  }
+  if (!tk.values || !Mp::active(lane)) return;
+  __builtin_amdgcn_wave_barrier();  // the image is this wavefront's own
+
+  const int g = Mp::g(lane);
+  uint32_t fresh[2] = {0, 0}, keep[2] = {0, 0};  // bytes of new and of moved earlier codes
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int slot = s0 + value_slot(g, j);
+    if (slot >= lo && slot < hi) fresh[j >> 2] |= 255u << (8 * (j & 3));
+    if (grown && slot < lo) keep[j >> 2] |= 255u << (8 * (j & 3));
+  }
+  if (!(fresh[0] | fresh[1] | keep[0] | keep[1])) return;
+  const bool all = (fresh[0] & fresh[1]) == 0xFFFFFFFFu;
+#pragma unroll
+  for (int u = 0; u < Mp::kUnits; ++u) {
+    const int cq = Mp::cq(lane, u);
+    const uint8_t* from = image + 32 * (cq >> 2) + 4 * (cq & 3);
+    uint32_t w[4][4];  // [dim][word]: word i holds dims d + 16 (i / 2), tokens 4 (i % 2) ..
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t in[4], out[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        in[n] = *reinterpret_cast<const uint32_t*>(
+            from + value_slot(g, 4 * (i & 1) + n) * Mp::kStride + 16 * (i >> 1));
+      transpose4(in, out);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) w[d][i] = out[d];
+    }
+    uint4* at = reinterpret_cast<uint4*>(codes + 1024 * (cq >> 2)) + 4 * (cq & 3) + 16 * g;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      if (!all) {
+        const uint4 q = at[d];
+        const uint32_t was[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          w[i] = 0;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) w[i] |= kv_code(raw[4 * u + i].get(n), s) << (8 * n);
+          uint32_t r = (w[d][i] & fresh[i & 1]) | (was[i] & ~fresh[i & 1]);
+          if (keep[i & 1]) r = (r & ~keep[i & 1]) | (kv_recode4(was[i], old, s) & keep[i & 1]);
+          w[d][i] = r;
         }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
-      } else if (grown && slot < lo) {
-        const uint4 q = *at;
-        uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t r = 0;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) r |= kv_recode((w[i] >> (8 * n)) & 255u, old, s) << (8 * n);
-          w[i] = r;
-        }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    }
-  } else if (VM::active(lane)) {
-    const int g = VM::g(lane);
-    bool any = false, all = true;  // of this lane's 8 slots: some change, all are new
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int slot = s0 + value_slot(g, j);
-      const bool isnew = slot >= lo && slot < hi;
-      any |= isnew || (grown && slot < lo);
-      all &= isnew;
-    }
-    if (!any) return;
-#pragma unroll
-    for (int u = 0; u < VM::kUnits; ++u) {
-      const int cq = VM::cq(lane, u);
-      uint4* at = reinterpret_cast<uint4*>(codes + 32 * D * wave + 1024 * (cq >> 2)) +
-                  4 * (cq & 3) + 16 * g;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (!all) q = at[d];
-        uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // word i: dims d + 16 * (i / 2), slots 4 * (i % 2) ..
-          uint32_t r = 0;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const int j = 4 * (i & 1) + n;
-            const int slot = s0 + value_slot(g, j);
-            uint32_t code = (w[i] >> (8 * n)) & 255u;
-            if (slot >= lo && slot < hi)
-              code = kv_code(raw[16 * u + 2 * j + (i >> 1)].get(d), s);
-            else if (grown && slot < lo)
-              code = kv_recode(code, old, s);
-            r |= code << (8 * n);
-          }
-          w[i] = r;
-        }
-        at[d] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      at[d] = make_uint4(w[d][0], w[d][1], w[d][2], w[d][3]);
     }
   }
 }
@@ -267,26 +317,24 @@ struct ReadArgs {
   int reach;
 };
 
-__device__ inline void store4(uint16_t* p, const float* x) {
+__device__ inline void store8(uint16_t* p, const float* x) {
   union {
-    __bf16 b[4];
-    uint2 u;
+    __bf16 b[8];
+    uint4 u;
   } o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o.b[i] = (__bf16)x[i];
-  *reinterpret_cast<uint2*>(p) = o.u;
+  for (int i = 0; i < 8; ++i) o.b[i] = (__bf16)x[i];
+  *reinterpret_cast<uint4*>(p) = o.u;
 }
-__device__ inline void store4(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-
-__device__ inline float kv_value(uint32_t w, int n, float s) {
-  return (float)((int)((w >> (8 * n)) & 255u) - 128) * s;
+__device__ inline void store8(float* p, const float* x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
 // HBM bound: codes in, values out, once each.
 template <int D, typename T>
 __global__ __launch_bounds__(512) void k_kv_read(ReadArgs a) {
+  using Mp = Map<D>;
   const Task tk = task_of(blockIdx.x, a.c.H, a.reach);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -301,60 +349,60 @@ __global__ __launch_bounds__(512) void k_kv_read(ReadArgs a) {
   const int id = kv_block(a.c, a.s, tk.b, e);
   const int lo = (int)max(f - base, (int64_t)0);
   const int hi = (int)min(f + count - base, (int64_t)P);
+  const int s0 = 32 * wave;
+  if (s0 >= hi || s0 + 32 <= lo) return;
   const int64_t row = (int64_t)row0 + base - f;
   const int64_t hb = (int64_t)max(id, 0) * a.c.H + tk.h;
   const float s = id < 0 ? 0.f : (tk.values ? a.c.vs : a.c.ks)[hb];
-  const uint8_t* codes = (tk.values ? a.c.vc : a.c.kc) + hb * P * D;
+  const uint8_t* codes = (tk.values ? a.c.vc : a.c.kc) + (hb * P + s0) * D;
   T* dst = reinterpret_cast<T*>(tk.values ? a.v : a.k) + (int64_t)tk.h * D;
   const int64_t ts = (int64_t)a.c.H * D;
-  const int s0 = 32 * wave;
-  using VM = ValueMap<D>;
+  const int part = Mp::part(lane);
+  uint8_t* image = smem_codes + wave * Mp::kImage;
+  uint2 q[Mp::kRows];
   if (!tk.values) {
 #pragma unroll
-    for (int u = 0; u < 2 * (D / 64); ++u) {
-      const int slot = s0 + 16 * (u & 1) + (lane & 15);
-      if (slot < lo || slot >= hi) continue;
-      const uint4 q =
-          *(reinterpret_cast<const uint4*>(codes + 16 * D * (slot >> 4) + 1024 * (u >> 1)) + lane);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      T* p = dst + (row + slot) * ts + 64 * (u >> 1) + 16 * (lane >> 4);
+    for (int u = 0; u < Mp::kRows; ++u)
+      q[u] = *reinterpret_cast<const uint2*>(codes + Mp::key_byte(Mp::row(lane, u), part));
+  } else {
+    if (Mp::active(lane)) {
+      const int g = Mp::g(lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x[4];
+      for (int u = 0; u < Mp::kUnits; ++u) {
+        const int cq = Mp::cq(lane, u);
+        const uint4* at = reinterpret_cast<const uint4*>(codes + 1024 * (cq >> 2)) + 4 * (cq & 3) + 16 * g;
+        uint8_t* to = image + 32 * (cq >> 2) + 4 * (cq & 3);
+        uint32_t w[4][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) x[n] = id < 0 ? 0.f : kv_value(w[i], n, s);
-        store4(p + 4 * i, x);
-      }
-    }
-  } else if (VM::active(lane)) {
-    const int g = VM::g(lane);
+        for (int d = 0; d < 4; ++d) {
+          const uint4 v = at[d];
+          w[0][d] = v.x, w[1][d] = v.y, w[2][d] = v.z, w[3][d] = v.w;
+        }
 #pragma unroll
-    for (int u = 0; u < VM::kUnits; ++u) {
-      const int cq = VM::cq(lane, u);
-      const uint4* at =
-          reinterpret_cast<const uint4*>(codes + 32 * D * wave + 1024 * (cq >> 2)) +
-          4 * (cq & 3) + 16 * g;
-      uint32_t w[4][4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t out[4];
+          transpose4(w[i], out);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const uint4 q = at[d];
-        w[d][0] = q.x, w[d][1] = q.y, w[d][2] = q.z, w[d][3] = q.w;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int slot = s0 + value_slot(g, j);
-        if (slot < lo || slot >= hi) continue;
-        T* p = dst + (row + slot) * ts + 32 * (cq >> 2) + 4 * (cq & 3);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float x[4];
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            x[d] = id < 0 ? 0.f : kv_value(w[d][2 * half + (j >> 2)], j & 3, s);
-          store4(p + 16 * half, x);
+          for (int n = 0; n < 4; ++n)
+            *reinterpret_cast<uint32_t*>(to + value_slot(g, 4 * (i & 1) + n) * Mp::kStride +
+                                         16 * (i >> 1)) = out[n];
         }
       }
     }
+    __builtin_amdgcn_wave_barrier();  // the image is this wavefront's own
+#pragma unroll
+    for (int u = 0; u < Mp::kRows; ++u)
+      q[u] = *reinterpret_cast<const uint2*>(image + Mp::row(lane, u) * Mp::kStride + 8 * part);
+  }
+#pragma unroll
+  for (int u = 0; u < Mp::kRows; ++u) {
+    const int slot = s0 + Mp::row(lane, u);
+    if (slot < lo || slot >= hi) continue;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = id < 0 ? 0.f : (float)((int)(((i < 4 ? q[u].x : q[u].y) >> (8 * (i & 3))) & 255u) - 128) * s;
+    store8(dst + (row + slot) * ts + 8 * part, x);
   }
 }
 
@@ -379,13 +427,13 @@ hipError_t dispatch(int D, int dtype, dim3 grid, dim3 block, hipStream_t stream,
 template <int D, typename T>
 struct LaunchWrite {
   static void go(dim3 grid, dim3 block, hipStream_t stream, const WriteArgs& a) {
-    hipLaunchKernelGGL((k_kv_write<D, T>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((k_kv_write<D, T>), grid, block, block.x / 64 * Map<D>::kImage, stream, a);
   }
 };
 template <int D, typename T>
 struct LaunchRead {
   static void go(dim3 grid, dim3 block, hipStream_t stream, const ReadArgs& a) {
-    hipLaunchKernelGGL((k_kv_read<D, T>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((k_kv_read<D, T>), grid, block, block.x / 64 * Map<D>::kImage, stream, a);
   }
 };
 
