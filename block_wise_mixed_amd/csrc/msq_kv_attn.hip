@@ -19,8 +19,11 @@
 // the code.  A query row is scaled by the power of two that puts its largest
 // value in [2^14, 2^15), so bf16 queries are exact down to 2^-21 of it.
 #include <hip/hip_runtime.h>
+#include <unistd.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -28,6 +31,9 @@
 #include "msq.h"
 #include "msq_kv.h"
 
+#ifndef KV_T
+#define KV_T 32
+#endif
 namespace msq {
 namespace {
 
@@ -44,6 +50,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
 constexpr int kSpan = 32;          // tokens of a tile of k_kv_decode
 constexpr int kRowTile = 16;       // and its query rows
+constexpr int kMostParts = 64;     // parts of a row tile's tokens
 constexpr float kTinyStep = 1e-37f;  // keeps -inf * step from being NaN where a step is 0
 
 struct AttnArgs {
@@ -56,6 +63,8 @@ struct AttnArgs {
   float* lse;
   float* part_o;   // [nsplit][total * Hq][D], null for one split
   float2* part_ml; // [nsplit][total * Hq]: M, L
+  uint64_t* tags;  // [item][kMostParts]: which parts of this call are there; null: a join launch
+  uint64_t call;
   int Hq, G, q_f32, out_f32, causal, window;
   int nsplit;      // workgroups along a row tile's tokens
   int span_tiles;  // tiles of one such part (more where nsplit parts cannot cover the range)
@@ -152,6 +161,17 @@ __device__ inline void write4(const AttnArgs& a, int64_t at, const float* x) {
   }
 }
 
+// Two floats at a time past the caches that the XCDs do not share.
+__device__ inline void put2(uint64_t* p, float x, float y, bool on) {
+  if (on)
+    __hip_atomic_store(p, (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline float2 get2(const uint64_t* p) {
+  const uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+
 // The tiles of a part: query rows r0 .. of a sequence with n * G rows see the
 // tokens lo .. hi - 1 between them, cut into tiles of tile_tokens and those
 // into parts of the same number of tiles.
@@ -213,7 +233,7 @@ __device__ inline void load_tile(Tile<D>& t, const KvCacheView& c, int id, int h
 }
 
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
   constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
   constexpr int kStride = D + 4;
   int64_t wg = blockIdx.x;
@@ -275,88 +295,90 @@ __global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
   for (int d = 0; d < kTiles; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
   float M = kNone, L = 0.f;
 
-  const int shift = a.c.shift - 5;  // tiles per block, as a shift
-  auto block_of = [&](int t) {
-    return __builtin_amdgcn_readfirstlane(kv_block(a.c, a.s, b, t >> shift));
+  // Lane j holds the block and the scales of this wavefront's j-th tile (of a
+  // batch of 64), so that a tile's loads wait for no chain of their own.
+  int id = 0;
+  float sk = 0.f, lam = 0.f, inv = 1.f;
+  auto batch_at = [&](int t) {
+    const int64_t mine = (int64_t)t + kWaves * lane;
+    id = mine < t1 ? kv_block(a.c, a.s, b, mine >> (a.c.shift - 5)) : -1;
+    const int64_t hb = (int64_t)max(id, 0) * a.c.H + h;
+    sk = a.c.ks[hb];
+    const float sv = a.c.vs[hb];
+    // a block of zeros takes no part in placing M: any scale stands for it
+    const float one = sv > 0.f ? fmaxf(sv, kTiny) : 1.f;
+    lam = log2_fast(one);
+    inv = __builtin_amdgcn_rcpf(one);
   };
-  Tile<D> cur, nxt;
-  int t = t0 + wave, id = -1, id_n = -1;
-  if (t < t1) {
-    id = block_of(t);
-    load_tile<D>(cur, a.c, id, h, t, lane);
-  }
-  if (t + kWaves < t1) id_n = block_of(t + kWaves);
-  for (; t < t1; t += kWaves) {
-    const bool more = t + kWaves < t1;
-    if (more) load_tile<D>(nxt, a.c, id_n, h, t + kWaves, lane);
-    const int id_nn = t + 2 * kWaves < t1 ? block_of(t + 2 * kWaves) : -1;
-    if (id >= 0) {
-      const int64_t hb = (int64_t)id * a.c.H + h;
-      const float sk = a.c.ks[hb], sv = a.c.vs[hb];
-      f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+  auto work = [&](const Tile<D>& tl, int t, int j) {
+    if (__builtin_amdgcn_readlane(id, j) < 0) return;  // an absent block
+    f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint4 k0 = cur.k[c], k1 = cur.k[D / 64 + c];
-        s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.x, k0.y), q[2 * c], s0, 0, 0, 0);
-        s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.x, k1.y), q[2 * c], s1, 0, 0, 0);
-        s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.z, k0.w), q[2 * c + 1], s0, 0, 0, 0);
-        s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.z, k1.w), q[2 * c + 1], s1, 0, 0, 0);
-      }
-      // lane (col, g): scores of row col at tokens 4g + 0..3 and 16 + 4g + 0..3
-      const float f = cq * sk;
-      float x[8];
+    for (int c = 0; c < D / 64; ++c) {
+      const uint4 k0 = tl.k[c], k1 = tl.k[D / 64 + c];
+      s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.x, k0.y), q[2 * c], s0, 0, 0, 0);
+      s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.x, k1.y), q[2 * c], s1, 0, 0, 0);
+      s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.z, k0.w), q[2 * c + 1], s0, 0, 0, 0);
+      s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.z, k1.w), q[2 * c + 1], s1, 0, 0, 0);
+    }
+    // lane (col, g): scores of row col at tokens 4g + 0..3 and 16 + 4g + 0..3
+    const float f = fmaxf(cq * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sk), j)), kTinyStep);
+    const float lm = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lam), j));
+    const float in = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(inv), j));
+    const int tok = t * kSpan;
+    if (tok < lo1 || tok + kSpan > hi0) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[e] = s0[e] * f;
-        x[4 + e] = s1[e] * f;
-      }
-      const int tok = t * kSpan;
-      if (tok < lo1 || tok + kSpan > hi0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int p = tok + 4 * g + (e & 3) + 16 * (e >> 2);
-          if (p < my_lo || p >= my_hi) x[e] = -INFINITY;
-        }
-      }
-      // a block of zeros takes no part in placing M: any scale stands for it
-      const float s = fmaxf(sv, kTiny);
-      const float lam = sv > 0.f ? log2_fast(s) : 0.f;
-      const float inv = sv > 0.f ? 1.f / s : 1.f;
-      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      if (__any(top + lam > M + kTop)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (top + lam > M + kTop) {
-          const float m = top + lam - kPlace;
-          const float al = exp2_fast(M - m);
-          L *= al;
-#pragma unroll
-          for (int d = 0; d < kTiles; ++d) o[d] *= al;
-          M = m;
-        }
-      }
-      const float add = lam - M;
-      float sum = 0.f;
-      half8 p;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float w = exp2_fast(x[e] + add);
-        sum += w;
-        p[e] = (_Float16)w;
-      }
-      L += sum * inv;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint4 v = cur.v[c];
-        o[2 * c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.x, v.y), p, o[2 * c], 0, 0, 0);
-        o[2 * c + 1] =
-            __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.z, v.w), p, o[2 * c + 1], 0, 0, 0);
+        const int p = tok + 4 * g + e;
+        if (p < my_lo || p >= my_hi) s0[e] = -INFINITY;
+        if (p + 16 < my_lo || p + 16 >= my_hi) s1[e] = -INFINITY;
       }
     }
-    cur = nxt;
-    id = id_n;
-    id_n = id_nn;
+    float top = fmaf(fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
+                           fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]))), f, lm);
+    if (__any(top > M + kTop)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m = top > M + kTop ? top - kPlace : M;
+      const float al = exp2_fast(M - m);
+      L *= al;
+#pragma unroll
+      for (int d = 0; d < kTiles; ++d) o[d] *= al;
+      M = m;
+    }
+    const float add = lm - M;
+    float sum = 0.f;
+    half8 p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float w = exp2_fast(fmaf(e < 4 ? s0[e & 3] : s1[e & 3], f, add));
+      sum += w;
+      p[e] = (_Float16)w;
+    }
+    L = fmaf(sum, in, L);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const uint4 v = tl.v[c];
+      o[2 * c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.x, v.y), p, o[2 * c], 0, 0, 0);
+      o[2 * c + 1] =
+          __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.z, v.w), p, o[2 * c + 1], 0, 0, 0);
+    }
+  };
+  for (int tb = t0 + wave; tb < t1; tb += 64 * kWaves) {
+    batch_at(tb);
+    const int tiles = min(64, (t1 - tb + kWaves - 1) / kWaves);
+    Tile<D> ta, tc;
+    auto fetch = [&](Tile<D>& tl, int j) {
+      load_tile<D>(tl, a.c, __builtin_amdgcn_readlane(id, j), h, tb + kWaves * j, lane);
+    };
+    fetch(ta, 0);
+    for (int j = 0; j < tiles; j += 2) {
+      if (j + 1 < tiles) fetch(tc, j + 1);
+      work(ta, tb + kWaves * j, j);
+      if (j + 1 >= tiles) break;
+      if (j + 2 < tiles) fetch(ta, j + 2);
+      work(tc, tb + kWaves * (j + 1), j + 1);
+    }
   }
 
   // join the wavefronts: M and L per row, then the weighted sum of O
@@ -373,9 +395,8 @@ __global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
     lo_l[wave * 16 + col] = L;
   }
   __syncthreads();
-  constexpr int kPer = D / 16;  // outputs per thread: 16 threads a row
-  const int rr = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * kPer;
-  if (r0 + rr >= rows) return;
+  constexpr int kPer = D / 4 / kWaves;  // outputs per thread, 4 kWaves threads a row
+  const int rr = threadIdx.x / (4 * kWaves), d0 = threadIdx.x % (4 * kWaves) * kPer;
   float m = kNone;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) m = fmaxf(m, lo_m[w * 16 + rr]);
@@ -389,16 +410,81 @@ __global__ __launch_bounds__(256) void k_kv_decode(AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[e] += f * lo_o[(w * 16 + rr) * kStride + d0 + e];
   }
-  const int64_t ro = r0 + rr;
+  const int64_t ro = min(r0 + rr, rows - 1);
   const int io = (int)(ro / a.G);
   const int64_t orow = (int64_t)(row0 + io) * a.Hq + h * a.G + (int)(ro - (int64_t)io * a.G);
+  const int64_t step = (int64_t)a.s.total * a.Hq;
+  const bool mine = r0 + rr < rows;
   if (a.nsplit > 1) {
-    const int64_t pr = (int64_t)sp * a.s.total * a.Hq + orow;
+    if (mine) {
+      put2(reinterpret_cast<uint64_t*>(a.part_ml + sp * step + orow), m, l, d0 == 0);
+      uint64_t* po = reinterpret_cast<uint64_t*>(a.part_o + (sp * step + orow) * D + d0);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) a.part_o[pr * D + d0 + e] = x[e];
-    if (d0 == 0) a.part_ml[pr] = make_float2(m, l);
-    return;
+      for (int e = 0; e < kPer; e += 2) put2(po + e / 2, x[e], x[e + 1], true);
+    }
+    if (!a.tags) return;
+    // Join here if this part is the last to come.  The device-scope stores above
+    // have reached the level that all XCDs share once vmcnt is 0; only then is
+    // the part's tag stored, and the tags are looked at after that, so the part
+    // whose tag comes last sees all of them.  (Two parts may both see all: they
+    // write the same results.)  A tag is this call's number, so whatever the
+    // workspace held before counts as not there; whoever joins clears the tags,
+    // for a graph replays the same number.
+    __shared__ int complete;
+    const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (wave == 0) {
+      uint64_t* tags = a.tags + (((int64_t)b * a.row_tiles + tile_row) * a.c.H + h) * kMostParts;
+      if (lane == 0)
+        __hip_atomic_store(tags + sp, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const bool there =
+          lane >= parts ||
+          __hip_atomic_load(tags + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.call;
+      const bool all = __all(there);
+      if (all && lane < parts)
+        __hip_atomic_store(tags + lane, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (lane == 0) complete = all;
+    }
+    __syncthreads();
+    if (!complete || !mine) return;
+    // four parts' loads in flight at a time, the sums rescaled as M moves
+    m = kNone;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += 4) {
+      float2 ml[4], v[4][kPer / 2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t at = min(p0 + j, parts - 1) * step + orow;
+        ml[j] = get2(reinterpret_cast<const uint64_t*>(a.part_ml + at));
+        const uint64_t* po = reinterpret_cast<const uint64_t*>(a.part_o + at * D + d0);
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) v[j][e] = get2(po + e);
+        if (p0 + j >= parts) ml[j] = make_float2(kNone, 0.f);
+      }
+      const float top = fmaxf(m, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+      const float al = exp2_fast(m - top);
+      l *= al;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] *= al;
+      m = top;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (p0 + j >= parts) break;
+        const float w = exp2_fast(ml[j].x - m);
+        l = fmaf(w, ml[j].y, l);
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) {
+          x[2 * e] = fmaf(w, v[j][e].x, x[2 * e]);
+          x[2 * e + 1] = fmaf(w, v[j][e].y, x[2 * e + 1]);
+        }
+      }
+    }
   }
+  if (!mine) return;
   const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) x[e] = l == 0.f ? 0.f : x[e] * f;
@@ -768,15 +854,16 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
 }
 
 // ---- the join of a split call ----------------------------------------------
-// One wavefront a query row and head: the parts that have tiles, in order.
+// Workgroup: one query row and head.  Lane j of every wavefront holds part j's
+// M and L (at most 64 parts); the four wavefronts add up a quarter of the parts
+// each, in order, and then one another's sums.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int64_t most) {
-  const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // (b, i, head)
-  const int per = a.s.max_count;
-  if (w >= most) return;
-  const int hq = (int)(w % a.Hq);
-  const int i = (int)(w / a.Hq % per), b = (int)(w / a.Hq / per);
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
+  constexpr int kPer = D / 64;
+  __shared__ float sums[4][D];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hq = blockIdx.x % a.Hq;
+  const int i = blockIdx.x / a.Hq % a.s.max_count, b = blockIdx.x / a.Hq / a.s.max_count;
   int row0, n;
   kv_rows(a.s, b, row0, n);
   if (i >= n) return;
@@ -786,24 +873,42 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int64_t most) {
   const Parts pt = parts_of(a, len, n, r / a.tile_rows * a.tile_rows);
   const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;
   const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq, step = (int64_t)a.s.total * a.Hq;
-  float m = kNone;
-  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[p * step + orow].x);
-  float l = 0.f, x[D / 64];
+  const float2 ml = lane < parts ? a.part_ml[lane * step + orow] : make_float2(kNone, 0.f);
+  float m = ml.x;
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e) x[e] = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = a.part_ml[p * step + orow];
-    const float f = exp2_fast(ml.x - m);
-    l += f * ml.y;
-    const float* po = a.part_o + (p * step + orow) * D + lane * (D / 64);
+  for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+  const float f = exp2_fast(ml.x - m);
+  float l = f * ml.y;
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) x[e] += f * po[e];
+  for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
+  float sum[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) sum[e] = 0.f;
+  const float* po = a.part_o + orow * D + lane * kPer;
+  const int each = (parts + 3) / 4, p1 = min(parts, (wave + 1) * each);
+  for (int p = wave * each; p < p1; p += 4) {
+    float v[4][kPer];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[j][e] = po[min(p + j, p1 - 1) * step * D + e];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float w = p + j < p1 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), (p + j) & 63)) : 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) sum[e] = p + j < p1 ? fmaf(w, v[j][e], sum[e]) : sum[e];
+    }
   }
-  const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e) x[e] = l == 0.f ? 0.f : x[e] * f;
-  write_row(a, orow * D + lane * (D / 64), D / 64, x);
-  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
+  for (int e = 0; e < kPer; ++e) sums[wave][lane * kPer + e] = sum[e];
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d < D) {
+    const float x = sums[0][d] + sums[1][d] + (sums[2][d] + sums[3][d]);
+    const float y = l == 0.f ? 0.f : x / l;
+    write_row(a, orow * D + d, 1, &y);
+  }
+  if (a.lse && d == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
 }
 
 // ---- host ------------------------------------------------------------------
@@ -811,10 +916,14 @@ struct AttnPlan {
   bool prefill;
   int tile_rows, tile_tokens, row_tiles, nsplit, span_tiles;
   int64_t blocks;     // workgroups of the attention launch
-  size_t workspace, ml_at;
+  size_t workspace, ml_at, tags_at;  // tags_at 0: the parts are joined by a launch of their own
 };
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Parts that their last workgroup joins itself; with more of them its reads
+// take longer than a launch that spreads them over the GPU.
+constexpr int kJoinInside = 16;
 
 // Sizes only; MSQ_OK with blocks == 0 for an empty call.
 msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_attn& t, int D,
@@ -831,7 +940,7 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   int64_t longest = (int64_t)s.width << c.shift;
   if (t.max_kv_len > 0) longest = std::min(longest, t.max_kv_len);
   if (t.window > 0) longest = std::min<int64_t>(longest, (int64_t)t.window + s.max_count + kSpan);
-  p.prefill = s.max_count * G > 2 * kRowTile;
+  p.prefill = s.max_count * G > KV_T;
   p.tile_rows = !p.prefill ? kRowTile
                 : D == 64  ? Prefill<64>::kRows
                 : D == 128 ? Prefill<128>::kRows
@@ -846,22 +955,46 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
     const int64_t want = std::max<int64_t>(1, 256 / items);
     span = std::max<int64_t>(8, (tiles + want - 1) / want);
   } else {
-    // parts: about four workgroups a compute unit, each 8 to 64 tiles
-    const int64_t want = std::max<int64_t>(1, 1024 / items);
-    span = std::min<int64_t>(std::max<int64_t>(8, (tiles + want - 1) / want), 64);
+    // parts: about two workgroups a compute unit, each 4 to 256 tiles.  More and
+    // smaller parts spend longer in their starts and joins (32 sequences of up
+    // to 4097 tokens on 8 heads: 2, 3, 4, 8 parts 44, 47, 54, 61 us; 4 of
+    // 131072: 16, 32, 64 parts 191, 205, 206 us), one a compute unit
+    // leaves it idle behind the short sequences (46 us)
+    const int64_t want = std::max<int64_t>(1, 512 / items);
+    span = std::min<int64_t>(std::max<int64_t>(4, (tiles + want - 1) / want), 256);
   }
-  p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, 256);
+  p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, kMostParts);
   p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
   p.blocks = items * p.nsplit;
   if (p.blocks > (int64_t)0x7FFFFFFF) return MSQ_ERR_SHAPE;
   if (p.nsplit > 1) {
-    // the join's grid: four (sequence, row, head) a workgroup
-    if ((int64_t)s.batch * s.max_count * G > (int64_t)0x7FFFFFFF * 4 / c.H) return MSQ_ERR_SHAPE;
+    // the join's grid: (sequence, row, head)
+    if ((int64_t)s.batch * s.max_count * G > (int64_t)0x7FFFFFFF / c.H) return MSQ_ERR_SHAPE;
     const size_t rows = (size_t)s.total * t.q_heads * p.nsplit;
     p.ml_at = (rows * D * 4 + 255) / 256 * 256;
     p.workspace = p.ml_at + rows * 8;
+    if (!p.prefill && p.nsplit <= kJoinInside) {
+      p.tags_at = (p.workspace + 255) / 256 * 256;
+      p.workspace = p.tags_at + (size_t)items * kMostParts * 8;
+    }
   }
   return MSQ_OK;
+}
+
+// A number for one call: never 0, and from a start that depends on the time, the
+// process and where it was loaded, so that no call finds its number in what a
+// workspace held before.
+uint64_t next_call() {
+  static std::atomic<uint64_t> count{0};
+  static const uint64_t start = [] {
+    uint64_t z = (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count() ^
+                 (uint64_t)getpid() << 40 ^ (uint64_t)reinterpret_cast<uintptr_t>(&count);
+    z = (z ^ z >> 30) * 0xBF58476D1CE4E5B9u;  // a mix of all bits (splitmix64)
+    z = (z ^ z >> 27) * 0x94D049BB133111EBu;
+    return z ^ z >> 31;
+  }();
+  const uint64_t n = start + count.fetch_add(1, std::memory_order_relaxed);
+  return n ? n : start + count.fetch_add(1, std::memory_order_relaxed);
 }
 
 template <int D>
@@ -870,13 +1003,12 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
     hipLaunchKernelGGL((k_kv_prefill<D>), dim3((unsigned)p.blocks),
                        dim3(Prefill<D>::kThreads), 8 * 16 * Prefill<D>::kStrip, stream, a);
   } else {
-    const size_t lds = 4 * kRowTile * (D + 4) * 4 + 2 * 4 * kRowTile * 4;
+    const size_t lds = 4 * kRowTile * (D + 4 + 2) * 4;
     hipLaunchKernelGGL((k_kv_decode<D>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
   }
-  if (p.nsplit > 1) {
-    const int64_t most = (int64_t)a.s.batch * a.s.max_count * a.Hq;
-    hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)((most + 3) / 4)), dim3(256), 0, stream, a,
-                       most);
+  if (p.nsplit > 1 && !p.tags_at) {
+    hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)((int64_t)a.s.batch * a.s.max_count * a.Hq)),
+                       dim3(256), 0, stream, a);
   }
   return hipGetLastError();
 }
@@ -925,6 +1057,10 @@ extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_s
     if (!workspace || !aligned_to(workspace, 256)) return MSQ_ERR_INVALID_ARG;
     a.part_o = reinterpret_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(workspace) + p.ml_at);
+    if (p.tags_at) {
+      a.tags = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(workspace) + p.tags_at);
+      a.call = next_call();
+    }
   }
   a.q = t.q;
   a.qts = t.q_token_stride;

@@ -348,6 +348,33 @@ def test_attention_long_split(msq):
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+def test_attention_workspace_may_hold_anything(msq):
+    """Calls of different shapes share one workspace, whose parts are joined inside the launch or
+    by a second one: whatever the last call left, and whatever it held at first, the results
+    are those with a workspace of their own, bit for bit."""
+    rng = np.random.default_rng(20)
+    shapes = [(128, 2, 4, [900, 300, 0], 1), (64, 1, 8, [700], 4), (128, 1, 2, [6000], 1),
+              (256, 2, 1, [300, 777], 1), (128, 2, 8, [400, 1000], 2), (128, 1, 8, [900], 30)]
+    made = []
+    for D, H, G, lens, n in shapes:
+        table, blocks = scattered(rng, lens, 64)
+        p = Pair(msq, blocks, H, D, 64, seed=D + n)
+        p.write(table, [0] * len(lens), lens)
+        q = torch.randn(n * len(lens), H * G, D, device="cuda")
+        need = msq.kv_attention_workspace_bytes(p.gpu, n * len(lens), H * G, len(lens), n,
+                                                table.shape[1] * 64)
+        want = msq.kv_attention(q, p.gpu, i32(table), i32(lens))
+        made.append((p.gpu, q, i32(table), i32(lens), need, want))
+    assert sum(m[4] > 0 for m in made) >= 5
+    ws = torch.randint(0, 256, (max(m[4] for m in made),), dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        for i in rng.permutation(len(made)):
+            gpu, q, table, lens, _, want = made[i]
+            got = msq.kv_attention(q, gpu, table, lens, workspace=ws)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want), shapes[i]
+
+
 def test_attention_value_scales_far_apart(msq):
     """Value blocks whose scales differ by 2^80, zero blocks among them: the error stays
     relative to the largest contribution."""
