@@ -31,9 +31,6 @@
 #include "msq.h"
 #include "msq_kv.h"
 
-#ifndef KV_T
-#define KV_T 32
-#endif
 namespace msq {
 namespace {
 
@@ -91,21 +88,27 @@ __device__ inline half8 codes_f16x8(uint32_t w0, uint32_t w1) {
   return r.h;
 }
 
-// Eight query values as fp32.
-__device__ inline void load8(const void* q, int f32, int64_t at, float* x) {
+// Eight query values, as loaded and as fp32.
+struct Raw8 {
+  uint4 a, b;  // bf16: a only
+};
+__device__ inline Raw8 load8(const void* q, int f32, int64_t at) {
+  Raw8 r{};
   if (f32) {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(q) + at);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(q) + at);
+    r.a = p[0];
+    r.b = p[1];
   } else {
-    const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(q) + at);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    r.a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(q) + at);
+  }
+  return r;
+}
+__device__ inline void widen8(const Raw8& r, int f32, float* x) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+  for (int i = 0; i < 4; ++i) {
+    x[i] = __uint_as_float(f32 ? w[i] : i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    x[4 + i] = __uint_as_float(f32 ? w[4 + i] : i & 1 ? w[2 + (i >> 1)] & 0xFFFF0000u : w[2 + (i >> 1)] << 16);
   }
 }
 
@@ -253,7 +256,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   const Parts pt = parts_of(a, len, n, r0);
   const int lo1 = pt.lo_last, hi0 = pt.hi_first;
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
-  if (t0 >= t1 && a.nsplit > 1) return;  // the join looks at the parts that have tiles only
+  const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;  // that have tiles
+  // rows that see nothing are left to the first part, or to the join launch
+  if (t0 >= t1 && a.nsplit > 1 && !(a.tags && parts == 0 && sp == 0)) return;
 
   const int64_t r = min(r0 + col, rows - 1);
   const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
@@ -269,7 +274,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
     const int64_t at = (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      load8(a.q, a.q_f32, at + 64 * (s >> 1) + 16 * g + 8 * (s & 1), x[s]);
+      widen8(load8(a.q, a.q_f32, at + 64 * (s >> 1) + 16 * g + 8 * (s & 1)), a.q_f32, x[s]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         amax = fmaxf(amax, fabsf(x[s][e]));
@@ -415,7 +420,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   const int64_t orow = (int64_t)(row0 + io) * a.Hq + h * a.G + (int)(ro - (int64_t)io * a.G);
   const int64_t step = (int64_t)a.s.total * a.Hq;
   const bool mine = r0 + rr < rows;
-  if (a.nsplit > 1) {
+  if (a.tags ? parts > 1 : a.nsplit > 1) {
     if (mine) {
       put2(reinterpret_cast<uint64_t*>(a.part_ml + sp * step + orow), m, l, d0 == 0);
       uint64_t* po = reinterpret_cast<uint64_t*>(a.part_o + (sp * step + orow) * D + d0);
@@ -431,7 +436,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
     // workspace held before counts as not there; whoever joins clears the tags,
     // for a graph replays the same number.
     __shared__ int complete;
-    const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (wave == 0) {
@@ -506,11 +510,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 // three do not depend on each other, so its vector instructions run between its
 // matrix instructions.  LDS holds four strips of keys and four of values, in
 // turn; one barrier a stage.
-template <int D>
+template <int D, int W>
 struct Prefill {
   static constexpr int kStage = 64;  // tokens: two strips
   static constexpr int kSteps = D / 16, kTiles = D / 32;
-  static constexpr int kWaves = D == 128 ? 8 : 4;
+  static constexpr int kWaves = W;
   static constexpr int kThreads = 64 * kWaves, kRows = 32 * kWaves;
   static constexpr int kUnits = 8 * D / kThreads;  // 16-byte pieces of keys and values a thread
   static constexpr int kStrip = 4 * D;             // 16-byte pieces of a strip in LDS
@@ -518,9 +522,9 @@ struct Prefill {
   static constexpr int kAhead = 4;                 // operands read from LDS before their product
 };
 
-template <int D>
-__global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
-  using C = Prefill<D>;
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
+  using C = Prefill<D, W>;
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
   constexpr int kProducts = C::kProducts, kAhead = C::kAhead;
   int64_t wg = blockIdx.x;
@@ -532,12 +536,12 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
   const int tile_row = a.row_tiles - 1 - (int)(wg / a.s.batch);  // the longest rows first
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
+  const int len = clamped_len(a, b);
   int row0, n;
   kv_rows(a.s, b, row0, n);
   const int64_t rows = (int64_t)n * a.G;
   const int64_t r0 = (int64_t)tile_row * C::kRows;
   if (r0 >= rows) return;
-  const int len = clamped_len(a, b);
   const Parts pt = parts_of(a, len, n, r0);
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   if (t0 >= t1 && a.nsplit > 1) return;
@@ -546,6 +550,10 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
   const int64_t w0 = r0 + 32 * wave;
   const int64_t r = min(w0 + col, rows - 1);
   const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
+  Raw8 qraw[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s)
+    qraw[s] = load8(a.q, a.q_f32, (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs + 8 * half + 16 * s);
   int my_lo, my_hi;
   row_range(len, n, i, a.causal, a.window, my_lo, my_hi);
   int w_lo, w_hi, w_lo_last, w_hi_first;
@@ -555,37 +563,6 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
   // its stages: a0 .. a1 - 1 (none: a0 == a1)
   const int a0 = min(max(t0, w_lo / kStage), t1);
   const int a1 = max(a0, min(t1, (int)(((int64_t)w_hi + kStage - 1) / kStage)));
-
-  half8 q[kSteps];  // slots (half, e) of step s are dims 16 s + 8 half + e
-  float cq;
-  {
-    const int64_t at = (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs + 8 * half;
-    float amax = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      float x[8];
-      load8(a.q, a.q_f32, at + 16 * s, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        amax = fmaxf(amax, fabsf(x[e]));
-        bad |= !(fabsf(x[e]) <= 3.402823466e38f);
-      }
-    }
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
-    int nb = bad;
-    nb |= __shfl_xor(nb, 32);
-    float up, down;
-    row_scale(amax, nb != 0, up, down);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      float x[8];
-      load8(a.q, a.q_f32, at + 16 * s, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(x[e] * up);
-    }
-    cq = a.c2 * down;
-  }
 
   f32x16 o[kTiles];
 #pragma unroll
@@ -619,13 +596,9 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
   };
   int batch = 2 * t0;  // its first strip
   int id0 = blocks_at(t0), id1 = blocks_at(t0 + 32), id2 = blocks_at(t0 + 64);
-  Scales sc0 = scales_at(t0, id0), sc1 = scales_at(t0 + 32, id1);
   auto id_of = [&](int i) {  // a strip of this batch, the next one, or just before
     const int j = i - batch;
     return __builtin_amdgcn_readlane(j < 64 ? id0 : id1, j & 63);
-  };
-  auto lane_of = [&](float x, int i) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i - batch));
   };
 
   // this thread's pieces of the keys of strips ik, ik + 1 and of the values of
@@ -633,22 +606,59 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
   const int64_t block_bytes = (int64_t)a.c.H * P * D;
   const uint8_t* const kc = a.c.kc + (int64_t)h * P * D;
   const uint8_t* const vc = a.c.vc + (int64_t)h * P * D;
-  uint4 st[C::kUnits];
-  auto load_one = [&](int ik, int iv, int u) {
+  typedef uint4 Codes[C::kUnits];
+  auto load_one = [&](Codes& st, int ik, int iv, int u) {
     const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
     const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
     const int64_t blk = max(id_of(i), 0) * block_bytes;
     const uint32_t at = (uint32_t)(((32 * i) & (P - 1)) * D + 16 * (n & (2 * D - 1)));
     st[u] = *reinterpret_cast<const uint4*>((kind ? vc : kc) + blk + at);
   };
-  auto load = [&](int ik, int iv) {
+  auto load = [&](Codes& st, int ik, int iv) {
 #pragma unroll
-    for (int u = 0; u < C::kUnits; ++u) load_one(ik, iv, u);
+    for (int u = 0; u < C::kUnits; ++u) load_one(st, ik, iv, u);
   };
+  // The keys of the first three strips and the values of the first; the strip of
+  // values before it is multiplied by weights of 0, so it gets finite numbers.
+  Codes st, st0, st1;
+  load(st0, 2 * t0 - 1, 2 * t0 - 1);
+  load(st1, 2 * t0 + 1, 2 * t0 + 1);
+  load(st, 2 * t0 + 3, 2 * t0 + 1);
+  Scales sc0 = scales_at(t0, id0), sc1 = scales_at(t0 + 32, id1);
+  auto lane_of = [&](float x, int i) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i - batch));
+  };
+
+  half8 q[kSteps];  // slots (half, e) of step s are dims 16 s + 8 half + e
+  float cq;
+  {
+    float x[kSteps][8], amax = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) widen8(qraw[s], a.q_f32, x[s]);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        amax = fmaxf(amax, fabsf(x[s][e]));
+        bad |= !(fabsf(x[s][e]) <= 3.402823466e38f);
+      }
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    int nb = bad;
+    nb |= __shfl_xor(nb, 32);
+    float up, down;
+    row_scale(amax, nb != 0, up, down);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(x[s][e] * up);
+    cq = a.c2 * down;
+  }
+
   // and from there as f16 into LDS: keys [strip][step][half][row], values
   // [strip][d tile][step][half][d], 16 bytes each
   half8* const lds = reinterpret_cast<half8*>(smem_kv);
-  auto convert_half = [&](int ik, int iv, int u, int second) {
+  auto convert_half = [&](const Codes& st, int ik, int iv, int u, int second) {
     const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
     const int m = n & (2 * D - 1), g = m % 64 / 16;
     const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
@@ -659,9 +669,9 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
     p[second * (kind ? 16 : 32)] =
         second ? codes_f16x8(st[u].z, st[u].w) : codes_f16x8(st[u].x, st[u].y);
   };
-  auto convert = [&](int ik, int iv) {
+  auto convert = [&](const Codes& st, int ik, int iv) {
 #pragma unroll
-    for (int j = 0; j < 2 * C::kUnits; ++j) convert_half(ik, iv, j >> 1, j & 1);
+    for (int j = 0; j < 2 * C::kUnits; ++j) convert_half(st, ik, iv, j >> 1, j & 1);
   };
   // operand m of strip i's products: the keys of strip i + 1, then the values
   // of strip i - 1
@@ -755,11 +765,11 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
       if constexpr (!kSecond) {
 #pragma unroll
         for (int j = 0; j < 2 * C::kUnits; ++j)
-          if (j * kProducts / (2 * C::kUnits) == m) convert_half(i + 3, i + 1, j >> 1, j & 1);
+          if (j * kProducts / (2 * C::kUnits) == m) convert_half(st, i + 3, i + 1, j >> 1, j & 1);
       } else {
 #pragma unroll
         for (int u = 0; u < C::kUnits; ++u)
-          if (u * kProducts / C::kUnits == m) load_one(i + 4, i + 2, u);
+          if (u * kProducts / C::kUnits == m) load_one(st, i + 4, i + 2, u);
       }
       if (m >= kProducts - kMax) {
 #pragma unroll
@@ -783,13 +793,8 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
     f32x16 sa, sb;
     half8 pa[2], pb[2];
     pa[0] = pa[1] = pb[0] = pb[1] = half8{};
-    // the first three strips of keys and the first of values; the strip of
-    // values before that is multiplied by weights of 0, so it gets finite numbers
-    load(2 * t0 - 1, 2 * t0 - 1);
-    convert(2 * t0 - 1, 2 * t0 - 1);
-    load(2 * t0 + 1, 2 * t0 + 1);
-    convert(2 * t0 + 1, 2 * t0 + 1);
-    load(2 * t0 + 3, 2 * t0 + 1);
+    convert(st0, 2 * t0 - 1, 2 * t0 - 1);
+    convert(st1, 2 * t0 + 1, 2 * t0 + 1);
     lds_barrier();
     sa = f32x16{};
 #pragma unroll
@@ -806,8 +811,8 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
     };
     auto convert_only = [&](int t) {
       next_batch(t);
-      convert(2 * t + 3, 2 * t + 1);
-      load(2 * t + 5, 2 * t + 3);
+      convert(st, 2 * t + 3, 2 * t + 1);
+      load(st, 2 * t + 5, 2 * t + 3);
       lds_barrier();
     };
     // outside its own stages a wavefront only converts; the stage before them
@@ -854,26 +859,39 @@ __global__ __launch_bounds__(Prefill<D>::kThreads, D == 256 ? 1 : 2) void k_kv_p
 }
 
 // ---- the join of a split call ----------------------------------------------
-// Workgroup: one query row and head.  Lane j of every wavefront holds part j's
-// M and L (at most 64 parts); the four wavefronts add up a quarter of the parts
-// each, in order, and then one another's sums.
-template <int D>
-__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
+// kWaves wavefronts (1 or 4) take one query row and head.  Lane j of each holds
+// part j's M and L (at most 64 parts); each wavefront adds up its share of the
+// parts, in order, and with four of them one another's sums.
+template <int D, int kWaves>
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
   constexpr int kPer = D / 64;
-  __shared__ float sums[4][D];
+  __shared__ float sums[kWaves == 4 ? 4 : 1][D];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hq = blockIdx.x % a.Hq;
-  const int i = blockIdx.x / a.Hq % a.s.max_count, b = blockIdx.x / a.Hq / a.s.max_count;
+  const int mine = kWaves == 4 ? wave : 0;
+  const int id = kWaves == 4 ? blockIdx.x : 4 * blockIdx.x + wave;
+  if (id >= rows) return;
+  const int hq = id % a.Hq, i = id / a.Hq % a.s.max_count, b = id / a.Hq / a.s.max_count;
   int row0, n;
   kv_rows(a.s, b, row0, n);
   if (i >= n) return;
   const int len = clamped_len(a, b);
   // the row tile this row was in, as the split kernel saw it
-  const int64_t r = (int64_t)i * a.G + hq % a.G;
+  const int r = i * a.G + hq % a.G;
   const Parts pt = parts_of(a, len, n, r / a.tile_rows * a.tile_rows);
   const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;
   const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq, step = (int64_t)a.s.total * a.Hq;
   const float2 ml = lane < parts ? a.part_ml[lane * step + orow] : make_float2(kNone, 0.f);
+  const int each = (parts + kWaves - 1) / kWaves, p1 = min(parts, (mine + 1) * each);
+  const float* po = a.part_o + orow * D + lane * kPer;
+  float v[4][kPer], sum[kPer];
+  auto fetch = [&](int p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[j][e] = po[min(p + j, p1 - 1) * step * D + e];
+  };
+  int p = mine * each;
+  if (p < p1) fetch(p);
   float m = ml.x;
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
@@ -881,39 +899,37 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
   float l = f * ml.y;
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
-  float sum[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) sum[e] = 0.f;
-  const float* po = a.part_o + orow * D + lane * kPer;
-  const int each = (parts + 3) / 4, p1 = min(parts, (wave + 1) * each);
-  for (int p = wave * each; p < p1; p += 4) {
-    float v[4][kPer];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) v[j][e] = po[min(p + j, p1 - 1) * step * D + e];
+  for (; p < p1; p += 4) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float w = p + j < p1 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), (p + j) & 63)) : 0.f;
+      const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), (p + j) & 63));
 #pragma unroll
       for (int e = 0; e < kPer; ++e) sum[e] = p + j < p1 ? fmaf(w, v[j][e], sum[e]) : sum[e];
     }
+    if (p + 4 < p1) fetch(p + 4);
+  }
+  if constexpr (kWaves == 4) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) sums[wave][lane * kPer + e] = sum[e];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int d = lane * kPer + e;
+      sum[e] = sums[0][d] + sums[1][d] + (sums[2][d] + sums[3][d]);
+    }
   }
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) sums[wave][lane * kPer + e] = sum[e];
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d < D) {
-    const float x = sums[0][d] + sums[1][d] + (sums[2][d] + sums[3][d]);
-    const float y = l == 0.f ? 0.f : x / l;
-    write_row(a, orow * D + d, 1, &y);
-  }
-  if (a.lse && d == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
+  for (int e = 0; e < kPer; ++e) sum[e] = l == 0.f ? 0.f : sum[e] / l;
+  write_row(a, orow * D + lane * kPer, kPer, sum);
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
 }
 
 // ---- host ------------------------------------------------------------------
 struct AttnPlan {
-  bool prefill;
+  int waves;  // of k_kv_prefill; 0: k_kv_decode
   int tile_rows, tile_tokens, row_tiles, nsplit, span_tiles;
   int64_t blocks;     // workgroups of the attention launch
   size_t workspace, ml_at, tags_at;  // tags_at 0: the parts are joined by a launch of their own
@@ -940,18 +956,18 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   int64_t longest = (int64_t)s.width << c.shift;
   if (t.max_kv_len > 0) longest = std::min(longest, t.max_kv_len);
   if (t.window > 0) longest = std::min<int64_t>(longest, (int64_t)t.window + s.max_count + kSpan);
-  p.prefill = s.max_count * G > KV_T;
-  p.tile_rows = !p.prefill ? kRowTile
-                : D == 64  ? Prefill<64>::kRows
-                : D == 128 ? Prefill<128>::kRows
-                           : Prefill<256>::kRows;
-  p.tile_tokens = p.prefill ? Prefill<128>::kStage : kSpan;
-  p.row_tiles = (int)((s.max_count * G + p.tile_rows - 1) / p.tile_rows);
-  const int64_t items = (int64_t)s.batch * c.H * p.row_tiles;
+  const int64_t rows = s.max_count * G, lists = (int64_t)s.batch * c.H;
+  p.waves = 0;
+  if (rows > (D == 256 ? 32 : 64)) {
+    p.waves = D == 128 && longest > 1024 ? 8 : 4;
+  }
+  p.tile_rows = p.waves ? 32 * p.waves : kRowTile;
+  p.tile_tokens = p.waves ? 64 : kSpan;
+  p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
+  const int64_t items = lists * p.row_tiles;
   const int64_t tiles = std::max<int64_t>(1, (longest + p.tile_tokens - 1) / p.tile_tokens);
   int64_t span;
-  if (p.prefill) {
-    // parts: one workgroup a compute unit, each at least 8 stages
+  if (p.waves) {
     const int64_t want = std::max<int64_t>(1, 256 / items);
     span = std::max<int64_t>(8, (tiles + want - 1) / want);
   } else {
@@ -973,7 +989,7 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
     const size_t rows = (size_t)s.total * t.q_heads * p.nsplit;
     p.ml_at = (rows * D * 4 + 255) / 256 * 256;
     p.workspace = p.ml_at + rows * 8;
-    if (!p.prefill && p.nsplit <= kJoinInside) {
+    if (!p.waves && p.nsplit <= kJoinInside) {
       p.tags_at = (p.workspace + 255) / 256 * 256;
       p.workspace = p.tags_at + (size_t)items * kMostParts * 8;
     }
@@ -999,16 +1015,26 @@ uint64_t next_call() {
 
 template <int D>
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  if (p.prefill) {
-    hipLaunchKernelGGL((k_kv_prefill<D>), dim3((unsigned)p.blocks),
-                       dim3(Prefill<D>::kThreads), 8 * 16 * Prefill<D>::kStrip, stream, a);
+  if (p.waves) {
+    auto prefill = [&](auto w) {
+      using C = Prefill<D, decltype(w)::value>;
+      hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves>), dim3((unsigned)p.blocks), dim3(C::kThreads),
+                         8 * 16 * C::kStrip, stream, a);
+    };
+    if constexpr (D == 128)
+      if (p.waves == 8) prefill(std::integral_constant<int, 8>{});
+    if (p.waves == 4) prefill(std::integral_constant<int, 4>{});
   } else {
     const size_t lds = 4 * kRowTile * (D + 4 + 2) * 4;
     hipLaunchKernelGGL((k_kv_decode<D>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
   }
   if (p.nsplit > 1 && !p.tags_at) {
-    hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)((int64_t)a.s.batch * a.s.max_count * a.Hq)),
-                       dim3(256), 0, stream, a);
+    const int rows = a.s.batch * a.s.max_count * a.Hq;
+    // many parts of few rows: four wavefronts a row
+    if (p.nsplit > 16)
+      hipLaunchKernelGGL((k_kv_join<D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, a, rows);
+    else
+      hipLaunchKernelGGL((k_kv_join<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, rows);
   }
   return hipGetLastError();
 }

@@ -94,9 +94,10 @@ class Pair:
                window=0, scale=0.0, **kw):
         q, qt = rounded(q, dtype)
         off = offsets(counts)
+        to = torch.full(qt.shape, float("nan"), dtype=out, device="cuda")  # every row is written
         got, lse = self.msq.kv_attention(qt, self.gpu, i32(table), i32(lens), i32(off),
-                                         max_count=max(counts, default=0), scale=scale, causal=causal, window=window,
-                                         out_dtype=out, return_lse=True, **kw)
+                                         max_count=max(counts, default=0), scale=scale, causal=causal,
+                                         window=window, out=to, return_lse=True, **kw)
         torch.cuda.synchronize()
         table = np.asarray(table)
         for b, (n, L) in enumerate(zip(counts, lens)):
@@ -328,6 +329,10 @@ def test_attention_rows_that_see_nothing(msq):
         for window in (0, 2):
             p.attend(q, table, lens, counts, window=window)
             p.attend(q, table, lens, counts, window=window, max_kv_len=100000)
+        # a long table: the work is split, and some sequences have no part
+        wide = np.concatenate([table, np.full((4, 40), -1, table.dtype)], 1)
+        for hint in (0, 600):
+            p.attend(q, wide, lens, counts, max_kv_len=hint)
 
 
 def test_attention_long_split(msq):
