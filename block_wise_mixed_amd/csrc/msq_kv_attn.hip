@@ -512,11 +512,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 // turn; one barrier a stage.
 template <int D, int W>
 struct Prefill {
-  static constexpr int kStage = 64;  // tokens: two strips
+  static constexpr int kStrips = 2;                // a stage
+  static constexpr int kStage = 32 * kStrips;      // tokens
   static constexpr int kSteps = D / 16, kTiles = D / 32;
   static constexpr int kWaves = W;
   static constexpr int kThreads = 64 * kWaves, kRows = 32 * kWaves;
-  static constexpr int kUnits = 8 * D / kThreads;  // 16-byte pieces of keys and values a thread
+  static constexpr int kUnits = 4 * kStrips * D / kThreads;  // 16-byte pieces of keys and values a thread
   static constexpr int kStrip = 4 * D;             // 16-byte pieces of a strip in LDS
   static constexpr int kProducts = kSteps + 2 * kTiles;  // of a strip: keys, then values
   static constexpr int kAhead = 4;                 // operands read from LDS before their product
@@ -526,7 +527,8 @@ template <int D, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
   using C = Prefill<D, W>;
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
-  constexpr int kProducts = C::kProducts, kAhead = C::kAhead;
+  constexpr int kProducts = C::kProducts, kAhead = C::kAhead, kStrips = C::kStrips;
+  constexpr int kRing = 2 * kStrips, kBatch = 64 / kStrips;
   int64_t wg = blockIdx.x;
   const int h = (int)(wg % a.c.H);
   wg /= a.c.H;
@@ -594,8 +596,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     s.inv = __builtin_amdgcn_rcpf(one);
     return s;
   };
-  int batch = 2 * t0;  // its first strip
-  int id0 = blocks_at(t0), id1 = blocks_at(t0 + 32), id2 = blocks_at(t0 + 64);
+  int batch = kStrips * t0;  // its first strip
+  int id0 = blocks_at(t0), id1 = blocks_at(t0 + kBatch), id2 = blocks_at(t0 + 2 * kBatch);
   auto id_of = [&](int i) {  // a strip of this batch, the next one, or just before
     const int j = i - batch;
     return __builtin_amdgcn_readlane(j < 64 ? id0 : id1, j & 63);
@@ -608,8 +610,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   const uint8_t* const vc = a.c.vc + (int64_t)h * P * D;
   typedef uint4 Codes[C::kUnits];
   auto load_one = [&](Codes& st, int ik, int iv, int u) {
-    const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
-    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
+    const int kind = C::kThreads * u / (2 * kStrips * D), n = C::kThreads * u + (int)threadIdx.x;
+    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & (kStrips - 1));
     const int64_t blk = max(id_of(i), 0) * block_bytes;
     const uint32_t at = (uint32_t)(((32 * i) & (P - 1)) * D + 16 * (n & (2 * D - 1)));
     st[u] = *reinterpret_cast<const uint4*>((kind ? vc : kc) + blk + at);
@@ -621,10 +623,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   // The keys of the first three strips and the values of the first; the strip of
   // values before it is multiplied by weights of 0, so it gets finite numbers.
   Codes st, st0, st1;
-  load(st0, 2 * t0 - 1, 2 * t0 - 1);
-  load(st1, 2 * t0 + 1, 2 * t0 + 1);
-  load(st, 2 * t0 + 3, 2 * t0 + 1);
-  Scales sc0 = scales_at(t0, id0), sc1 = scales_at(t0 + 32, id1);
+  const int i0 = kStrips * t0;
+  load(st0, i0 - kStrips + 1, i0 - 1);
+  load(st1, i0 + 1, i0 + kStrips - 1);
+  load(st, i0 + kStrips + 1, i0 + kStrips - 1);
+  Scales sc0 = scales_at(t0, id0), sc1 = scales_at(t0 + kBatch, id1);
   auto lane_of = [&](float x, int i) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i - batch));
   };
@@ -659,11 +662,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   // [strip][d tile][step][half][d], 16 bytes each
   half8* const lds = reinterpret_cast<half8*>(smem_kv);
   auto convert_half = [&](const Codes& st, int ik, int iv, int u, int second) {
-    const int kind = C::kThreads * u / (4 * D), n = C::kThreads * u + (int)threadIdx.x;
+    const int kind = C::kThreads * u / (2 * kStrips * D), n = C::kThreads * u + (int)threadIdx.x;
     const int m = n & (2 * D - 1), g = m % 64 / 16;
-    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & 1);
+    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & (kStrips - 1));
     const int tok = 16 * (m / D) + (m & 15);
-    half8* p = lds + (4 * kind + (i & 3)) * C::kStrip +
+    half8* p = lds + (kRing * kind + (i & (kRing - 1))) * C::kStrip +
                (kind ? (4 * (m / 64) + g) * 32 + (m & 15)
                      : (4 * (m % D / 64) + g) * 64 + ((tok & 7) | (tok & 8) << 1 | (tok & 16) >> 1));
     p[second * (kind ? 16 : 32)] =
@@ -676,8 +679,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   // operand m of strip i's products: the keys of strip i + 1, then the values
   // of strip i - 1
   auto operand = [&](int i, int m) {
-    const half8* kl = lds + ((i + 1) & 3) * C::kStrip + lane;
-    const half8* vl = lds + (4 + ((i - 1) & 3)) * C::kStrip + lane;
+    const half8* kl = lds + ((i + 1) & (kRing - 1)) * C::kStrip + lane;
+    const half8* vl = lds + (kRing + ((i - 1) & (kRing - 1))) * C::kStrip + lane;
     const int v = m - kSteps;
     return m < kSteps ? kl[m * 64] : vl[(2 * (v % kTiles) + v / kTiles) * 64];
   };
@@ -700,8 +703,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   // Lane (col, half), register e: row col, token 8 (e / 8) + 4 half + e % 4 +
   // 16 (e / 4 % 2).
   auto strip = [&](int i, f32x16& s, f32x16& sn, float& top, half8 (&p)[2], half8 (&pp)[2],
-                   auto second) {
-    constexpr bool kSecond = decltype(second)::value;  // of its stage
+                   auto which) {
+    constexpr int kWhich = decltype(which)::value;  // of its stage
     const int tok = 32 * i;
     const bool gone = __builtin_amdgcn_readlane(id0, i - batch) < 0;
     const float f = fmaxf(cq * lane_of(sc0.sk, i), kTinyStep);
@@ -754,7 +757,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
                                                                o[v % kTiles], 0, 0, 0);
       if (m + kAhead < kProducts)
         fr[m % kAhead] = operand(i, m + kAhead);
-      else if (!kSecond)
+      else if (kWhich < kStrips - 1)
         fr[m % kAhead] = operand(i + 1, m + kAhead - kProducts);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -762,14 +765,17 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
         w[e] = exp2_fast(fmaf(s[e], f, add));
         if (e >= 2) use(e - 2);
       }
-      if constexpr (!kSecond) {
+      // a stage's first strip converts, its second one loads
+      if constexpr (kWhich == 0) {
 #pragma unroll
         for (int j = 0; j < 2 * C::kUnits; ++j)
-          if (j * kProducts / (2 * C::kUnits) == m) convert_half(st, i + 3, i + 1, j >> 1, j & 1);
+          if (j * kProducts / (2 * C::kUnits) == m)
+            convert_half(st, i + kStrips + 1, i + kStrips - 1, j >> 1, j & 1);
       } else {
 #pragma unroll
         for (int u = 0; u < C::kUnits; ++u)
-          if (u * kProducts / C::kUnits == m) load_one(st, i + 4, i + 2, u);
+          if (u * kProducts / C::kUnits == m)
+            load_one(st, i - 1 + 2 * kStrips + 1, i - 1 + 2 * kStrips - 1, u);
       }
       if (m >= kProducts - kMax) {
 #pragma unroll
@@ -793,26 +799,27 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     f32x16 sa, sb;
     half8 pa[2], pb[2];
     pa[0] = pa[1] = pb[0] = pb[1] = half8{};
-    convert(st0, 2 * t0 - 1, 2 * t0 - 1);
-    convert(st1, 2 * t0 + 1, 2 * t0 + 1);
+    convert(st0, i0 - kStrips + 1, i0 - 1);
+    convert(st1, i0 + 1, i0 + kStrips - 1);
     lds_barrier();
     sa = f32x16{};
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
-      sa = __builtin_amdgcn_mfma_f32_32x32x16_f16(operand(2 * t0 - 1, k), q[k], sa, 0, 0, 0);
+      sa = __builtin_amdgcn_mfma_f32_32x32x16_f16(operand(i0 - 1, k), q[k], sa, 0, 0, 0);
     float top = largest(sa);
+    lds_barrier();  // the first stage's conversion takes the place of these keys
     auto next_batch = [&](int t) {
-      if (2 * t - batch == 64) {
-        batch = 2 * t;
+      if (kStrips * t - batch == 64) {
+        batch = kStrips * t;
         id0 = id1, sc0 = sc1, id1 = id2;
-        sc1 = scales_at(t + 32, id1);
-        id2 = blocks_at(t + 64);
+        sc1 = scales_at(t + kBatch, id1);
+        id2 = blocks_at(t + 2 * kBatch);
       }
     };
     auto convert_only = [&](int t) {
       next_batch(t);
-      convert(st, 2 * t + 3, 2 * t + 1);
-      load(st, 2 * t + 5, 2 * t + 3);
+      convert(st, kStrips * (t + 1) + 1, kStrips * (t + 1) - 1);
+      load(st, kStrips * (t + 2) + 1, kStrips * (t + 2) - 1);
       lds_barrier();
     };
     // outside its own stages a wavefront only converts; the stage before them
@@ -821,13 +828,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     for (; t < a0 - 1; ++t) convert_only(t);
     for (const int end = min(a1 + 1, t1); t < end; ++t) {
       next_batch(t);
+      const int i = kStrips * t;
 #pragma unroll
-      for (int m = 0; m < kAhead; ++m) fr[m] = operand(2 * t, m);
-      strip(2 * t, sa, sb, top, pa, pb, std::false_type{});
-      strip(2 * t + 1, sb, sa, top, pb, pa, std::true_type{});
+      for (int m = 0; m < kAhead; ++m) fr[m] = operand(i, m);
+      strip(i, sa, sb, top, pa, pb, std::integral_constant<int, 0>{});
+      strip(i + 1, sb, sa, top, pb, pa, std::integral_constant<int, 1>{});
       lds_barrier();
     }
-    if (a1 >= t1) values(2 * t1 - 1, pb);
+    if (a1 >= t1) values(kStrips * t1 - 1, pb);
     for (; t < t1; ++t) convert_only(t);
   }
 
@@ -962,7 +970,7 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
     p.waves = D == 128 && longest > 1024 ? 8 : 4;
   }
   p.tile_rows = p.waves ? 32 * p.waves : kRowTile;
-  p.tile_tokens = p.waves ? 64 : kSpan;
+  p.tile_tokens = p.waves ? Prefill<128, 8>::kStage : kSpan;
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   const int64_t items = lists * p.row_tiles;
   const int64_t tiles = std::max<int64_t>(1, (longest + p.tile_tokens - 1) / p.tile_tokens);
@@ -1019,7 +1027,7 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
     auto prefill = [&](auto w) {
       using C = Prefill<D, decltype(w)::value>;
       hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves>), dim3((unsigned)p.blocks), dim3(C::kThreads),
-                         8 * 16 * C::kStrip, stream, a);
+                         4 * C::kStrips * 16 * C::kStrip, stream, a);
     };
     if constexpr (D == 128)
       if (p.waves == 8) prefill(std::integral_constant<int, 8>{});

@@ -296,6 +296,12 @@ CASES = [  # D, P, H, G, lens, counts
     (128, 32, 1, 1, [400], [130]),
     (128, 64, 2, 8, [260, 300], [33, 260]),
     (64, 32, 1, 71, [90], [2]),
+    # tables past 1024 tokens: the eight-wavefront tiles
+    (128, 64, 2, 4, [1500, 300, 1025], [200, 300, 64]),
+    (128, 32, 1, 8, [1090, 33], [700, 33]),
+    (128, 256, 1, 3, [2700], [90]),
+    (64, 128, 1, 2, [1300, 700], [140, 129]),
+    (256, 32, 1, 4, [1100], [40]),
 ]
 
 
