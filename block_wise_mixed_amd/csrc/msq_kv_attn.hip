@@ -974,10 +974,20 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   const int64_t items = lists * p.row_tiles;
   const int64_t tiles = std::max<int64_t>(1, (longest + p.tile_tokens - 1) / p.tile_tokens);
-  int64_t span;
+  int64_t span = tiles;
   if (p.waves) {
-    const int64_t want = std::max<int64_t>(1, 256 / items);
-    span = std::max<int64_t>(8, (tiles + want - 1) / want);
+    // Parts: the number that takes the least time, counted in tiles: rounds of
+    // workgroups over the GPU, each its tiles and 4 more to start and end; where
+    // there are several parts, 3 for the join's launch and their traffic
+    // (8 MB in the time of a tile).
+    const int64_t slots = D == 128 && p.waves == 4 ? 512 : D == 64 ? 768 : 256;
+    const double traffic = (double)s.total * t.q_heads * D * 8 / 8e6;
+    double least = 1e300;
+    for (int64_t n = 1; n <= std::min<int64_t>(kMostParts, tiles); ++n) {
+      const int64_t each = (tiles + n - 1) / n, rounds = (items * n + slots - 1) / slots;
+      const double cost = (double)rounds * (double)(each + 4) + (n > 1 ? 3 + traffic * (double)n : 0);
+      if (cost < least) least = cost, span = each;
+    }
   } else {
     // parts: about two workgroups a compute unit, each 4 to 256 tiles.  More and
     // smaller parts spend longer in their starts and joins (32 sequences of up
