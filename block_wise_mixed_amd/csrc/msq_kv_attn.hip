@@ -41,6 +41,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kNone = -1e30f;    // M before any token
 constexpr float kTop = 14.f;       // weights stay below 2^kTop
+constexpr float kTopWeight = 16384.f;  // 2^kTop
 constexpr float kPlace = 6.f;      // a moved M puts the largest weight at 2^kPlace
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -520,7 +521,7 @@ struct Prefill {
   static constexpr int kUnits = 4 * kStrips * D / kThreads;  // 16-byte pieces of keys and values a thread
   static constexpr int kStrip = 4 * D;             // 16-byte pieces of a strip in LDS
   static constexpr int kProducts = kSteps + 2 * kTiles;  // of a strip: keys, then values
-  static constexpr int kAhead = 4;                 // operands read from LDS before their product
+  static constexpr int kAhead = 2;                 // operands read from LDS before their product
 };
 
 template <int D, int W>
@@ -691,19 +692,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
       o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
           operand(i + 1, kSteps + v), p[v / kTiles], o[v % kTiles], 0, 0, 0);
   };
-  auto largest = [](const f32x16& s) {
-    float m = s[0];
-#pragma unroll
-    for (int e = 1; e < 16; ++e) m = fmaxf(m, s[e]);
-    return m;
-  };
-
-  // Strip i: its scores s, whose largest is top, -> weights p; scores sn of
-  // strip i + 1 and their largest; values of strip i - 1 by their weights pp.
-  // Lane (col, half), register e: row col, token 8 (e / 8) + 4 half + e % 4 +
-  // 16 (e / 4 % 2).
-  auto strip = [&](int i, f32x16& s, f32x16& sn, float& top, half8 (&p)[2], half8 (&pp)[2],
-                   auto which) {
+  // Strip i: its scores s -> weights p; scores sn of strip i + 1; values of strip
+  // i - 1 by their weights pp.  Lane (col, half), register e: row col, token
+  // 8 (e / 8) + 4 half + e % 4 + 16 (e / 4 % 2).
+  auto strip = [&](int i, f32x16& s, f32x16& sn, half8 (&p)[2], const half8 (&pp)[2], auto which) {
     constexpr int kWhich = decltype(which)::value;  // of its stage
     const int tok = 32 * i;
     const bool gone = __builtin_amdgcn_readlane(id0, i - batch) < 0;
@@ -715,20 +707,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
         const int at = tok + 8 * (e >> 3) + 4 * half + (e & 3) + 16 * ((e >> 2) & 1);
         if (at < my_lo || at >= my_hi || gone) s[e] = -INFINITY;
       }
-      top = largest(s);
-    }
-    float most = fmaf(top, f, lam);
-    if (__any(most > M + kTop)) {
-      most = fmaxf(most, __shfl_xor(most, 32));
-      // a power of two, so that the last strip's weights move exactly
-      const float m = most > M + kTop ? ceilf(most - kPlace) : M;
-      const float al = exp2_fast(M - m);
-      L *= al;
-#pragma unroll
-      for (int d = 0; d < kTiles; ++d) o[d] *= al;
-      pp[0] *= (_Float16)al;
-      pp[1] *= (_Float16)al;
-      M = m;
     }
     const float add = lam - M;
     float w[16], sum = 0.f;
@@ -746,7 +724,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     // A product, the read of a later one's operand, and a share of the vector
     // work at a time, in this order: the scheduler left to itself reads operands
     // right before their products and gathers the vector work at the end.
-    constexpr int kMax = D == 64 ? 2 : 4;  // the last products, beside the search of sn
 #pragma unroll
     for (int m = 0; m < kProducts; ++m) {
       const int v = m - kSteps;
@@ -777,18 +754,32 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
           if (u * kProducts / C::kUnits == m)
             load_one(st, i - 1 + 2 * kStrips + 1, i - 1 + 2 * kStrips - 1, u);
       }
-      if (m >= kProducts - kMax) {
-#pragma unroll
-        for (int e = 0; e < 16 / kMax; ++e) {
-          const float x = sn[16 / kMax * (m - kProducts + kMax) + e];
-          top = m == kProducts - kMax && e == 0 ? x : fmaxf(top, x);
-        }
-        asm volatile("" : "+v"(top));
-      }
       __builtin_amdgcn_sched_barrier(0);
     }
     use(14);
     use(15);
+    // Every weight is below 2^kTop unless some lane's sum is not (a sum of NaN is
+    // a row of NaN); only then is M moved and are the weights made again.
+    if (__any(sum > kTopWeight)) {
+      float most = s[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) most = fmaxf(most, s[e]);
+      most = fmaf(most, f, lam);
+      most = fmaxf(most, __shfl_xor(most, 32));
+      const float m = most > M + kPlace ? most - kPlace : M;
+      const float al = exp2_fast(M - m);
+      L *= al;
+#pragma unroll
+      for (int d = 0; d < kTiles; ++d) o[d] *= al;
+      M = m;
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = exp2_fast(fmaf(s[e], f, lam - M));
+        sum += x;
+        pairs[e >> 1][e & 1] = (_Float16)x;
+      }
+    }
     L = fmaf(sum, inv, L);
     asm volatile("" : "+v"(L));
 #pragma unroll
@@ -806,7 +797,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
       sa = __builtin_amdgcn_mfma_f32_32x32x16_f16(operand(i0 - 1, k), q[k], sa, 0, 0, 0);
-    float top = largest(sa);
     lds_barrier();  // the first stage's conversion takes the place of these keys
     auto next_batch = [&](int t) {
       if (kStrips * t - batch == 64) {
@@ -831,8 +821,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
       const int i = kStrips * t;
 #pragma unroll
       for (int m = 0; m < kAhead; ++m) fr[m] = operand(i, m);
-      strip(i, sa, sb, top, pa, pb, std::integral_constant<int, 0>{});
-      strip(i + 1, sb, sa, top, pb, pa, std::integral_constant<int, 1>{});
+      strip(i, sa, sb, pa, pb, std::integral_constant<int, 0>{});
+      strip(i + 1, sb, sa, pb, pa, std::integral_constant<int, 1>{});
       lds_barrier();
     }
     if (a1 >= t1) values(kStrips * t1 - 1, pb);
