@@ -574,49 +574,49 @@ def _kv_dtype(dtype) -> int:
 
 
 def _kv_rows(t, name, heads, dim, index):
-    """t as (tensor, address, token stride, head stride, type) of [rows][heads][dim] the kernels
-    can read: any token and head strides that are multiples of 16 bytes with contiguous dims;
-    anything else is copied."""
+    """t as (tensor, rows, address, token stride, head stride, type) of [rows][heads][dim] the
+    kernels can read: any token and head strides that are multiples of 16 bytes with contiguous
+    dims; anything else is copied."""
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [rows][{heads}][{dim}]")
     if t.get_device() != index:
         raise ValueError(f"{name} must be on the cache's device")
-    code = _kv_dtype(t.dtype)
+    code = _KV_DTYPE.get(t.dtype)
+    if code is None:
+        code = _kv_dtype(t.dtype)
     st, sh, sd = t.stride()
     at = t.data_ptr()
     per16 = 4 if code else 8
     if sd != 1 or st % per16 or sh % per16 or at % 16:
         t = t.clone(memory_format=_torch().contiguous_format)
         at, st, sh = t.data_ptr(), heads * dim, dim
-    return t, at, st, sh, code
+    return t, shape[0], at, st, sh, code
 
 
-def _kv_index(t, name, shape, index):
-    if t.dtype != _torch().int32 or t.shape != shape or t.get_device() != index:
-        raise ValueError(f"{name} must be int32 {list(shape)} on the cache's device")
+def _kv_index(t, name, count, index):
+    """t as a contiguous int32 tensor of count entries on the cache's device."""
+    if t.dtype is not _torch().int32 or t.dim() != 1 or t.numel() != count or t.get_device() != index:
+        raise ValueError(f"{name} must be int32 [{count}] on the cache's device")
     return t if t.is_contiguous() else t.contiguous()
 
 
 def _kv_seqs(cache: KVCache, block_table, offset, total: int, max_count: int):
     """(sequences struct, the tensors it points into)."""
     shape = block_table.shape
-    if len(shape) != 2 or shape[1] < 1:
-        raise ValueError("block_table must be int32 [batch][entries]")
+    if len(shape) != 2 or shape[1] < 1 or block_table.dtype is not _torch().int32 or \
+            block_table.get_device() != cache._index:
+        raise ValueError("block_table must be int32 [batch][entries] on the cache's device")
     batch, width = shape
-    block_table = _kv_index(block_table, "block_table", shape, cache._index)
-    if offset is not None:
-        offset = _kv_index(offset, "offset", (batch + 1,), cache._index)
-    elif total % max(batch, 1) or (batch == 0 and total):
-        raise ValueError("without offset every sequence has the same number of rows")
-    return (_KvSeqs(batch, width, block_table.data_ptr(),
-                    None if offset is None else offset.data_ptr(), total, max_count),
+    if not block_table.is_contiguous():
+        block_table = block_table.contiguous()
+    if offset is None:
+        if total % max(batch, 1) or (batch == 0 and total):
+            raise ValueError("without offset every sequence has the same number of rows")
+        return _KvSeqs(batch, width, block_table.data_ptr(), None, total, max_count), block_table
+    offset = _kv_index(offset, "offset", batch + 1, cache._index)
+    return (_KvSeqs(batch, width, block_table.data_ptr(), offset.data_ptr(), total, max_count),
             (block_table, offset))
-
-
-def _kv_here(index: int, stream) -> bool:
-    """Whether a call can go to the current stream of the current device as it is."""
-    return stream is None and _torch().cuda.current_device() == index
 
 
 def _kv_on(cache: KVCache, stream, tensors, call):
@@ -633,10 +633,6 @@ def _kv_on(cache: KVCache, stream, tensors, call):
     return result
 
 
-def _kv_stream(index: int) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(index)
-
-
 def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: int = 0,
              stream=None) -> None:
     """Quantise new tokens' keys and values into the cache (msq_kv_write).
@@ -646,20 +642,21 @@ def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: i
     which is the number of tokens it has in the cache (negative: leave the sequence out).
     offset: int32 [batch + 1], sequence b's rows are offset[b] .. offset[b + 1] - 1; None:
     rows / batch each.  max_count: the largest sequence's rows, if known (else all rows)."""
-    index = cache._index
-    if not _kv_here(index, stream):
+    index, cuda = cache._index, _torch()._C
+    if stream is not None or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (k, v, block_table, first, offset),
                       lambda: kv_write(cache, k, v, block_table, first, offset, max_count))
-    lib = load_library()
-    k, k_at, k_st, k_sh, code = _kv_rows(k, "k", cache.kv_heads, cache.head_dim, index)
-    v, v_at, v_st, v_sh, v_code = _kv_rows(v, "v", cache.kv_heads, cache.head_dim, index)
-    rows = k.shape[0]
-    if v.shape[0] != rows or v_code != code:
+    heads, dim = cache.kv_heads, cache.head_dim
+    k, rows, k_at, k_st, k_sh, code = _kv_rows(k, "k", heads, dim, index)
+    v, v_rows, v_at, v_st, v_sh, v_code = _kv_rows(v, "v", heads, dim, index)
+    if v_rows != rows or v_code != code:
         raise ValueError("k and v must have the same rows and type")
     s, keep = _kv_seqs(cache, block_table, offset, rows, max_count)
-    first = _kv_index(first, "first", (s.batch,), index)
-    _check(lib.msq_kv_write(cache._desc, s, first.data_ptr(), k_at, k_st, k_sh, v_at, v_st, v_sh,
-                            code, _kv_stream(index)), "msq_kv_write")
+    first = _kv_index(first, "first", s.batch, index)
+    status = load_library().msq_kv_write(cache._desc, s, first.data_ptr(), k_at, k_st, k_sh, v_at,
+                                         v_st, v_sh, code, cuda._cuda_getCurrentRawStream(index))
+    if status:
+        raise MsqError(status, "msq_kv_write")
 
 
 def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int] = None,
@@ -667,22 +664,23 @@ def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int
     """Read positions first[b] .. first[b] + rows - 1 of every sequence back (msq_kv_read):
     (k, v), [total][kv_heads][head_dim] of dtype (bf16 unless given; or fp32), code * scale.
     offset as in kv_write, total its last entry; with offset None, total / batch rows each."""
-    index = cache._index
-    if not _kv_here(index, stream):
+    index, cuda = cache._index, _torch()._C
+    if stream is not None or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (block_table, first, offset),
                       lambda: kv_read(cache, block_table, first, offset, total, max_count, dtype))
     torch = _torch()
-    lib = load_library()
     if total is None or total < 0:
         raise ValueError("total: the number of rows to read")
     s, keep = _kv_seqs(cache, block_table, offset, total, max_count)
-    first = _kv_index(first, "first", (s.batch,), index)
+    first = _kv_index(first, "first", s.batch, index)
     dtype = dtype or torch.bfloat16
     code = _kv_dtype(dtype)
     both = torch.empty((2, total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
     k, v = both.unbind(0)
-    _check(lib.msq_kv_read(cache._desc, s, first.data_ptr(), k.data_ptr(), v.data_ptr(), code,
-                           _kv_stream(index)), "msq_kv_read")
+    status = load_library().msq_kv_read(cache._desc, s, first.data_ptr(), k.data_ptr(),
+                                        v.data_ptr(), code, cuda._cuda_getCurrentRawStream(index))
+    if status:
+        raise MsqError(status, "msq_kv_read")
     return k, v
 
 
@@ -712,8 +710,8 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     unless out or out_dtype says fp32), with return_lse also the fp32 [rows][q_heads] natural
     log of each row's softmax denominator.  A query that sees nothing gives zeros and -inf.
     workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
-    index = cache._index
-    if not _kv_here(index, stream):
+    index, cuda = cache._index, _torch()._C
+    if stream is not None or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (q, block_table, kv_len, offset, out, workspace),
                       lambda: kv_attention(q, cache, block_table, kv_len, offset, max_count,
                                            max_kv_len, scale, causal, window, out, out_dtype,
@@ -722,11 +720,10 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     lib = load_library()
     if q.dim() != 3:
         raise ValueError("q must be [rows][q_heads][head_dim]")
-    heads, dim = q.shape[1], cache.head_dim
-    q, q_at, q_st, q_sh, q_code = _kv_rows(q, "q", heads, dim, index)
-    rows = q.shape[0]
+    heads, dim = q.size(1), cache.head_dim
+    q, rows, q_at, q_st, q_sh, q_code = _kv_rows(q, "q", heads, dim, index)
     s, keep = _kv_seqs(cache, block_table, offset, rows, max_count)
-    kv_len = _kv_index(kv_len, "kv_len", (s.batch,), index)
+    kv_len = _kv_index(kv_len, "kv_len", s.batch, index)
     if out is None:
         out = torch.empty((rows, heads, dim), dtype=out_dtype or torch.bfloat16, device=cache.device)
     elif out.shape != (rows, heads, dim) or not out.is_contiguous() or out.get_device() != index or \
@@ -741,7 +738,9 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the cache's device")
-    _check(lib.msq_kv_attention(cache._desc, s, a, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _kv_stream(index)),
-           "msq_kv_attention")
+    status = lib.msq_kv_attention(cache._desc, s, a, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(),
+                                  cuda._cuda_getCurrentRawStream(index))
+    if status:
+        raise MsqError(status, "msq_kv_attention")
     return (out, lse) if return_lse else out

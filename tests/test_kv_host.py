@@ -143,7 +143,7 @@ def test_binding_refuses(lib):
     assert c.nbytes == 2 * 4 * 2 * 32 * 64 + 2 * 4 * 2 * 4
     x = torch.zeros(3, 2, 64)
     dev = -1
-    assert msq._kv_rows(x, "k", 2, 64, dev) == (x, x.data_ptr(), 128, 64, 1)
+    assert msq._kv_rows(x, "k", 2, 64, dev) == (x, 3, x.data_ptr(), 128, 64, 1)
     for bad in (x[:, :1], x[..., :32], x[0]):
         with pytest.raises(ValueError):
             msq._kv_rows(bad, "k", 2, 64, dev)
