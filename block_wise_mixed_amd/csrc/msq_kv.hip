@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "msq.h"
 #include "msq_kv.h"
@@ -180,13 +181,14 @@ struct WriteArgs {
   int reach;
 };
 
-// Workgroup of block_tokens / 32 wavefronts.  HBM bound on long runs (each
-// value is read once and kept in registers between the maximum and the
-// coding); a call of single tokens is a chain of four dependent loads.
-template <int D, typename T>
-__global__ __launch_bounds__(512) void k_kv_write(WriteArgs a) {
-  using Mp = Map<D>;
-  __shared__ float part_max[8];
+// A wavefront takes 32 slots x E dims (64 where the workgroup's 16 wavefronts
+// allow it).  HBM bound on long runs (each value is read once and kept in
+// registers between the maximum and the coding); a call of single tokens is a
+// chain of four dependent loads.
+template <int D, int E, typename T>
+__global__ __launch_bounds__(1024) void k_kv_write(WriteArgs a) {
+  using Mp = Map<E>;
+  __shared__ float part_max[16];
   const Task tk = task_of(blockIdx.x, a.c.H, a.reach);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -206,14 +208,14 @@ __global__ __launch_bounds__(512) void k_kv_write(WriteArgs a) {
   const int64_t row = (int64_t)row0 + base - f;  // row of slot 0
   const int64_t hb = (int64_t)id * a.c.H + tk.h;
   float* scale = (tk.values ? a.c.vs : a.c.ks) + hb;
-  const int s0 = 32 * wave;
+  const int s0 = 32 * (wave / (D / E)), first_part = wave % (D / E) * (E / 8);
   uint8_t* codes = (tk.values ? a.c.vc : a.c.kc) + (hb * P + s0) * D;
   const T* src = reinterpret_cast<const T*>(tk.values ? a.v : a.k) +
                  tk.h * (tk.values ? a.vhs : a.khs);
   const int64_t ts = tk.values ? a.vts : a.kts;
   const float old = lo > 0 ? *scale : 0.f;
 
-  const int part = Mp::part(lane);
+  const int here = Mp::part(lane), part = first_part + here;
   Raw8<T> raw[Mp::kRows];
 #pragma unroll
   for (int u = 0; u < Mp::kRows; ++u) {
@@ -248,13 +250,13 @@ __global__ __launch_bounds__(512) void k_kv_write(WriteArgs a) {
 #pragma unroll
   for (int u = 0; u < Mp::kRows; ++u) {
     const int in = Mp::row(lane, u), slot = s0 + in;
-    uint2* at = reinterpret_cast<uint2*>(codes + Mp::key_byte(in, part));
+    uint2* at = reinterpret_cast<uint2*>(codes + Map<D>::key_byte(in, part));
     if (slot >= lo && slot < hi) {
       float x[8];
       raw[u].get(x);
       const uint2 q = kv_codes8(x, s, inv);
       if (tk.values)
-        *reinterpret_cast<uint2*>(image + in * Mp::kStride + 8 * part) = q;
+        *reinterpret_cast<uint2*>(image + in * Mp::kStride + 8 * here) = q;
       else
         *at = q;
     } else if (grown && slot < lo && !tk.values) {
@@ -291,7 +293,7 @@ __global__ __launch_bounds__(512) void k_kv_write(WriteArgs a) {
 #pragma unroll
       for (int d = 0; d < 4; ++d) w[d][i] = out[d];
     }
-    uint4* at = reinterpret_cast<uint4*>(codes + 1024 * (cq >> 2)) + 4 * (cq & 3) + 16 * g;
+    uint4* at = reinterpret_cast<uint4*>(codes + 1024 * ((first_part + cq) >> 2)) + 4 * (cq & 3) + 16 * g;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       if (!all) {
@@ -414,28 +416,29 @@ int64_t reach_of(const KvSeqsView& s, int shift) {
   return (n + P - 2) / P + 1;
 }
 
-template <template <int, typename> class Launch, typename Args>
-hipError_t dispatch(int D, int dtype, dim3 grid, dim3 block, hipStream_t stream, const Args& a) {
-  const bool f32 = dtype == MSQ_DTYPE_F32;
-  switch (D) {
-    case 64: f32 ? Launch<64, float>::go(grid, block, stream, a) : Launch<64, uint16_t>::go(grid, block, stream, a); break;
-    case 128: f32 ? Launch<128, float>::go(grid, block, stream, a) : Launch<128, uint16_t>::go(grid, block, stream, a); break;
-    default: f32 ? Launch<256, float>::go(grid, block, stream, a) : Launch<256, uint16_t>::go(grid, block, stream, a); break;
-  }
-  return hipGetLastError();
+template <int D, typename T>
+void launch_write(unsigned blocks, const WriteArgs& a, hipStream_t stream) {
+  const int strips = 1 << (a.c.shift - 5);
+  auto go = [&](auto dims) {
+    constexpr int E = decltype(dims)::value;
+    const int waves = strips * (D / E);
+    hipLaunchKernelGGL((k_kv_write<D, E, T>), dim3(blocks), dim3(64 * waves),
+                       waves * Map<E>::kImage, stream, a);
+  };
+  // More wavefronts shorten the coding of a run (2011 tokens of 8 heads of 128:
+  // 10.7 -> 7.9 us) and idle where a block gets a token or two (256 single
+  // tokens: 10.9 -> 14.4 us).
+  if (a.s.max_count >= 16 && strips * (D / 64) <= 16)
+    go(std::integral_constant<int, 64>{});
+  else
+    go(std::integral_constant<int, D < 128 ? 64 : 128>{});
 }
 template <int D, typename T>
-struct LaunchWrite {
-  static void go(dim3 grid, dim3 block, hipStream_t stream, const WriteArgs& a) {
-    hipLaunchKernelGGL((k_kv_write<D, T>), grid, block, block.x / 64 * Map<D>::kImage, stream, a);
-  }
-};
-template <int D, typename T>
-struct LaunchRead {
-  static void go(dim3 grid, dim3 block, hipStream_t stream, const ReadArgs& a) {
-    hipLaunchKernelGGL((k_kv_read<D, T>), grid, block, block.x / 64 * Map<D>::kImage, stream, a);
-  }
-};
+void launch_read(unsigned blocks, const ReadArgs& a, hipStream_t stream) {
+  const int waves = 1 << (a.c.shift - 5);
+  hipLaunchKernelGGL((k_kv_read<D, T>), dim3(blocks), dim3(64 * waves), waves * Map<D>::kImage,
+                     stream, a);
+}
 
 }  // namespace
 
@@ -533,9 +536,14 @@ extern "C" msq_status msq_kv_write(const msq_kv_cache* cache, const msq_kv_seqs*
   a.vts = v_token_stride;
   a.vhs = v_head_stride;
   a.reach = (int)reach;
-  const hipError_t e = dispatch<LaunchWrite>(cache->head_dim, dtype, dim3((unsigned)blocks),
-                                             dim3(2u << a.c.shift), stream, a);
-  return e == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
+  const bool f32 = dtype == MSQ_DTYPE_F32;
+  const unsigned n = (unsigned)blocks;
+  switch (cache->head_dim) {
+    case 64: f32 ? launch_write<64, float>(n, a, stream) : launch_write<64, uint16_t>(n, a, stream); break;
+    case 128: f32 ? launch_write<128, float>(n, a, stream) : launch_write<128, uint16_t>(n, a, stream); break;
+    default: f32 ? launch_write<256, float>(n, a, stream) : launch_write<256, uint16_t>(n, a, stream); break;
+  }
+  return hipGetLastError() == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
 }
 
 extern "C" msq_status msq_kv_read(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
@@ -549,7 +557,12 @@ extern "C" msq_status msq_kv_read(const msq_kv_cache* cache, const msq_kv_seqs* 
   a.k = k;
   a.v = v;
   a.reach = (int)reach;
-  const hipError_t e = dispatch<LaunchRead>(cache->head_dim, dtype, dim3((unsigned)blocks),
-                                            dim3(2u << a.c.shift), stream, a);
-  return e == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
+  const bool f32 = dtype == MSQ_DTYPE_F32;
+  const unsigned n = (unsigned)blocks;
+  switch (cache->head_dim) {
+    case 64: f32 ? launch_read<64, float>(n, a, stream) : launch_read<64, uint16_t>(n, a, stream); break;
+    case 128: f32 ? launch_read<128, float>(n, a, stream) : launch_read<128, uint16_t>(n, a, stream); break;
+    default: f32 ? launch_read<256, float>(n, a, stream) : launch_read<256, uint16_t>(n, a, stream); break;
+  }
+  return hipGetLastError() == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
 }

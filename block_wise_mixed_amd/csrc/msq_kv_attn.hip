@@ -985,7 +985,7 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
     // 131072: 16, 32, 64 parts 191, 205, 206 us), one a compute unit
     // leaves it idle behind the short sequences (46 us)
     const int64_t want = std::max<int64_t>(1, 512 / items);
-    span = std::min<int64_t>(std::max<int64_t>(4, (tiles + want - 1) / want), 256);
+    span = std::min<int64_t>(std::max<int64_t>(tiles <= 12 ? 12 : 4, (tiles + want - 1) / want), 256);
   }
   p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, kMostParts);
   p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
