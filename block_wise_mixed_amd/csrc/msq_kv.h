@@ -9,6 +9,8 @@
 
 namespace msq {
 
+constexpr int64_t kMostThreads = 0xFFFFFFFF;  // of one launch
+
 // Cache and sequences as the kernels take them.
 struct KvCacheView {
   uint8_t *kc, *vc;

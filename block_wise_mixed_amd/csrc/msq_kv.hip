@@ -454,7 +454,8 @@ msq_status kv_views(const msq_kv_cache* cache, const msq_kv_seqs* seqs, KvCacheV
   while (shift < 8 && (1 << shift) != cache->block_tokens) ++shift;
   if ((1 << shift) != cache->block_tokens) return MSQ_ERR_UNSUPPORTED;
   if (seqs->batch < 0 || seqs->total < 0 || seqs->total > most || seqs->table_width < 1 ||
-      (int64_t)seqs->table_width * cache->block_tokens > most || seqs->max_count < 0)
+      (int64_t)seqs->table_width * cache->block_tokens > ((int64_t)1 << 30) ||
+      seqs->max_count < 0)
     return MSQ_ERR_SHAPE;
   if (!seqs->offset && (seqs->batch == 0 ? seqs->total != 0 : seqs->total % seqs->batch != 0))
     return MSQ_ERR_SHAPE;
@@ -506,7 +507,8 @@ msq_status kv_common(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const i
     return MSQ_ERR_INVALID_ARG;
   *reach = reach_of(s, c.shift);
   const int64_t lists = (int64_t)s.batch * *reach;  // < 2^31 * 2^27
-  if (lists > (int64_t)0x7FFFFFFF / 2 / c.H) return MSQ_ERR_SHAPE;
+  // workgroups of up to 1024 threads; a launch holds fewer than 2^32
+  if (lists > kMostThreads / 1024 / 2 / c.H) return MSQ_ERR_SHAPE;
   *blocks = lists * 2 * c.H;
   return MSQ_OK;
 }

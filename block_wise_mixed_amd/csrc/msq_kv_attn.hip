@@ -990,10 +990,10 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, kMostParts);
   p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
   p.blocks = items * p.nsplit;
-  if (p.blocks > (int64_t)0x7FFFFFFF) return MSQ_ERR_SHAPE;
+  if (p.blocks > kMostThreads / 512) return MSQ_ERR_SHAPE;
   if (p.nsplit > 1) {
     // the join's grid: (sequence, row, head)
-    if ((int64_t)s.batch * s.max_count * G > (int64_t)0x7FFFFFFF / c.H) return MSQ_ERR_SHAPE;
+    if ((int64_t)s.batch * s.max_count * G > kMostThreads / 256 / c.H) return MSQ_ERR_SHAPE;
     const size_t rows = (size_t)s.total * t.q_heads * p.nsplit;
     p.ml_at = (rows * D * 4 + 255) / 256 * 256;
     p.workspace = p.ml_at + rows * 8;

@@ -418,12 +418,13 @@ typedef struct {
 typedef struct {
   int32_t batch;              /* sequences, >= 0 */
   int32_t table_width;        /* block-table entries per sequence, >= 1;
-                                 table_width * block_tokens < 2^31 */
+                                 table_width * block_tokens <= 2^30 */
   const int32_t *block_table; /* [batch][table_width] */
   const int32_t *offset;      /* [batch + 1], non-decreasing, or null */
   int64_t total;              /* rows of all sequences, 0 .. 2^31 - 1 */
   int32_t max_count;          /* at least the largest sequence's rows; rows past it are not
-                                 processed.  0: total.  Ignored with a null offset */
+                                 processed.  0: total.  Ignored with a null offset.  Launches
+                                 are sized by batch * max_count: give it for ragged batches */
 } msq_kv_seqs;
 
 /* Quantises k and v rows into the cache: row i of sequence b goes to position
@@ -432,8 +433,10 @@ typedef struct {
  * of dtype, with token and head strides in elements (dims contiguous; 16-byte
  * aligned pointers and byte strides).  One launch, asynchronous.
  * Errors: MSQ_ERR_INVALID_ARG (null or misaligned pointer, unknown dtype),
- * MSQ_ERR_SHAPE (a size outside the ranges above), MSQ_ERR_UNSUPPORTED
- * (head_dim or block_tokens not listed above), MSQ_ERR_HIP. */
+ * MSQ_ERR_SHAPE (a size outside the ranges above, or batch * kv_heads *
+ * blocks of max_count rows past what one launch takes, 2^21),
+ * MSQ_ERR_UNSUPPORTED (head_dim or block_tokens not listed above),
+ * MSQ_ERR_HIP. */
 msq_status msq_kv_write(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
                         const void *k, int64_t k_token_stride, int64_t k_head_stride,
                         const void *v, int64_t v_token_stride, int64_t v_head_stride,
@@ -479,6 +482,7 @@ size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_
  * value gives NaN.  Products run on the f16 matrix instructions: codes are
  * exact there, the query row is scaled by a power of two and the softmax
  * weights are rounded to f16; scores, softmax statistics and sums are fp32.
+ * Rows outside every sequence are left as they are.
  * workspace: msq_kv_attention_workspace_bytes, 256-byte aligned; calls that
  * share one must be ordered on one stream.  One launch, and one more to join
  * the parts where a sequence's tokens are split over workgroups.  Errors as
