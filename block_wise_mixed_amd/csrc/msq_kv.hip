@@ -31,8 +31,17 @@ template <>
 struct Raw8<uint16_t> {
   uint4 v;
   __device__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
-  // forget the widened values: they are made again, in half the registers
-  __device__ void narrow() { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+  // the larger of m and the magnitudes, as bit patterns: two in the halves of a word
+  __device__ uint32_t most(uint32_t m) const {
+    typedef uint16_t pair __attribute__((ext_vector_type(2)));
+    pair r = __builtin_bit_cast(pair, m);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r = __builtin_elementwise_max(r, __builtin_bit_cast(pair, w[i] & 0x7FFF7FFFu));
+    return __builtin_bit_cast(uint32_t, r);
+  }
+  __device__ static float widen(uint32_t m) { return __uint_as_float(max(m << 16, m & 0xFFFF0000u)); }
   __device__ void get(float* x) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -49,7 +58,13 @@ struct Raw8<float> {
     a = *reinterpret_cast<const float4*>(p);
     b = *reinterpret_cast<const float4*>(p + 4);
   }
-  __device__ void narrow() {}
+  __device__ uint32_t most(uint32_t m) const {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ static float widen(uint32_t m) { return __uint_as_float(m); }
   __device__ void get(float* x) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
@@ -78,23 +93,21 @@ __device__ inline uint32_t kv_recode(uint32_t u, float old, float s) {
 // Codes of eight values.  inv > 0: a reciprocal of s (v_rcp_f32, 1 ulp) that
 // may stand in for the division: t = x * inv and fl(x / s) are within 127 *
 // (1.5 * 2^-23 + 2^-24) < 2^-15 of each other, so they round to the same code
-// unless t is within 2^-14 of a half-integer; then, and for a NaN, the lane
-// divides.  The rounding is an addition of 1.5 * 2^23, which leaves code + 128
-// in the low byte.
+// unless t is within 2^-14 of a half-integer; then the lane divides.  (inv is 0
+// where s is out of range or the lane has a NaN.)  The rounding is an addition
+// of 1.5 * 2^23, which leaves code + 128 in the low byte.
 __device__ inline uint2 kv_codes8(const float* x, float s, float inv) {
   constexpr float kMagic = 12582912.f + 128.f;
   uint32_t m[8], w[2];
   float off = 0.f;
-  bool nan = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = fminf(fmaxf(x[i] * inv, -127.f), 127.f);
+    const float t = __builtin_amdgcn_fmed3f(x[i] * inv, -127.f, 127.f);
     const float r = t + kMagic;
     off = fmaxf(off, fabsf(t - (r - kMagic)));
-    nan |= x[i] != x[i];
     m[i] = __float_as_uint(r);
   }
-  if (!(inv > 0.f) || nan || off > 0.5f - 0x1p-14f) {
+  if (!(inv > 0.f) || off > 0.5f - 0x1p-14f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) m[i] = kv_code(x[i], s);
   }
@@ -222,16 +235,25 @@ __global__ __launch_bounds__(1024) void k_kv_write(WriteArgs a) {
     const int slot = s0 + Mp::row(lane, u);
     if (slot >= lo && slot < hi) raw[u].load(src + (row + slot) * ts + 8 * part);
   }
-  float amax = 0.f;
+  uint32_t most = 0;
 #pragma unroll
   for (int u = 0; u < Mp::kRows; ++u) {
     const int slot = s0 + Mp::row(lane, u);
-    if (slot >= lo && slot < hi) {
-      float x[8];
-      raw[u].get(x);
+    if (slot >= lo && slot < hi) most = raw[u].most(most);
+  }
+  float amax = Raw8<T>::widen(most);
+  const bool finite = amax <= kFinite;  // all of this lane's values
+  if (!finite) {
+    amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[i]));
-      raw[u].narrow();
+    for (int u = 0; u < Mp::kRows; ++u) {
+      const int slot = s0 + Mp::row(lane, u);
+      if (slot >= lo && slot < hi) {
+        float x[8];
+        raw[u].get(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(x[i]));
+      }
     }
   }
   amax = wave_max(amax);
@@ -244,7 +266,7 @@ __global__ __launch_bounds__(1024) void k_kv_write(WriteArgs a) {
   const bool grown = lo > 0 && s > old;
   if (lo > 0 && !grown) s = old;
   if (threadIdx.x == 0 && (lo == 0 || grown)) *scale = s;
-  const float inv = s > 1e-30f && s < 1e30f ? __builtin_amdgcn_rcpf(s) : 0.f;
+  const float inv = finite && s > 1e-30f && s < 1e30f ? __builtin_amdgcn_rcpf(s) : 0.f;
 
   uint8_t* image = smem_codes + wave * Mp::kImage;
 #pragma unroll
