@@ -149,14 +149,13 @@ __device__ inline float wave_max(float v) {
 struct Task {
   int b, j, h, values;
 };
-__device__ inline Task task_of(int64_t id, int H, int reach) {
+__device__ inline Task task_of(unsigned id, unsigned H, unsigned reach) {
   Task t;
-  t.h = (int)(id % H);
-  id /= H;
-  t.values = (int)(id & 1);
-  id >>= 1;
-  t.j = (int)(id % reach);
-  t.b = (int)(id / reach);
+  const unsigned list = id / H, seq = list / 2 / reach;
+  t.h = (int)(id - list * H);
+  t.values = (int)(list & 1);
+  t.j = (int)(list / 2 - seq * reach);
+  t.b = (int)seq;
   return t;
 }
 

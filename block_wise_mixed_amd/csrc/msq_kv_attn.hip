@@ -66,7 +66,7 @@ struct AttnArgs {
   int Hq, G, q_f32, out_f32, causal, window;
   int nsplit;      // workgroups along a row tile's tokens
   int span_tiles;  // tiles of one such part (more where nsplit parts cannot cover the range)
-  int row_tiles, tile_rows, tile_tokens;
+  int row_tiles, tile_rows, tile_shift;  // tiles of tile_rows x 2^tile_shift tokens
   float c2;        // scale * log2 e
 };
 
@@ -126,14 +126,16 @@ __device__ inline void row_scale(float amax, bool bad, float& up, float& down) {
   down = ldexpf(1.f, -e);
 }
 
-// The positions lo <= t < hi that row i of n of a sequence with len tokens sees.
+// The positions lo <= t < hi that row i of n of a sequence with len tokens sees
+// (len <= 2^30; 32-bit numbers and unsigned divisions here and below: the
+// kernels start with a chain of them).
 __device__ inline void row_range(int len, int n, int i, int causal, int window, int& lo, int& hi) {
   lo = 0;
   hi = len;
   if (causal) {
-    const int64_t pos = (int64_t)len - n + i;
-    hi = (int)max(min(pos + 1, (int64_t)len), (int64_t)0);
-    if (window > 0) lo = (int)max(pos - window + 1, (int64_t)0);
+    const int pos = len - n + i;
+    hi = max(pos + 1, 0);
+    if (window > 0 && pos >= window) lo = pos - window + 1;
   }
 }
 
@@ -177,23 +179,47 @@ __device__ inline float2 get2(const uint64_t* p) {
 }
 
 // The tiles of a part: query rows r0 .. of a sequence with n * G rows see the
-// tokens lo .. hi - 1 between them, cut into tiles of tile_tokens and those
+// tokens lo .. hi - 1 between them, cut into tiles and those
 // into parts of the same number of tiles.
 struct Parts {
   int lo, hi;          // of all rows together
   int lo_last, hi_first;  // tokens from lo_last to hi_first are seen by every row
   int first, end;      // tiles
-  int span;            // tiles per part
+  int span, parts;     // tiles per part, parts that have tiles
 };
-__device__ inline Parts parts_of(const AttnArgs& a, int len, int n, int64_t r0) {
+__device__ inline int over(int x, int y) { return (int)((unsigned)x / (unsigned)y); }
+__device__ inline Parts parts_of(const AttnArgs& a, int len, int n, int r0) {
   Parts p;
-  const int64_t rows = (int64_t)n * a.G;
-  const int i0 = (int)(r0 / a.G), i1 = (int)(min(r0 + a.tile_rows, rows) - 1) / a.G;
-  row_range(len, n, i0, a.causal, a.window, p.lo, p.hi_first);
-  row_range(len, n, i1, a.causal, a.window, p.lo_last, p.hi);
-  p.first = p.lo / a.tile_tokens;
-  p.end = max(p.first, (int)(((int64_t)p.hi + a.tile_tokens - 1) / a.tile_tokens));
-  p.span = max(a.span_tiles, (p.end - p.first + a.nsplit - 1) / a.nsplit);
+  const int last = min(r0 + a.tile_rows, n * a.G) - 1;
+  row_range(len, n, over(r0, a.G), a.causal, a.window, p.lo, p.hi_first);
+  row_range(len, n, over(last, a.G), a.causal, a.window, p.lo_last, p.hi);
+  p.first = p.lo >> a.tile_shift;
+  p.end = max(p.first, (p.hi + (1 << a.tile_shift) - 1) >> a.tile_shift);
+  p.span = max(a.span_tiles, p.end - p.first);
+  p.parts = p.end > p.first ? 1 : 0;
+  if (a.nsplit > 1) {
+    p.span = max(a.span_tiles, over(p.end - p.first + a.nsplit - 1, a.nsplit));
+    p.parts = over(p.end - p.first + p.span - 1, p.span);
+  }
+  return p;
+}
+
+// Workgroup n = ((high * lows + low) * parts + part) * H + h.
+struct Place {
+  int h, part, low, high;
+};
+__device__ inline Place place_of(int H, int parts, int lows) {
+  Place p;
+  int n = blockIdx.x, m = over(n, H);
+  p.h = n - m * H;
+  p.part = 0;
+  if (parts > 1) {
+    n = m;
+    m = over(n, parts);
+    p.part = n - m * parts;
+  }
+  p.high = over(m, lows);
+  p.low = m - p.high * lows;
   return p;
 }
 
@@ -240,29 +266,24 @@ template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
   constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
   constexpr int kStride = D + 4;
-  int64_t wg = blockIdx.x;
-  const int h = (int)(wg % a.c.H);
-  wg /= a.c.H;
-  const int sp = (int)(wg % a.nsplit);
-  wg /= a.nsplit;
-  const int tile_row = (int)(wg % a.row_tiles), b = (int)(wg / a.row_tiles);
+  const Place at_wg = place_of(a.c.H, a.nsplit, a.row_tiles);
+  const int h = at_wg.h, sp = at_wg.part, tile_row = at_wg.low, b = at_wg.high;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
+  const int len = clamped_len(a, b);
   int row0, n;
   kv_rows(a.s, b, row0, n);
-  const int64_t rows = (int64_t)n * a.G;
-  const int64_t r0 = (int64_t)tile_row * kRowTile;
+  const int rows = n * a.G, r0 = tile_row * kRowTile;
   if (r0 >= rows) return;
-  const int len = clamped_len(a, b);
   const Parts pt = parts_of(a, len, n, r0);
   const int lo1 = pt.lo_last, hi0 = pt.hi_first;
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
-  const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;  // that have tiles
+  const int parts = pt.parts;
   // rows that see nothing are left to the first part, or to the join launch
   if (t0 >= t1 && a.nsplit > 1 && !(a.tags && parts == 0 && sp == 0)) return;
 
-  const int64_t r = min(r0 + col, rows - 1);
-  const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
+  const int r = min(r0 + col, rows - 1);
+  const int i = over(r, a.G), hq = h * a.G + r - i * a.G;
   int my_lo, my_hi;
   row_range(len, n, i, a.causal, a.window, my_lo, my_hi);
 
@@ -416,9 +437,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[e] += f * lo_o[(w * 16 + rr) * kStride + d0 + e];
   }
-  const int64_t ro = min(r0 + rr, rows - 1);
-  const int io = (int)(ro / a.G);
-  const int64_t orow = (int64_t)(row0 + io) * a.Hq + h * a.G + (int)(ro - (int64_t)io * a.G);
+  const int ro = min(r0 + rr, rows - 1);
+  const int io = over(ro, a.G);
+  const int64_t orow = (int64_t)(row0 + io) * a.Hq + h * a.G + ro - io * a.G;
   const int64_t step = (int64_t)a.s.total * a.Hq;
   const bool mine = r0 + rr < rows;
   if (a.tags ? parts > 1 : a.nsplit > 1) {
@@ -530,29 +551,24 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
   constexpr int kProducts = C::kProducts, kAhead = C::kAhead, kStrips = C::kStrips;
   constexpr int kRing = 2 * kStrips, kBatch = 64 / kStrips;
-  int64_t wg = blockIdx.x;
-  const int h = (int)(wg % a.c.H);
-  wg /= a.c.H;
-  const int sp = (int)(wg % a.nsplit);
-  wg /= a.nsplit;
-  const int b = (int)(wg % a.s.batch);
-  const int tile_row = a.row_tiles - 1 - (int)(wg / a.s.batch);  // the longest rows first
+  const Place at_wg = place_of(a.c.H, a.nsplit, a.s.batch);
+  const int h = at_wg.h, sp = at_wg.part, b = at_wg.low;
+  const int tile_row = a.row_tiles - 1 - at_wg.high;  // the longest rows first
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   const int len = clamped_len(a, b);
   int row0, n;
   kv_rows(a.s, b, row0, n);
-  const int64_t rows = (int64_t)n * a.G;
-  const int64_t r0 = (int64_t)tile_row * C::kRows;
+  const int rows = n * a.G, r0 = tile_row * C::kRows;
   if (r0 >= rows) return;
   const Parts pt = parts_of(a, len, n, r0);
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   if (t0 >= t1 && a.nsplit > 1) return;
 
   // this wavefront's rows (past the end: the last row again, never written)
-  const int64_t w0 = r0 + 32 * wave;
-  const int64_t r = min(w0 + col, rows - 1);
-  const int i = (int)(r / a.G), hq = h * a.G + (int)(r - (int64_t)i * a.G);
+  const int w0 = r0 + 32 * wave;
+  const int r = min(w0 + col, rows - 1);
+  const int i = over(r, a.G), hq = h * a.G + r - i * a.G;
   Raw8 qraw[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s)
@@ -560,12 +576,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   int my_lo, my_hi;
   row_range(len, n, i, a.causal, a.window, my_lo, my_hi);
   int w_lo, w_hi, w_lo_last, w_hi_first;
-  row_range(len, n, (int)(min(w0, rows - 1) / a.G), a.causal, a.window, w_lo, w_hi_first);
-  row_range(len, n, (int)(min(w0 + 31, rows - 1) / a.G), a.causal, a.window, w_lo_last, w_hi);
+  row_range(len, n, over(min(w0, rows - 1), a.G), a.causal, a.window, w_lo, w_hi_first);
+  row_range(len, n, over(min(w0 + 31, rows - 1), a.G), a.causal, a.window, w_lo_last, w_hi);
   if (w0 >= rows) w_hi = 0;
   // its stages: a0 .. a1 - 1 (none: a0 == a1)
   const int a0 = min(max(t0, w_lo / kStage), t1);
-  const int a1 = max(a0, min(t1, (int)(((int64_t)w_hi + kStage - 1) / kStage)));
+  const int a1 = max(a0, min(t1, (w_hi + kStage - 1) / kStage));
 
   f32x16 o[kTiles];
 #pragma unroll
@@ -868,15 +884,16 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
   const int mine = kWaves == 4 ? wave : 0;
   const int id = kWaves == 4 ? blockIdx.x : 4 * blockIdx.x + wave;
   if (id >= rows) return;
-  const int hq = id % a.Hq, i = id / a.Hq % a.s.max_count, b = id / a.Hq / a.s.max_count;
+  const int row = over(id, a.Hq), hq = id - row * a.Hq, b = over(row, a.s.max_count);
+  const int i = row - b * a.s.max_count;
   int row0, n;
   kv_rows(a.s, b, row0, n);
   if (i >= n) return;
   const int len = clamped_len(a, b);
   // the row tile this row was in, as the split kernel saw it
-  const int r = i * a.G + hq % a.G;
-  const Parts pt = parts_of(a, len, n, r / a.tile_rows * a.tile_rows);
-  const int parts = (pt.end - pt.first + pt.span - 1) / pt.span;
+  const int r = i * a.G + hq - over(hq, a.G) * a.G;
+  const Parts pt = parts_of(a, len, n, over(r, a.tile_rows) * a.tile_rows);
+  const int parts = pt.parts;
   const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq, step = (int64_t)a.s.total * a.Hq;
   const float2 ml = lane < parts ? a.part_ml[lane * step + orow] : make_float2(kNone, 0.f);
   const int each = (parts + kWaves - 1) / kWaves, p1 = min(parts, (mine + 1) * each);
@@ -1107,12 +1124,12 @@ extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_s
   a.q_f32 = t.q_dtype == MSQ_DTYPE_F32;
   a.out_f32 = t.out_dtype == MSQ_DTYPE_F32;
   a.causal = t.causal != 0;
-  a.window = t.window;
+  a.window = std::min(t.window, 1 << 30);
   a.nsplit = p.nsplit;
   a.span_tiles = p.span_tiles;
   a.row_tiles = p.row_tiles;
   a.tile_rows = p.tile_rows;
-  a.tile_tokens = p.tile_tokens;
+  a.tile_shift = p.tile_tokens == 64 ? 6 : 5;
   a.c2 = (t.scale > 0.f ? t.scale : 1.f / std::sqrt((float)D)) * kLog2e;
   hipError_t e;
   switch (D) {
