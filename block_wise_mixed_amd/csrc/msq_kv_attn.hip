@@ -89,7 +89,7 @@ __device__ inline half8 codes_f16x8(uint32_t w0, uint32_t w1) {
   return r.h;
 }
 
-// Eight query values, as loaded and as fp32.
+// Eight query values as loaded.
 struct Raw8 {
   uint4 a, b;  // bf16: a only
 };
@@ -104,26 +104,67 @@ __device__ inline Raw8 load8(const void* q, int f32, int64_t at) {
   }
   return r;
 }
-__device__ inline void widen8(const Raw8& r, int f32, float* x) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = __uint_as_float(f32 ? w[i] : i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-    x[4 + i] = __uint_as_float(f32 ? w[4 + i] : i & 1 ? w[2 + (i >> 1)] & 0xFFFF0000u : w[2 + (i >> 1)] << 16);
-  }
-}
-
 // The power of two 2^e that the row is multiplied by, from its largest
 // magnitude (NaN if the row has a non-finite value), and its inverse.
 __device__ inline void row_scale(float amax, bool bad, float& up, float& down) {
   int e = 0;
-  if (amax > 0.f) {
+  if (amax > 0.f && !bad) {
     (void)frexpf(amax, &e);  // amax = m 2^e, 1/2 <= m < 1
     e = 15 - e;
   }
   e = min(max(e, -126), 126);
   up = bad ? __uint_as_float(0x7FC00000u) : ldexpf(1.f, e);
   down = ldexpf(1.f, -e);
+}
+
+// The f16 fragments of a query row, whose values the lanes lane ^ kFirst * m
+// hold between them, and the inverse of their scale.
+template <int N, int kFirst>
+__device__ inline void query_fragments(const Raw8 (&raw)[N], int f32, half8 (&q)[N], float& down) {
+  typedef uint16_t pair __attribute__((ext_vector_type(2)));
+  uint32_t most = 0;  // the largest magnitude, as an fp32 bit pattern
+  if (f32) {
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const uint32_t w[8] = {raw[s].a.x, raw[s].a.y, raw[s].a.z, raw[s].a.w,
+                             raw[s].b.x, raw[s].b.y, raw[s].b.z, raw[s].b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = max(most, w[e] & 0x7FFFFFFFu);
+    }
+  } else {
+    pair m = {0, 0};
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const uint32_t w[4] = {raw[s].a.x, raw[s].a.y, raw[s].a.z, raw[s].a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(pair, w[e] & 0x7FFF7FFFu));
+    }
+    most = (uint32_t)max(m[0], m[1]) << 16;
+  }
+#pragma unroll
+  for (int x = kFirst; x < 64; x <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, x));
+  float up;
+  row_scale(__uint_as_float(most), most >= 0x7F800000u, up, down);
+  if (f32) {
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const uint32_t w[8] = {raw[s].a.x, raw[s].a.y, raw[s].a.z, raw[s].a.w,
+                             raw[s].b.x, raw[s].b.y, raw[s].b.z, raw[s].b.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(__uint_as_float(w[e]) * up);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const uint32_t w[4] = {raw[s].a.x, raw[s].a.y, raw[s].a.z, raw[s].a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        q[s][2 * e] = (_Float16)(__uint_as_float(w[e] << 16) * up);
+        q[s][2 * e + 1] = (_Float16)(__uint_as_float(w[e] & 0xFFFF0000u) * up);
+      }
+    }
+  }
 }
 
 // The positions lo <= t < hi that row i of n of a sequence with len tokens sees
@@ -291,29 +332,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   half8 q[kSteps];
   float down;
   {
-    float x[kSteps][8], amax = 0.f;
-    bool bad = false;
-    const int64_t at = (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      widen8(load8(a.q, a.q_f32, at + 64 * (s >> 1) + 16 * g + 8 * (s & 1)), a.q_f32, x[s]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        amax = fmaxf(amax, fabsf(x[s][e]));
-        bad |= !(fabsf(x[s][e]) <= 3.402823466e38f);
-      }
-    }
-    amax = fmaxf(amax, __shfl_xor(amax, 16));
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
-    int nb = bad;
-    nb |= __shfl_xor(nb, 16);
-    nb |= __shfl_xor(nb, 32);
-    float up;
-    row_scale(amax, nb != 0, up, down);
+    Raw8 raw[kSteps];
+    const int64_t at = (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs + 16 * g;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(x[s][e] * up);
+      raw[s] = load8(a.q, a.q_f32, at + 64 * (s >> 1) + 8 * (s & 1));
+    query_fragments<kSteps, 16>(raw, a.q_f32, q, down);
   }
   const float cq = a.c2 * down;
 
@@ -650,30 +674,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   };
 
   half8 q[kSteps];  // slots (half, e) of step s are dims 16 s + 8 half + e
-  float cq;
-  {
-    float x[kSteps][8], amax = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) widen8(qraw[s], a.q_f32, x[s]);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        amax = fmaxf(amax, fabsf(x[s][e]));
-        bad |= !(fabsf(x[s][e]) <= 3.402823466e38f);
-      }
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
-    int nb = bad;
-    nb |= __shfl_xor(nb, 32);
-    float up, down;
-    row_scale(amax, nb != 0, up, down);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(x[s][e] * up);
-    cq = a.c2 * down;
-  }
+  float down;
+  query_fragments<kSteps, 32>(qraw, a.q_f32, q, down);
+  const float cq = a.c2 * down;
 
   // and from there as f16 into LDS: keys [strip][step][half][row], values
   // [strip][d tile][step][half][d], 16 bytes each
@@ -807,7 +810,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     half8 pa[2], pb[2];
     pa[0] = pa[1] = pb[0] = pb[1] = half8{};
     convert(st0, i0 - kStrips + 1, i0 - 1);
-    convert(st1, i0 + 1, i0 + kStrips - 1);
+#pragma unroll
+    for (int j = 0; j < C::kUnits; ++j) convert_half(st1, i0 + 1, 0, j >> 1, j & 1);
     lds_barrier();
     sa = f32x16{};
 #pragma unroll
