@@ -194,20 +194,6 @@ __device__ inline void write_row(const AttnArgs& a, int64_t at, int n, const flo
   }
 }
 
-__device__ inline void write4(const AttnArgs& a, int64_t at, const float* x) {
-  if (a.out_f32) {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
-  } else {
-    union {
-      __bf16 b[4];
-      uint2 u;
-    } o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.b[i] = (__bf16)x[i];
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) = o.u;
-  }
-}
-
 // Two floats at a time past the caches that the XCDs do not share.
 __device__ inline void put2(uint64_t* p, float x, float y, bool on) {
   if (on)
@@ -580,6 +566,16 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   const int tile_row = a.row_tiles - 1 - at_wg.high;  // the longest rows first
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
+  // Blocks of the strips: lane j holds that of the j-th strip of a batch of 64,
+  // read with vector loads two batches ahead (scalar loads would share their
+  // counter with the LDS reads, so that every stage waited for them).  The first
+  // ones are read from where the part begins unless it has a window or more
+  // tokens than the plan knew of, beside the lengths and not after them.
+  auto blocks_at = [&](int t) {  // of the batch that begins at stage t
+    return kv_block(a.c, a.s, b, ((int64_t)t * kStage + 32 * lane) >> a.c.shift);
+  };
+  const int guess = sp * a.span_tiles;
+  int id0 = blocks_at(guess), id1 = blocks_at(guess + kBatch), id2 = blocks_at(guess + 2 * kBatch);
   const int len = clamped_len(a, b);
   int row0, n;
   kv_rows(a.s, b, row0, n);
@@ -588,6 +584,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   const Parts pt = parts_of(a, len, n, r0);
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   if (t0 >= t1 && a.nsplit > 1) return;
+  if (t0 != guess) id0 = blocks_at(t0), id1 = blocks_at(t0 + kBatch), id2 = blocks_at(t0 + 2 * kBatch);
 
   // this wavefront's rows (past the end: the last row again, never written)
   const int w0 = r0 + 32 * wave;
@@ -612,16 +609,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   for (int d = 0; d < kTiles; ++d) o[d] = f32x16{};
   float M = kNone, L = 0.f;
 
-  // Blocks and scales of the strips: lane j holds those of the j-th strip of a
-  // batch of 64, read with vector loads one batch ahead (the blocks two ahead,
-  // since the scales need them).  Scalar loads would share their counter with
-  // the LDS reads, so that every stage waited for them.
+  // The strips' scales, held like their blocks and read a batch ahead.
   const int P = 1 << a.c.shift;
   struct Scales {
     float sk, lam, inv;  // keys' scale; values': log2 and inverse
-  };
-  auto blocks_at = [&](int t) {  // of the batch that begins at stage t
-    return kv_block(a.c, a.s, b, ((int64_t)t * kStage + 32 * lane) >> a.c.shift);
   };
   auto scales_at = [&](int t, int id) {
     // a strip past the end: its block may be absent or never written, whose
@@ -638,7 +629,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     return s;
   };
   int batch = kStrips * t0;  // its first strip
-  int id0 = blocks_at(t0), id1 = blocks_at(t0 + kBatch), id2 = blocks_at(t0 + 2 * kBatch);
   auto id_of = [&](int i) {  // a strip of this batch, the next one, or just before
     const int j = i - batch;
     return __builtin_amdgcn_readlane(j < 64 ? id0 : id1, j & 63);
@@ -849,28 +839,57 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     for (; t < t1; ++t) convert_only(t);
   }
 
+  // Out through LDS, 64 dims at a time, so that a store instruction writes whole
+  // lines (from the registers it would write 16 bytes of each of 32 rows).
+  // Register e of tile d: dim 32 d + 8 (e / 4) + 4 half + e % 4.
   L += __shfl_xor(L, 32);
-  if (w0 + col >= rows) return;
-  const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq;
-  const int64_t pr = (int64_t)sp * a.s.total * a.Hq + orow;
+  const int orow = (row0 + i) * a.Hq + hq;  // total * q_heads < 2^31
+  const int64_t first = a.nsplit > 1 ? (int64_t)sp * a.s.total * a.Hq : 0;  // part's first row
   const float f = a.nsplit > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L;
-  // register e of tile d: dim 32 d + 8 (e / 4) + 4 half + e % 4
+  float4* const page = reinterpret_cast<float4*>(smem_kv) + wave * (32 * 16);  // [row][4 dims]
+  lds_barrier();
 #pragma unroll
-  for (int d = 0; d < kTiles; ++d)
+  for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-      float x[4];
+    for (int d = 0; d < 2; ++d)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = L == 0.f ? 0.f : o[d][e + c] * f;
-      const int dim = 32 * d + 2 * e + 4 * half;
-      if (a.nsplit > 1)
-        *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = make_float4(x[0], x[1], x[2], x[3]);
-      else
-        write4(a, orow * D + dim, x);
+      for (int e = 0; e < 16; e += 4) {
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = L == 0.f ? 0.f : o[2 * c + d][e + k] * f;
+        page[col * 16 + ((8 * d + e / 2 + half) ^ (col & 15))] = make_float4(x[0], x[1], x[2], x[3]);
+      }
+    __builtin_amdgcn_wave_barrier();  // the page is this wavefront's own
+    if (a.nsplit > 1 || a.out_f32) {
+      float* to = a.nsplit > 1 ? a.part_o : reinterpret_cast<float*>(a.out);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int rr = 4 * k + (lane >> 4), v = lane & 15;
+        const int64_t at = (first + __shfl(orow, rr)) * D + 64 * c + 4 * v;
+        const float4 x = page[rr * 16 + (v ^ (rr & 15))];
+        if (w0 + rr < rows) *reinterpret_cast<float4*>(to + at) = x;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = 8 * k + (lane >> 3), v = lane & 7;
+        const int64_t at = (int64_t)__shfl(orow, rr) * D + 64 * c + 8 * v;
+        const float4 x = page[rr * 16 + (2 * v ^ (rr & 15))], y = page[rr * 16 + ((2 * v + 1) ^ (rr & 15))];
+        union {
+          __bf16 b[8];
+          uint4 u;
+        } w;
+        w.b[0] = (__bf16)x.x, w.b[1] = (__bf16)x.y, w.b[2] = (__bf16)x.z, w.b[3] = (__bf16)x.w;
+        w.b[4] = (__bf16)y.x, w.b[5] = (__bf16)y.y, w.b[6] = (__bf16)y.z, w.b[7] = (__bf16)y.w;
+        if (w0 + rr < rows)
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at) = w.u;
+      }
     }
-  if (half == 0) {
+    __builtin_amdgcn_wave_barrier();
+  }
+  if (half == 0 && w0 + col < rows) {
     if (a.nsplit > 1)
-      a.part_ml[pr] = make_float2(M, L);
+      a.part_ml[first + orow] = make_float2(M, L);
     else if (a.lse)
       a.lse[orow] = L == 0.f ? -INFINITY : kLn2 * (M + log2_fast(L));
   }
