@@ -571,3 +571,168 @@ def test_graph_replay(msq):
         first += 1
         length += 1
         torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- many query rows
+# A call with more than 64 query rows for a head, whose 16-row tiles would read more than
+# 400 MB of cache between them, takes another kernel.  Idle sequences beside the small ones
+# bring a call there.
+
+def crowd(H, G, D, P, table, lens, counts, window=0, hint=0):
+    rows, longest = max(counts) * G, len(table[0]) * P
+    if hint:
+        longest = min(longest, hint)
+    if window:
+        longest = min(longest, window + max(counts) + 32)
+    assert rows > 64
+    more = 450_000_000 // (H * -(-rows // 16) * longest * 2 * D) + 1
+    table = np.concatenate([np.asarray(table), np.full((more, len(table[0])), -1)])
+    return table, list(lens) + [0] * more, list(counts) + [0] * more
+
+
+MANY = [(128, 64, 1, 4, [64, 65, 127, 500, 1], [17, 20, 33, 40, 1]),
+        (128, 64, 2, 16, [300, 31], [9, 5]),
+        (64, 128, 2, 5, [700, 129, 257], [70, 1, 64]),
+        (256, 64, 2, 3, [130, 310], [43, 90])] + [c for c in CASES if max(c[5]) * c[3] > 64]
+
+
+@pytest.mark.parametrize("window", [0, 1, 50])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attention_many_rows(msq, case, window):
+    D, P, H, G, lens, counts = MANY[case]
+    print(f"many rows {MANY[case]} window={window}", flush=True)
+    rng = np.random.default_rng(100 + case)
+    table, blocks = scattered(rng, lens, P)
+    p = Pair(msq, blocks, H, D, P, seed=case, fill=float("nan"))
+    p.write(table, [0] * len(lens), lens)
+    q = rng.normal(size=(sum(counts), H * G, D)) * 1.5
+    full = crowd(H, G, D, P, table, lens, counts, window)
+    p.attend(q, *full, window=window)
+    p.attend(q, *full, window=window, dtype=torch.float32, out=torch.bfloat16)
+    if window == 0:
+        p.attend(q, *full, causal=False, scale=0.2)
+        for hint in (30, 200):  # fewer tokens announced than there are
+            p.attend(q, *crowd(H, G, D, P, table, lens, counts, hint=hint), max_kv_len=hint)
+        # more tokens than there are: the work is split, and most parts stay empty
+        width = 450_000_000 // (len(lens) * H * -(-max(counts) * G // 16) * 2 * D * P) + 1
+        wide = np.concatenate([table, np.full((len(lens), width), -1)], 1)
+        p.attend(q, wide, lens, counts)
+
+
+@pytest.mark.parametrize("D,P,H,G,lens,counts,window", [
+    (128, 64, 8, 4, [8100], [150], 0), (128, 64, 8, 4, [8100], [150], 5000),
+    (64, 128, 8, 4, [9000, 3000], [200, 130], 0), (256, 32, 4, 4, [6600, 0], [140, 30], 0)])
+def test_attention_many_rows_split(msq, D, P, H, G, lens, counts, window):
+    """Long enough for several parts with tokens each; the same bits every time."""
+    print(f"many rows split D={D} P={P} lens={lens} window={window}", flush=True)
+    table, blocks = scattered(np.random.default_rng(21), lens, P)
+    p = Pair(msq, blocks, H, D, P, seed=21, fill=float("nan"))
+    p.write(table, [0] * len(lens), lens)
+    q = np.random.default_rng(22).normal(size=(sum(counts), H * G, D)) * 1.5
+    a, la = p.attend(q, table, lens, counts, window=window)
+    b, lb = p.attend(q, table, lens, counts, window=window)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_attention_many_rows_that_see_nothing(msq):
+    lens, counts = [0, 3, 0, 33], [60, 3, 90, 64]
+    table, blocks = scattered(np.random.default_rng(1), [64] * 4, 64)
+    for D, G in ((128, 8), (64, 3), (256, 2)):
+        p = Pair(msq, blocks, 2, D, 64, seed=1, fill=float("nan"))
+        p.write(table, [0] * 4, lens)
+        q = np.random.default_rng(2).normal(size=(sum(counts), 2 * G, D))
+        for window in (0, 2):
+            p.attend(q, *crowd(2, G, D, 64, table, lens, counts, window), window=window)
+        wide = np.concatenate([table, np.full((4, 30000), -1)], 1)
+        for hint in (0, 600):
+            p.attend(q, wide, lens, counts, max_kv_len=hint)
+
+
+def test_attention_many_rows_extremes(msq):
+    """Value scales far apart, scores in the thousands, tiny and huge queries, keys of zeros."""
+    D, P, L, n, G = 128, 32, 256, 40, 4
+    table = [np.arange(8)]
+    full = crowd(1, G, D, P, table, [L], [n])
+    p = Pair(msq, 8, 1, D, P, seed=23)
+    v = p.tokens(L) * np.repeat(2.0 ** np.array([0, -40, 20, 3, -60, 0, 10, 1]), P)[:, None, None]
+    v[5 * P:6 * P] = 0
+    k = p.tokens(L)
+    k[64:128] = 0
+    rng = np.random.default_rng(24)
+    for values in (v, v * 0, p.tokens(L) * 1e-24):
+        p.write(table, [0], [L], torch.float32, k=k, v=values)
+        for f in (3.0, 30.0, 1e-30, 1e-42, 1e4, 0.0):
+            p.attend(rng.normal(size=(n, G, D)) * f, *full)
+        p.attend(rng.normal(size=(n, G, D)) * 1e30, *full, scale=1e-30)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("gap", [4, 40, 90, 400])
+def test_attention_zero_values_under_the_top_scores(msq, D, gap):
+    """A block of zero values whose scores are e^gap above all others takes nearly all of the
+    softmax; what is left of the other values is still as exact, wherever the block stands."""
+    P, L, H, G = 32, 448, 2, 2
+    table = [np.arange(14)]
+    p = Pair(msq, 14, H, D, P, seed=28)
+    rng = np.random.default_rng(29)
+    unit = np.sign(rng.normal(size=(H, D)))
+    for at in (0, 5, 13):
+        k, v = rng.normal(size=(L, H, D)) * 0.3, p.tokens(L) * 1e-3
+        k[at * P:(at + 1) * P] += unit * gap / D
+        v[at * P:(at + 1) * P] = 0
+        v[((at + 4) % 14) * P:((at + 4) % 14 + 1) * P] = 0
+        p.write(table, [0], [L], torch.float32, k=k, v=v)
+        for n in (1, 40):
+            q = (unit[:, None] + rng.normal(size=(n, H, G, D)) * 0.01).reshape(n, H * G, D)
+            p.attend(q, table, [L], [n], scale=1.0)
+            p.attend(q, table, [L], [n], scale=1.0, max_kv_len=1 << 20)
+            if n * G > 64:
+                p.attend(q, *crowd(H, G, D, P, table, [L], [n]), scale=1.0)
+                wide = np.concatenate([table, np.full((1, 30000), -1)], 1)
+                p.attend(q, wide, [L], [n], scale=1.0)
+
+
+def test_attention_many_rows_ignore_what_is_masked(msq):
+    """Slots past a sequence's length, absent blocks, non-finite queries of other rows."""
+    D, P, L, n, G = 128, 64, 200, 70, 4
+    p = Pair(msq, 6, 1, D, P, seed=25, fill=float("inf"))
+    table = np.array([[1, 4, 2, 3]])
+    p.write(table, [0], [L])
+    q, qt = rounded(np.random.default_rng(26).normal(size=(n, G, D)), torch.bfloat16)
+    hole = table.copy()
+    hole[0, 1] = -7
+    for row in (table, hole):
+        full, lens, counts = crowd(1, G, D, P, row, [L], [n])
+        call = lambda x: msq.kv_attention(x, p.gpu, i32(full), i32(lens), i32(offsets(counts)),
+                                          max_count=n, out_dtype=torch.float32, return_lse=True)
+        got, lse = call(qt)
+        torch.cuda.synchronize()
+        hide = (np.arange(L) // P == 1) if row is hole else None
+        p.close(got, lse, q, table[0], L, torch.bfloat16, True, 0, 1 / np.sqrt(D), hide)
+        q2 = qt.clone()
+        q2[0, 1, 5] = float("nan")
+        q2[n - 1, 3, 0] = float("inf")
+        other, _ = call(q2)
+        torch.cuda.synchronize()
+        bad = torch.zeros(n, G, dtype=torch.bool)
+        bad[0, 1] = bad[n - 1, 3] = True
+        assert torch.isnan(other.cpu()[bad]).all()
+        assert torch.equal(other.cpu()[~bad], got.cpu()[~bad])
+
+
+def test_attention_many_rows_past_32_bits_of_bytes(msq):
+    """A cache whose code buffers pass 4 GiB, its last blocks in use."""
+    P, H, D, n, L = 256, 8, 256, 40, 300
+    blocks = (1 << 32) // (P * H * D) + 9
+    p = Pair(msq, 2, H, D, P, seed=27)
+    big = msq.allocate_kv_cache(blocks, H, D, P)
+    k, kt = rounded(p.tokens(L), torch.bfloat16)
+    v, vt = rounded(p.tokens(L), torch.bfloat16)
+    p.ref.write(k, v, np.array([[1, 0]]), [0], [0, L])
+    table, lens, counts = crowd(H, 2, D, P, [[blocks - 1, blocks - 7]], [L], [n])
+    msq.kv_write(big, kt, vt, i32(table[:1]), i32([0]))
+    q, qt = rounded(np.random.default_rng(n).normal(size=(n, 2 * H, D)), torch.bfloat16)
+    got, lse = msq.kv_attention(qt, big, i32(table), i32(lens), i32(offsets(counts)), max_count=n,
+                                out_dtype=torch.float32, return_lse=True)
+    torch.cuda.synchronize()
+    p.close(got, lse, q, np.array([1, 0]), L, torch.bfloat16, True, 0, 1 / 16)
