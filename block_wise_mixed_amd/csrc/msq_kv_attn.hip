@@ -313,7 +313,14 @@ extern __shared__ __align__(16) unsigned char smem_kv[];
 // operand order), the next tile's loads in flight during the current one's
 // products.  S^T = K Q^T (16 x 16 x 32, tokens down, rows across), whose
 // result registers are the B operand of O^T = V^T P^T: no LDS in the loop.
-// Bound by HBM: 2 D bytes a token and kv head.
+//
+// Bound by HBM, 2 D bytes a token and kv head: 4 sequences of 131072 tokens, 64
+// query heads on 8 of 128, 1.07 GB in 190 us, 5.6 TB/s; 32 of up to 4097, 179 MB in
+// 43 us, 4.1 TB/s (their lengths differ, and each workgroup starts with a chain
+// of loads: lengths, table, codes).  Few tokens: that chain, 4.7 us from launch to
+// launch for one token on 1 to 128, 7.6 on 777.  Tiles of 32 rows halve what
+// more than 16 rows read but leave two wavefronts a SIMD instead of three (128
+// rows on 4096 tokens of 128 heads: 45 -> 54 us).
 template <int D>
 struct Tile {
   uint4 k[D / 32];  // [16-token half][64-dim chunk]
@@ -591,6 +598,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 // three do not depend on each other, so its vector instructions run between its
 // matrix instructions.  LDS holds four strips of keys and four of values, in
 // turn; one barrier a stage.
+//
+// Bound by the matrix and the vector instructions together, and by the clock
+// that the card holds under them (1.9 to 2.0 GHz): 2048 tokens, 64 query heads on
+// 8 of 128, on 32049 tokens, 2.08 Tflop in 1.85 ms (1.82 to 1.92 over cards), 1.1
+// Pflop/s; matrix units busy 58% of the time, vector units 59% (16 exponentials, at a
+// quarter of the rate, and some 60 other instructions a strip and 16 products), the
+// LDS 36%, no bank conflicts.  Tried and slower: stages of 128 tokens (1900 ->
+// 1925 us), 4 or 8 operands read ahead instead of 2 (1%), two groups of wavefronts
+// that alternate between products and softmax (1972 -> 2090), 64 rows a
+// wavefront (1850 -> 2430: past 256 registers every operand is copied between the
+// two files), the row sums as dot products of the rounded weights (1846 ->
+// 1855).
 template <int D, int W>
 struct Prefill {
   static constexpr int kStrips = 2;                // a stage
@@ -891,7 +910,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   }
 
   // Out through LDS, 64 dims at a time, so that a store instruction writes whole
-  // lines (from the registers it would write 16 bytes of each of 32 rows).
+  // lines (from the registers it would write 16 bytes of each of 32 rows; with
+  // the early table loads, two sequences of 2048 tokens 78.5 -> 73.6 us).
   // Register e of tile d: dim 32 d + 8 (e / 4) + 4 half + e % 4.
   const float grown = join_zeros<32>(M, L, Mz, Lz);
   const int orow = (row0 + i) * a.Hq + hq;  // total * q_heads < 2^31
@@ -949,7 +969,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
 // ---- the join of a split call ----------------------------------------------
 // kWaves wavefronts (1 or 4) take one query row and head.  Lane j of each holds
 // part j's M and L (at most 64 parts); each wavefront adds up its share of the
-// parts, in order, and with four of them one another's sums.
+// parts, in order, and with four of them one another's sums.  Bound by its
+// chain of loads (lengths, M and L, partial sums), 2 to 3 us, or for many rows by
+// the partials' traffic, 4 D bytes a row and part.
 template <int D, int kWaves>
 __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
   constexpr int kPer = D / 64;

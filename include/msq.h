@@ -482,11 +482,14 @@ size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_
  * value gives NaN.  Products run on the f16 matrix instructions: codes are
  * exact there, the query row is scaled by a power of two and the softmax
  * weights are rounded to f16; scores, softmax statistics and sums are fp32.
- * Rows outside every sequence are left as they are.
+ * Value scales below 2^-100 count as 0.  Rows outside every sequence are left
+ * as they are.
  * workspace: msq_kv_attention_workspace_bytes, 256-byte aligned; calls that
- * share one must be ordered on one stream.  One launch, and one more to join
- * the parts where a sequence's tokens are split over workgroups.  Errors as
- * msq_kv_write, plus MSQ_ERR_BUFFER_TOO_SMALL. */
+ * share one must be ordered on one stream, and it may hold anything before a
+ * call.  One launch; where a sequence's tokens are split over workgroups, their
+ * parts are joined inside it (few of them) or by one more.  Asynchronous, and
+ * the same bits every time.  Errors as msq_kv_write, plus
+ * MSQ_ERR_BUFFER_TOO_SMALL. */
 msq_status msq_kv_attention(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
                             const msq_kv_attn *attn, void *workspace, size_t workspace_bytes,
                             hipStream_t stream);
