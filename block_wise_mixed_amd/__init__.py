@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -110,6 +111,9 @@ class _KvAttn(ctypes.Structure):
                 ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int32),
                 ("lse", ctypes.c_void_p)]
+
+
+_KV_ATTN = struct.Struct("@PqqiiPqfiiPiP")  # the fields of _KvAttn
 
 
 def load_library():
@@ -675,8 +679,8 @@ def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int
     first = _kv_index(first, "first", s.batch, index)
     dtype = dtype or torch.bfloat16
     code = _kv_dtype(dtype)
-    both = torch.empty((2, total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
-    k, v = both.unbind(0)
+    k = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
+    v = torch.empty_like(k)
     status = load_library().msq_kv_read(cache._desc, s, first.data_ptr(), k.data_ptr(),
                                         v.data_ptr(), code, cuda._cuda_getCurrentRawStream(index))
     if status:
@@ -725,14 +729,19 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     s, keep = _kv_seqs(cache, block_table, offset, rows, max_count)
     kv_len = _kv_index(kv_len, "kv_len", s.batch, index)
     if out is None:
-        out = torch.empty((rows, heads, dim), dtype=out_dtype or torch.bfloat16, device=cache.device)
+        out = torch.empty_like(q, dtype=out_dtype or torch.bfloat16,
+                               memory_format=torch.contiguous_format)
     elif out.shape != (rows, heads, dim) or not out.is_contiguous() or out.get_device() != index or \
             (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be contiguous, [rows][q_heads][head_dim], on the cache's device")
     lse = torch.empty((rows, heads), dtype=torch.float32, device=cache.device) if return_lse else None
-    a = _KvAttn(q_at, q_st, q_sh, q_code, heads, kv_len.data_ptr(), max_kv_len, scale,
-                1 if causal else 0, window, out.data_ptr(), _kv_dtype(out.dtype),
-                None if lse is None else lse.data_ptr())
+    a = _KvAttn()
+    try:  # all fields at once: a third of the time that the constructor takes
+        _KV_ATTN.pack_into(a, 0, q_at, q_st, q_sh, q_code, heads, kv_len.data_ptr(), max_kv_len,
+                           scale, 1 if causal else 0, window, out.data_ptr(), _kv_dtype(out.dtype),
+                           0 if lse is None else lse.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"max_kv_len, scale or window: {e}") from None
     if workspace is None:
         need = int(lib.msq_kv_attention_workspace_bytes(cache._desc, s, a))
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
