@@ -620,7 +620,18 @@ struct Prefill {
   static constexpr int kUnits = 4 * kStrips * D / kThreads;  // 16-byte pieces of keys and values a thread
   static constexpr int kStrip = 4 * D;             // 16-byte pieces of a strip in LDS
   static constexpr int kProducts = kSteps + 2 * kTiles;  // of a strip: keys, then values
+  static constexpr int kPage = 32 * 16;            // 16-byte pieces of a wavefront's 32 rows x 64 results
+  static constexpr int kRingPieces = 4 * kStrips * kStrip;
+  static constexpr int kLds =                      // bytes: the strips, and then the results
+      16 * (kRingPieces > kWaves * kPage ? kRingPieces : kWaves * kPage);
   static constexpr int kAhead = 2;                 // operands read from LDS before their product
+  // whether a thread's piece u is one of the values' (the same in a wavefront)
+  __device__ static int kind(int u) {
+    if constexpr (kThreads > 2 * kStrips * D)
+      return __builtin_amdgcn_readfirstlane(threadIdx.x) / (2 * kStrips * D);
+    else
+      return kThreads * u / (2 * kStrips * D);
+  }
 };
 
 template <int D, int W>
@@ -705,7 +716,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   const uint8_t* const vc = a.c.vc + (int64_t)h * P * D;
   typedef uint4 Codes[C::kUnits];
   auto load_one = [&](Codes& st, int ik, int iv, int u) {
-    const int kind = C::kThreads * u / (2 * kStrips * D), n = C::kThreads * u + (int)threadIdx.x;
+    const int n = C::kThreads * u + (int)threadIdx.x, kind = C::kind(u);
     const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & (kStrips - 1));
     const int64_t blk = max(id_of(i), 0) * block_bytes;
     const uint32_t at = (uint32_t)(((32 * i) & (P - 1)) * D + 16 * (n & (2 * D - 1)));
@@ -736,7 +747,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   // [strip][d tile][step][half][d], 16 bytes each
   half8* const lds = reinterpret_cast<half8*>(smem_kv);
   auto convert_half = [&](const Codes& st, int ik, int iv, int u, int second) {
-    const int kind = C::kThreads * u / (2 * kStrips * D), n = C::kThreads * u + (int)threadIdx.x;
+    const int n = C::kThreads * u + (int)threadIdx.x, kind = C::kind(u);
     const int m = n & (2 * D - 1), g = m % 64 / 16;
     const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & (kStrips - 1));
     const int tok = 16 * (m / D) + (m & 15);
@@ -871,7 +882,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     pa[0] = pa[1] = pb[0] = pb[1] = half8{};
     convert(st0, i0 - kStrips + 1, i0 - 1);
 #pragma unroll
-    for (int j = 0; j < C::kUnits; ++j) convert_half(st1, i0 + 1, 0, j >> 1, j & 1);
+    for (int u = 0; u < C::kUnits; ++u)
+      if (C::kind(u) == 0) {  // its values have no place yet
+        convert_half(st1, i0 + 1, 0, u, 0);
+        convert_half(st1, i0 + 1, 0, u, 1);
+      }
     lds_barrier();
     sa = f32x16{};
 #pragma unroll
@@ -917,7 +932,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   const int orow = (row0 + i) * a.Hq + hq;  // total * q_heads < 2^31
   const int64_t first = a.nsplit > 1 ? (int64_t)sp * a.s.total * a.Hq : 0;  // part's first row
   const float f = grown * (a.nsplit > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L);
-  float4* const page = reinterpret_cast<float4*>(smem_kv) + wave * (32 * 16);  // [row][4 dims]
+  float4* const page = reinterpret_cast<float4*>(smem_kv) + wave * C::kPage;  // [row][4 dims]
   lds_barrier();
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) {
@@ -1105,24 +1120,39 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   const int64_t at_work = std::max(fill, items * ((tiles + span - 1) / span));
   p.waves = 0;
   if (rows > kFewRows && at_work * std::min(span, tiles) > kDecodeBytes / (2 * D * kSpan)) {
-    // k_kv_prefill.  With 8 wavefronts two share a SIMD, as of two workgroups of 4,
-    // and a strip is converted for twice the rows (4 and 8 wavefronts: 4 sequences of 1024
-    // rows of 8 heads on 1500 tokens 94, 86 us, 1024 on 8192 166, 142); workgroups of 4
-    // fill the GPU better where sequences are short (256 on 512: 22.1, 23.8 us).
-    p.waves = D == 128 && longest > 1024 ? 8 : 4;
-    cut(32 * p.waves, Prefill<128, 8>::kStage);
-    // Parts: the number that takes the least time, counted in tiles: rounds of
-    // workgroups over the GPU, each its tiles and 4 more to start and end; where
-    // there are several parts, 3 for the join's launch and their traffic
-    // (8 MB in the time of a tile).
-    const int64_t slots = D == 128 && p.waves == 4 ? 512 : D == 64 ? 768 : 256;
-    const double traffic = (double)s.total * t.q_heads * D * 8 / 8e6;
+    // k_kv_prefill.  Parts: the number that takes the least time, counted in tiles:
+    // rounds of workgroups over the GPU (in fractions where three share a compute
+    // unit), each its tiles and some more to start and end; where there are
+    // several parts, 3 for the join's launch and their traffic (8 MB in the time of
+    // a tile).
     double least = 1e300;
-    for (int64_t n = 1; n <= std::min<int64_t>(kMostParts, tiles); ++n) {
-      const int64_t each = (tiles + n - 1) / n, rounds = (items * n + slots - 1) / slots;
-      const double cost = (double)rounds * (double)(each + 4) + (n > 1 ? 3 + traffic * (double)n : 0);
-      if (cost < least) least = cost, span = each;
+    auto consider = [&](int waves, int64_t slots, double tile, int64_t start) {
+      const int64_t rows_of = 32 * waves, all = lists * ((rows + rows_of - 1) / rows_of);
+      const int64_t stages = (longest + Prefill<128, 8>::kStage - 1) / Prefill<128, 8>::kStage;
+      const double traffic = (double)s.total * t.q_heads * D * 8 / 8e6;
+      for (int64_t n = 1; n <= std::min<int64_t>(kMostParts, stages); ++n) {
+        const int64_t each = (stages + n - 1) / n;
+        const double rounds = slots == 768 ? std::max(1., (double)(all * n) / 768)
+                                           : (double)((all * n + slots - 1) / slots);
+        const double cost = rounds * (double)(each + start) * tile + (n > 1 ? 3 + traffic * (double)n : 0);
+        if (cost < least) least = cost, p.waves = waves, span = each;
+      }
+    };
+    // With 8 wavefronts a strip is converted for twice the rows.  Head dim 128: two
+    // wavefronts a SIMD either way, and workgroups of 4 only fill the GPU better
+    // where sequences are short (4 and 8 wavefronts: 4 x 1024 rows of 8 heads on
+    // 1500 tokens 94, 86 us, 1024 on 8192 166, 142; 256 on 512 22.1, 23.8).  64: three
+    // workgroups of 4 a compute unit or one of 8, a tile 1.73 to 1 in time (2048 rows
+    // of 128 heads on 16000 tokens 1337, 1180 us; 8 x 512 of 64 on 2000 158, 164).
+    if (D == 64) {
+      consider(4, 768, 1.73, 4);
+      consider(8, 256, 1, 10);
+    } else if (D == 128 && longest > 1024) {
+      consider(8, 256, 1, 4);
+    } else {
+      consider(4, D == 128 ? 512 : 256, 1, 4);
     }
+    cut(32 * p.waves, Prefill<128, 8>::kStage);
   }
   p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, kMostParts);
   p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
@@ -1165,9 +1195,9 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
     auto prefill = [&](auto w) {
       using C = Prefill<D, decltype(w)::value>;
       hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves>), dim3((unsigned)p.blocks), dim3(C::kThreads),
-                         4 * C::kStrips * 16 * C::kStrip, stream, a);
+                         C::kLds, stream, a);
     };
-    if constexpr (D == 128)
+    if constexpr (D != 256)
       if (p.waves == 8) prefill(std::integral_constant<int, 8>{});
     if (p.waves == 4) prefill(std::integral_constant<int, 4>{});
   } else {

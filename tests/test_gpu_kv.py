@@ -596,11 +596,9 @@ MANY = [(128, 64, 1, 4, [64, 65, 127, 500, 1], [17, 20, 33, 40, 1]),
         (256, 64, 2, 3, [130, 310], [43, 90])] + [c for c in CASES if max(c[5]) * c[3] > 64]
 
 
-@pytest.mark.parametrize("window", [0, 1, 50])
-@pytest.mark.parametrize("case", range(len(MANY)))
-def test_attention_many_rows(msq, case, window):
-    D, P, H, G, lens, counts = MANY[case]
-    print(f"many rows {MANY[case]} window={window}", flush=True)
+def many_rows(msq, shape, case, window):
+    D, P, H, G, lens, counts = shape
+    print(f"many rows {shape} window={window}", flush=True)
     rng = np.random.default_rng(100 + case)
     table, blocks = scattered(rng, lens, P)
     p = Pair(msq, blocks, H, D, P, seed=case, fill=float("nan"))
@@ -617,6 +615,21 @@ def test_attention_many_rows(msq, case, window):
         width = 450_000_000 // (len(lens) * H * -(-max(counts) * G // 16) * 2 * D * P) + 1
         wide = np.concatenate([table, np.full((len(lens), width), -1)], 1)
         p.attend(q, wide, lens, counts)
+
+
+@pytest.mark.parametrize("window", [0, 1, 50])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attention_many_rows(msq, case, window):
+    many_rows(msq, MANY[case], case, window)
+
+
+@pytest.mark.parametrize("window", [0, 3500])
+@pytest.mark.parametrize("shape", [(64, 64, 1, 4, [4000, 333], [64, 50]),
+                                   (64, 256, 2, 2, [5000, 600], [127, 128]),
+                                   (128, 128, 1, 3, [3333], [85])])
+def test_attention_many_rows_long(msq, shape, window):
+    """Long sequences: tiles of 256 rows for heads of 64 too."""
+    many_rows(msq, shape, 50, window)
 
 
 @pytest.mark.parametrize("D,P,H,G,lens,counts,window", [
