@@ -692,7 +692,9 @@ def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch:
                                  max_count: int, max_kv_len: int, causal: bool = True,
                                  window: int = 0) -> int:
     """Workspace of kv_attention for calls of these sizes (rows: query rows of all sequences)
-    whose block tables have no more entries than max_kv_len tokens need."""
+    whose block tables have no more entries than max_kv_len tokens need.  Fewer sequences can
+    need more, since theirs are split further: a buffer for calls of several sizes takes the
+    largest."""
     width = max(1, -(-max_kv_len // cache.block_tokens))
     s = _KvSeqs(batch, width, None, 1, rows, max_count)  # of offset only whether it is there
     a = _KvAttn()

@@ -487,6 +487,44 @@ def test_empty_calls(msq):
     torch.cuda.synchronize()
 
 
+def test_refusals(msq):
+    """What does not fit raises, before any launch, and leaves the cache as it is."""
+    c = msq.allocate_kv_cache(4, 2, 64, 32)
+    c.k_codes.zero_(), c.v_codes.zero_()
+    x, q = torch.ones(4, 2, 64, device="cuda"), torch.ones(4, 6, 64, device="cuda")
+    table, first = i32([[0, 1]]), i32([0])
+    for args in ((x[:, :1], x, table, first), (x, x[:3], table, first), (x, x.bfloat16(), table, first),
+                 (x.cpu(), x, table, first), (x, x, table.long(), first), (x, x, table[0], first),
+                 (x, x, table, i32([0, 0])), (x, x, table.cpu(), first)):
+        with pytest.raises(ValueError):
+            msq.kv_write(c, *args)
+    with pytest.raises(TypeError):
+        msq.kv_write(c, x.half(), x.half(), table, first)
+    with pytest.raises(ValueError):
+        msq.kv_read(c, table, first)
+    with pytest.raises(ValueError):
+        msq.kv_read(c, i32([[0], [1]]), i32([0, 0]), total=3)
+    lens = i32([4])
+    for kw in (dict(out=torch.empty(4, 6, 32, device="cuda")), dict(out=torch.empty(4, 6, 64)),
+               dict(out=torch.empty(4, 6, 64, device="cuda"), out_dtype=torch.bfloat16),
+               dict(max_kv_len=1 << 70), dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            msq.kv_attention(q, c, table, lens, **kw)
+    with pytest.raises(TypeError):
+        msq.kv_attention(q, c, table, lens, out_dtype=torch.float16)
+    wide = i32(np.zeros((1, 4000)))
+    for kw in (dict(window=4, causal=False), dict(window=-1), dict(scale=-1.0), dict(scale=float("nan")),
+               dict(max_kv_len=-1)):
+        with pytest.raises(msq.MsqError):
+            msq.kv_attention(q, c, table, lens, **kw)
+    with pytest.raises(msq.MsqError):                           # 5 query heads on 2
+        msq.kv_attention(q[:, :5], c, table, lens)
+    with pytest.raises(msq.MsqError):                           # too small for the parts
+        msq.kv_attention(q, c, wide, lens, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert not bool(c.k_codes.any()) and not bool(c.k_scale.any())
+
+
 def test_blocks_past_32_bits_of_bytes(msq):
     """A cache whose code buffers pass 4 GiB, its last blocks in use."""
     P, H, D = 256, 8, 256
