@@ -1155,12 +1155,15 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
     cut(32 * p.waves, Prefill<128, 8>::kStage);
   }
   p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, kMostParts);
+  // unsplit where the parts, or the join's grid of (sequence, row, head), would pass
+  // one launch
+  if (items * p.nsplit > most_blocks ||
+      (int64_t)s.batch * s.max_count * G > kMostThreads / 256 / c.H)
+    p.nsplit = 1;
   p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
   p.blocks = items * p.nsplit;
   if (p.blocks > most_blocks) return MSQ_ERR_SHAPE;
   if (p.nsplit > 1) {
-    // the join's grid: (sequence, row, head)
-    if ((int64_t)s.batch * s.max_count * G > kMostThreads / 256 / c.H) return MSQ_ERR_SHAPE;
     const size_t partials = (size_t)s.total * t.q_heads * p.nsplit;
     p.ml_at = (partials * D * 4 + 255) / 256 * 256;
     p.workspace = p.ml_at + partials * 8;

@@ -131,6 +131,26 @@ def test_workspace_sizes(lib):
         w(c, seqs(table_width=4096), attn(max_kv_len=64 * 4096))
 
 
+def test_attention_many_sequences(lib):
+    """Sizes past one launch are refused without overflow; calls whose parts alone would pass it
+    are taken unsplit (then only the missing pointer is left to refuse)."""
+    f = lib.msq_kv_attention
+    run = lambda c, s, **kw: f(c, s, attn(q=None, **kw), BASE * 10, 1 << 40, None)
+    c = cache(kv_heads=64)
+    many = seqs(batch=1 << 18, total=1 << 18, max_count=0, table_width=1 << 14)
+    assert run(cache(), many) == SHAPE                      # max_count 0: 2^18 rows each
+    many.max_count = 1
+    assert run(cache(), many) == INVALID
+    assert run(c, many, q_heads=64) == SHAPE                # 2^24 workgroups
+    many.batch = many.total = 1 << 16
+    assert run(c, many, q_heads=64) == INVALID              # 2^22 of 2^13 tiles: unsplit
+    assert lib.msq_kv_attention_workspace_bytes(c, many, attn(q_heads=64)) == 0
+    for batch, total, heads in ((2**31 - 1, 1, 2**31 - 1), (2**31 - 1, 2**31 - 1, 1), (1, 1, 2**31 - 1),
+                                (2**23, 2**23, 1), (1, 2**31 - 1, 1)):
+        s = seqs(batch=batch, total=total, max_count=0, table_width=1 << 24)
+        assert run(cache(kv_heads=heads), s, q_heads=heads) in (SHAPE, INVALID)
+
+
 def test_binding_refuses(lib):
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError):
