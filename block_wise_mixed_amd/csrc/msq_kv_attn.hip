@@ -625,6 +625,15 @@ struct Prefill {
   static constexpr int kLds =                      // bytes: the strips, and then the results
       16 * (kRingPieces > kWaves * kPage ? kRingPieces : kWaves * kPage);
   static constexpr int kAhead = 2;                 // operands read from LDS before their product
+  // which of the stage's strips a thread's piece u is of (the same in a wavefront,
+  // and known here or the same for all its pieces, which then share its address)
+  __device__ static int strip_of(int u) {
+    static_assert(2 * D % kThreads == 0 || kThreads % (2 * D * kStrips) == 0);
+    if constexpr (2 * D % kThreads == 0)
+      return kThreads * u / (2 * D) & (kStrips - 1);
+    else
+      return __builtin_amdgcn_readfirstlane(threadIdx.x) / (2 * D) & (kStrips - 1);
+  }
   // whether a thread's piece u is one of the values' (the same in a wavefront)
   __device__ static int kind(int u) {
     if constexpr (kThreads > 2 * kStrips * D)
@@ -717,7 +726,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   typedef uint4 Codes[C::kUnits];
   auto load_one = [&](Codes& st, int ik, int iv, int u) {
     const int n = C::kThreads * u + (int)threadIdx.x, kind = C::kind(u);
-    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & (kStrips - 1));
+    const int i = (kind ? iv : ik) + C::strip_of(u);
     const int64_t blk = max(id_of(i), 0) * block_bytes;
     const uint32_t at = (uint32_t)(((32 * i) & (P - 1)) * D + 16 * (n & (2 * D - 1)));
     st[u] = *reinterpret_cast<const uint4*>((kind ? vc : kc) + blk + at);
@@ -741,6 +750,15 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   half8 q[kSteps];  // slots (half, e) of step s are dims 16 s + 8 half + e
   float down;
   query_fragments<kSteps, 32>(qraw, a.q_f32, q, down);
+#ifdef __HIP_DEVICE_COMPILE__
+  // Head dim 256: into the accumulation registers, from which the products read
+  // them too (left to itself the compiler moves them there and back in every
+  // strip: 1097 -> 1055 us for 2048 rows of 32 heads on 16000 tokens).
+  if constexpr (D == 256) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) asm volatile("" : "+a"(q[k]));
+  }
+#endif
   const float cq = a.c2 * down;
 
   // and from there as f16 into LDS: keys [strip][step][half][row], values
@@ -749,7 +767,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   auto convert_half = [&](const Codes& st, int ik, int iv, int u, int second) {
     const int n = C::kThreads * u + (int)threadIdx.x, kind = C::kind(u);
     const int m = n & (2 * D - 1), g = m % 64 / 16;
-    const int i = (kind ? iv : ik) + (__builtin_amdgcn_readfirstlane(n) / (2 * D) & (kStrips - 1));
+    const int i = (kind ? iv : ik) + C::strip_of(u);
     const int tok = 16 * (m / D) + (m & 15);
     half8* p = lds + (kRing * kind + (i & (kRing - 1))) * C::kStrip +
                (kind ? (4 * (m / 64) + g) * 32 + (m & 15)
@@ -1074,9 +1092,10 @@ constexpr int kJoinInside = 16, kJoinFloats = 8192;
 // mostly from the L2s) from which more than kFewRows rows take k_kv_prefill.
 // k_kv_decode and k_kv_prefill: head dim 128, 98 MB 17.7, 28.3 us; 268 MB 21.7, 37.5;
 // 393 MB 31.2, 33.3; 491 MB 45, 36; 1074 MB 75, 62; 64, 262 MB 30.3, 32.1; 524 MB 48.2,
-// 43.7; 256, 262 MB 35.3, 45.3; 524 MB 55.7, 49.5.  Up to kFewRows rows k_kv_decode keeps
-// ahead or level at any size (64 rows, 537 MB 49.6, 55.7; 2147 MB 180, 173).
-constexpr int64_t kDecodeBytes = 400000000;
+// 43.7; 256, 134 MB 16.7, 30.4; 246 MB 40.8, 36.9; 262 MB 37.3, 41.7; 268 MB 42.5,
+// 30.6; 319 MB 41.6, 37.5.  Up to kFewRows rows k_kv_decode keeps ahead or level at any
+// size (64 rows, 537 MB 49.6, 55.7; 2147 MB 180, 173).
+constexpr int64_t decode_bytes(int D) { return D == 256 ? 240000000 : 400000000; }
 constexpr int kFewRows = 64;
 
 // Sizes only; MSQ_OK with blocks == 0 for an empty call.
@@ -1119,7 +1138,7 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   span = std::min<int64_t>(std::max<int64_t>(tiles <= 12 ? 12 : 4, (tiles + want - 1) / want), 256);
   const int64_t at_work = std::max(fill, items * ((tiles + span - 1) / span));
   p.waves = 0;
-  if (rows > kFewRows && at_work * std::min(span, tiles) > kDecodeBytes / (2 * D * kSpan)) {
+  if (rows > kFewRows && at_work * std::min(span, tiles) > decode_bytes(D) / (2 * D * kSpan)) {
     // k_kv_prefill.  Parts: the number that takes the least time, counted in tiles:
     // rounds of workgroups over the GPU (in fractions where three share a compute
     // unit), each its tiles and some more to start and end; where there are

@@ -613,7 +613,7 @@ def test_graph_replay(msq):
 
 # ---------------------------------------------------------------- many query rows
 # A call with more than 64 query rows for a head, whose 16-row tiles would read more than
-# 400 MB of cache between them, takes another kernel.  Idle sequences beside the small ones
+# 400 MB of cache between them (240 MB for heads of 256), takes another kernel.  Idle sequences beside the small ones
 # bring a call there.
 
 def crowd(H, G, D, P, table, lens, counts, window=0, hint=0):
