@@ -19,6 +19,14 @@
 // nor a rescale, and weights down to 2^-20 of the largest stay normal f16
 // numbers.
 //
+// Scores may have any finite size.  Fp32 numbers of 2^28 lie 32 apart: log2 s - 6
+// is lost in an M of that size, and an exact product less a rounded M can be as far
+// from 0 at the top itself.  For a row whose top score passes 2^11 (where numbers lie
+// 2^-12 apart, a weight's rounding) the reference is therefore M + off, a score
+// rounded like all others and the small rest, and the exponents are
+// (x_t - M) + (log2 s - off), whose difference is exact near the top.  Such a row
+// takes this way in every tile.
+//
 // Codes become f16 exactly: the bytes code + 128 under the exponent byte 0x64
 // are the f16 numbers 1024 + byte, and one packed subtraction of 1152 leaves
 // the code.  A query row is scaled by the power of two that puts its largest
@@ -44,10 +52,11 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr float kNone = -1e30f;    // M before any token
+constexpr float kNone = -3.402823466e38f;  // M before any token: no score is below it
 constexpr float kTop = 14.f;       // weights stay below 2^kTop
 constexpr float kTopWeight = 16384.f;  // 2^kTop
 constexpr float kPlace = 6.f;      // a moved M puts the largest weight at 2^kPlace
+constexpr float kNear = 2048.f;    // up to here M holds a score and log2 s in one number
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100: value scales below it count as 0
@@ -179,6 +188,32 @@ __device__ inline void value_scale(float s, float& lam, float& inv) {
   inv = s >= kTiny ? __builtin_amdgcn_rcpf(s) : 0.f;
 }
 
+// A score s * f, rounded (and no part of an fma).
+__device__ inline float score_of(float s, float f) {
+#pragma clang fp contract(off)
+  return s * f;
+}
+
+// Moves the reference of a row to the score `most` of a block whose values have
+// scale 2^lam; returns the factor of what was summed with the old one.
+__device__ inline float move_reference(float most, float lam, float& M, float& off, bool& far) {
+  far = fabsf(most) > kNear;
+  const float m = far ? most : most + lam - kPlace, rest = far ? lam - kPlace : 0.f;
+  const float al = exp2_fast((M - m) + (off - rest));
+  M = m;
+  off = rest;
+  return al;
+}
+
+// M + off as one number, M; what rounding takes from it goes to L and, as the
+// factor that it returns, to O.
+__device__ inline float one_reference(float& M, float off, float& L) {
+  const float m = M + off, g = exp2_fast((M - m) + off);
+  M = m;
+  L *= g;
+  return g;
+}
+
 // Scores s (times f; -inf where masked) of a block of zeros into Mz and Lz; the
 // lanes lane ^ kFirst * m have the same row.
 template <int kFirst, int N>
@@ -188,17 +223,18 @@ __device__ inline void add_zeros(const float (&s)[N], float f, float& Mz, float&
   for (int e = 1; e < N; ++e) most = fmaxf(most, s[e]);
 #pragma unroll
   for (int x = kFirst; x < 64; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
-  const float m = fmaxf(Mz, most * f);
+  const float m = fmaxf(Mz, score_of(most, f));
   float sum = 0.f;
 #pragma unroll
-  for (int e = 0; e < N; ++e) sum += exp2_fast(fmaf(s[e], f, -m));
+  for (int e = 0; e < N; ++e) sum += exp2_fast(score_of(s[e], f) - m);
   Lz = fmaf(Lz, exp2_fast(Mz - m), sum);
   Mz = m;
 }
 
 // The sums of a row's lanes joined, and Mz and Lz joined to M and L; O is to be
-// multiplied by what it returns.  M ends at least 2^64 below Mz, so that L stays
-// finite; where that takes bits of O, the result ends below 2^-126.
+// multiplied by what it returns.  M ends at least 2^64 below Mz (level with it where
+// numbers of its size lie further apart), so that L stays finite; where that
+// takes bits of O, the result ends below 2^-126.
 template <int kFirst>
 __device__ inline float join_zeros(float& M, float& L, float Mz, float Lz) {
 #pragma unroll
@@ -206,7 +242,7 @@ __device__ inline float join_zeros(float& M, float& L, float Mz, float Lz) {
     L += __shfl_xor(L, x);
     Lz += __shfl_xor(Lz, x);
   }
-  const float m = fmaxf(M, Mz - 64.f), g = exp2_fast(M - m);
+  const float m = fmaxf(M, fabsf(Mz) < 0x1p28f ? Mz - 64.f : Mz), g = exp2_fast(M - m);
   if (Lz != 0.f) L = fmaf(L, g, Lz * exp2_fast(Mz - m));
   M = m;
   return g;
@@ -382,7 +418,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   f32x4 o[kTiles];
 #pragma unroll
   for (int d = 0; d < kTiles; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float M = kNone, L = 0.f, Mz = kNone, Lz = 0.f;
+  // limit: of the exponents x + log2 s, M + kTop; -inf for a row whose off is in use
+  float M = kNone, off = 0.f, limit = kNone, L = 0.f, Mz = kNone, Lz = 0.f;
 
   // Lane j holds the block and the scales of this wavefront's j-th tile (of a
   // batch of 64), so that a tile's loads wait for no chain of their own.
@@ -423,24 +460,36 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
       const float z[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
       add_zeros<16>(z, f, Mz, Lz);
     }
-    float top = fmaf(fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
-                           fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3]))), f, lm);
-    if (__any(top > M + kTop)) {
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float m = top > M + kTop ? top - kPlace : M;
-      const float al = exp2_fast(M - m);
-      L *= al;
+    float most = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
+                       fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
+    float ff = f, add = lm - M;
+    if (__any(fmaf(most, f, lm) > limit)) {
+      most = fmaxf(most, __shfl_xor(most, 16));
+      most = score_of(fmaxf(most, __shfl_xor(most, 32)), f);
+      if ((most - M) + (lm - off) > kTop) {
+        bool far;
+        const float al = move_reference(most, lm, M, off, far);
+        limit = far ? -INFINITY : M + kTop;
+        L *= al;
 #pragma unroll
-      for (int d = 0; d < kTiles; ++d) o[d] *= al;
-      M = m;
+        for (int d = 0; d < kTiles; ++d) o[d] *= al;
+      }
+      add = lm - M;
+      if (limit == -INFINITY) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s0[e] = (score_of(s0[e], f) - M) + (lm - off);
+          s1[e] = (score_of(s1[e], f) - M) + (lm - off);
+        }
+        ff = 1.f;
+        add = 0.f;
+      }
     }
-    const float add = lm - M;
     float sum = 0.f;
     half8 p;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float w = exp2_fast(fmaf(e < 4 ? s0[e & 3] : s1[e & 3], f, add));
+      const float w = exp2_fast(fmaf(e < 4 ? s0[e & 3] : s1[e & 3], ff, add));
       sum += w;
       p[e] = (_Float16)w;
     }
@@ -471,7 +520,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   }
 
   // join the wavefronts: M and L per row, then the weighted sum of O
-  const float grown = join_zeros<16>(M, L, Mz, Lz);
+  float grown = one_reference(M, off, L);
+  grown *= join_zeros<16>(M, L, Mz, Lz);
   float* lo_o = reinterpret_cast<float*>(smem_kv);           // [wave][16][kStride]
   float* lo_m = lo_o + kWaves * 16 * kStride;                 // [wave][16]
   float* lo_l = lo_m + kWaves * 16;
@@ -695,7 +745,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   f32x16 o[kTiles];
 #pragma unroll
   for (int d = 0; d < kTiles; ++d) o[d] = f32x16{};
-  float M = kNone, L = 0.f, Mz = kNone, Lz = 0.f;
+  // limit: of the sums of weights; below all of them for a row whose off is in use
+  float M = kNone, off = 0.f, limit = kTopWeight, L = 0.f, Mz = kNone, Lz = 0.f;
 
   // The strips' scales, held like their blocks and read a batch ahead.
   const int P = 1 << a.c.shift;
@@ -862,24 +913,26 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     use(15);
     // Every weight is below 2^kTop unless some lane's sum is not (a sum of NaN is
     // a row of NaN); only then is M moved and are the weights made again.
-    if (__any(sum > kTopWeight)) {
+    if (__float_as_int(inv) != 0 && __any(sum > limit)) {
       float most = s[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) most = fmaxf(most, s[e]);
-      most = fmaf(most, f, lam);
-      most = fmaxf(most, __shfl_xor(most, 32));
-      const float m = most > M + kPlace ? most - kPlace : M;
-      const float al = exp2_fast(M - m);
-      L *= al;
+      most = score_of(fmaxf(most, __shfl_xor(most, 32)), f);
+      if ((most - M) + (lam - off) > kPlace) {
+        bool far;
+        const float al = move_reference(most, lam, M, off, far);
+        limit = far ? -1.f : kTopWeight;
+        L *= al;
 #pragma unroll
-      for (int d = 0; d < kTiles; ++d) o[d] *= al;
-      M = m;
+        for (int d = 0; d < kTiles; ++d) o[d] *= al;
+      }
       sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float x = exp2_fast(fmaf(s[e], f, lam - M));
-        sum += x;
-        pairs[e >> 1][e & 1] = (_Float16)x;
+        const float x = limit < 0.f ? (score_of(s[e], f) - M) + (lam - off) : fmaf(s[e], f, lam - M);
+        const float y = exp2_fast(x);
+        sum += y;
+        pairs[e >> 1][e & 1] = (_Float16)y;
       }
     }
     if (__float_as_int(inv) == 0) {
@@ -946,7 +999,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   // lines (from the registers it would write 16 bytes of each of 32 rows; with
   // the early table loads, two sequences of 2048 tokens 78.5 -> 73.6 us).
   // Register e of tile d: dim 32 d + 8 (e / 4) + 4 half + e % 4.
-  const float grown = join_zeros<32>(M, L, Mz, Lz);
+  float grown = one_reference(M, off, L);
+  grown *= join_zeros<32>(M, L, Mz, Lz);
   const int orow = (row0 + i) * a.Hq + hq;  // total * q_heads < 2^31
   const int64_t first = a.nsplit > 1 ? (int64_t)sp * a.s.total * a.Hq : 0;  // part's first row
   const float f = grown * (a.nsplit > 1 ? 1.f : L == 0.f ? 0.f : 1.f / L);

@@ -483,6 +483,8 @@ size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_
  * value gives NaN.  Products run on the f16 matrix instructions: codes are
  * exact there, the query row is scaled by a power of two and the softmax
  * weights are rounded to f16; scores, softmax statistics and sums are fp32.
+ * Scores may have any size that log2(e) times fp32 holds: the weights are those of
+ * the scores as rounded to fp32.
  * Value scales below 2^-100 count as 0.  Rows outside every sequence are left
  * as they are.
  * workspace: msq_kv_attention_workspace_bytes, 256-byte aligned; calls that

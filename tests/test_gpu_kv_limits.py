@@ -1,0 +1,93 @@
+"""The 8-bit key/value cache on the GPU at the limits of its inputs, against the numpy oracle
+and, where scores are so large that only the top ones count, against what is left of the
+softmax.  Helpers and error bounds: test_gpu_kv.py."""
+import numpy as np
+import pytest
+
+from oracle import msq_kv as O
+from test_gpu_kv import Pair, crowd, i32, msq, offsets, rounded  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def ways(H, G, D, P, table, L, n):
+    """(kv_attention's block table, kv_len, counts) of one sequence with n query rows, alone and
+    so that the work is split; for more than 64 rows of a head also so that the kernel for
+    many rows takes it, unsplit and split."""
+    wide = lambda w: np.concatenate([table, np.full((1, w), -1)], 1)
+    yield table, [L], [n]
+    yield wide(400), [L], [n]
+    if n * G > 64:
+        yield crowd(H, G, D, P, table, [L], [n])
+        yield wide(450_000_000 // (H * -(-n * G // 16) * 2 * D * P) + 1), [L], [n]
+
+
+# ---------------------------------------------------------------- scores of any finite size
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("size", [5e3, 2.0 ** 19, 3e8, 1e9, 1e12, 1e20, 1e30, 1e37])
+def test_attention_scores_of_any_size(msq, D, size):
+    """Scores of +-size times code / 127, two tokens level at the top and the others so far below
+    that only these two count: the result is the mean of their values within the rounding of
+    two weights to f16 (2^-11) and of their exponents (2 x 2^-13 ln 2 while one number of at
+    most 2^11 is their reference), lse their score + ln 2.  One of the two may be of a block
+    of zeros.  The top is the largest, the least negative, or 0 among huge negative ones."""
+    P, L, H, G = 32, 96, 1, 2
+    rng = np.random.default_rng(int(np.log2(size)) + D)
+    unit = np.sign(rng.normal(size=D))
+    table = np.array([[1, 3, 0]])
+    tied = [10, 77]
+    for sign, top, others in ((1, 127, (1, 41)), (-1, 64, (90, 127)), (-1, 0, (90, 127))):
+        code = rng.integers(*others, size=L)
+        if sign < 0:
+            code[[0, 33, 65]] = 127  # blocks 0 and 2 have the same scale
+        code[tied] = top
+        k = (code.astype(np.float32) * (np.float32(1) / np.float32(127)))[:, None, None] * unit
+        for zeros in (False, True):
+            p = Pair(msq, 4, H, D, P, seed=30)
+            v = p.tokens(L) * np.repeat([1.0, 30.0, 1000.0], P)[:, None, None]
+            if zeros:
+                v[:P] = 0
+            p.write(table, [0], [L], torch.float32, k=k, v=v)
+            kv, vv = (p.ref.values(name, table[0], 0, L)[tied, 0].astype(np.float64) for name in "kv")
+            assert np.array_equal(kv[0], kv[1])
+            want = vv.mean(0)
+            bound = np.abs(vv).mean(0) * (2.0 ** -11 + 2.0 ** -12 * np.log(2) + 2.0 ** -17) + 1e-37
+            for n in (1, 40):
+                part = 2.0 ** -rng.integers(0, 3, size=(n, G))
+                q, qt = rounded(sign * unit * (size * part / D)[..., None], torch.bfloat16)
+                score = q.astype(np.float64) @ kv[0]
+                for tb, lens, counts in ways(H, G, D, P, table, L, n):
+                    print(f"D={D} size={size:g} {sign} {top} zeros={zeros} n={n} batch={len(lens)} "
+                          f"width={np.shape(tb)[1]}", flush=True)
+                    got, lse = msq.kv_attention(qt, p.gpu, i32(tb), i32(lens), i32(offsets(counts)),
+                                                max_count=n, scale=1.0, causal=False,
+                                                out_dtype=torch.float32, return_lse=True)
+                    torch.cuda.synchronize()
+                    got, lse = got.cpu().numpy(), lse.cpu().numpy()
+                    assert (np.abs(got - want) <= bound).all(), (got[0, 0, :4], want[:4])
+                    e = np.abs(score) * ((D + 32) * 2.0 ** -24 + 2.0 ** -22) + 2.0 ** -11
+                    assert (np.abs(lse - (score + np.log(2))) <= e).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_one_token_at_scores_of_any_size(msq, D):
+    """A row that sees one token returns its value, whatever its score."""
+    P, G = 64, 4
+    table = np.array([[2]])
+    rng = np.random.default_rng(D)
+    p = Pair(msq, 3, 1, D, P, seed=31)
+    p.write(table, [0], [1], torch.float32)
+    k, v = (p.ref.values(name, table[0], 0, 1)[0, 0].astype(np.float64) for name in "kv")
+    bound = np.abs(v) * (2.0 ** -11 + 2.0 ** -18) + 1e-37
+    for n in (1, 40):
+        q, qt = rounded(rng.normal(size=(n, G, D)) * 10.0 ** rng.uniform(5, 36, size=(n, G, 1)), torch.bfloat16)
+        for tb, lens, counts in ways(1, G, D, P, table, 1, n):
+            got, lse = msq.kv_attention(qt, p.gpu, i32(tb), i32(lens), i32(offsets(counts)), max_count=n,
+                                        scale=0.05, causal=False, out_dtype=torch.float32, return_lse=True)
+            torch.cuda.synchronize()
+            assert (np.abs(got.cpu().numpy() - v) <= bound).all()
+            size = 0.05 * np.abs(q.astype(np.float64)) @ np.abs(k)
+            e = size * ((D + 32) * 2.0 ** -24 + 2.0 ** -22) + 2.0 ** -16
+            assert (np.abs(lse.cpu().numpy() - 0.05 * (q.astype(np.float64) @ k)) <= e).all()
