@@ -248,22 +248,22 @@ __device__ inline float join_zeros(float& M, float& L, float Mz, float Lz) {
   return g;
 }
 
-// The positions lo <= t < hi that row i of n of a sequence with len tokens sees
-// (len <= 2^30; 32-bit numbers and unsigned divisions here and below: the
-// kernels start with a chain of them).
-__device__ inline void row_range(int len, int n, int i, int causal, int window, int& lo, int& hi) {
+// The positions lo <= t < hi of the table that row i of n of a sequence with len
+// tokens sees: a length past the table still says where its rows stand (32-bit
+// numbers and unsigned divisions here and below: the kernels start with a chain
+// of them).
+__device__ inline void row_range(const AttnArgs& a, int len, int n, int i, int& lo, int& hi) {
   lo = 0;
   hi = len;
-  if (causal) {
+  if (a.causal) {
     const int pos = len - n + i;
     hi = max(pos + 1, 0);
-    if (window > 0 && pos >= window) lo = pos - window + 1;
+    if (a.window > 0 && pos >= a.window) lo = pos - a.window + 1;
   }
+  hi = min(hi, a.s.width << a.c.shift);
 }
 
-__device__ inline int clamped_len(const AttnArgs& a, int b) {
-  return min(max(a.kv_len[b], 0), a.s.width << a.c.shift);
-}
+__device__ inline int length_of(const AttnArgs& a, int b) { return max(a.kv_len[b], 0); }
 
 __device__ inline void write_row(const AttnArgs& a, int64_t at, int n, const float* x) {
   if (a.out_f32) {
@@ -299,8 +299,8 @@ __device__ inline int over(int x, int y) { return (int)((unsigned)x / (unsigned)
 __device__ inline Parts parts_of(const AttnArgs& a, int len, int n, int r0) {
   Parts p;
   const int last = min(r0 + a.tile_rows, n * a.G) - 1;
-  row_range(len, n, over(r0, a.G), a.causal, a.window, p.lo, p.hi_first);
-  row_range(len, n, over(last, a.G), a.causal, a.window, p.lo_last, p.hi);
+  row_range(a, len, n, over(r0, a.G), p.lo, p.hi_first);
+  row_range(a, len, n, over(last, a.G), p.lo_last, p.hi);
   p.first = p.lo >> a.tile_shift;
   p.end = max(p.first, (p.hi + (1 << a.tile_shift) - 1) >> a.tile_shift);
   p.span = max(a.span_tiles, p.end - p.first);
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   const int h = at_wg.h, sp = at_wg.part, tile_row = at_wg.low, b = at_wg.high;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int len = clamped_len(a, b);
+  const int len = length_of(a, b);
   int row0, n;
   kv_rows(a.s, b, row0, n);
   const int rows = n * a.G, r0 = tile_row * kRowTile;
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   const int r = min(r0 + col, rows - 1);
   const int i = over(r, a.G), hq = h * a.G + r - i * a.G;
   int my_lo, my_hi;
-  row_range(len, n, i, a.causal, a.window, my_lo, my_hi);
+  row_range(a, len, n, i, my_lo, my_hi);
 
   // query fragments: slots (g, e) of step 2c + u are dims 64c + 16g + 8u + e
   half8 q[kSteps];
@@ -714,7 +714,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   };
   const int guess = sp * a.span_tiles;
   int id0 = blocks_at(guess), id1 = blocks_at(guess + kBatch), id2 = blocks_at(guess + 2 * kBatch);
-  const int len = clamped_len(a, b);
+  const int len = length_of(a, b);
   int row0, n;
   kv_rows(a.s, b, row0, n);
   const int rows = n * a.G, r0 = tile_row * C::kRows;
@@ -733,10 +733,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   for (int s = 0; s < kSteps; ++s)
     qraw[s] = load8(a.q, a.q_f32, (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs + 8 * half + 16 * s);
   int my_lo, my_hi;
-  row_range(len, n, i, a.causal, a.window, my_lo, my_hi);
+  row_range(a, len, n, i, my_lo, my_hi);
   int w_lo, w_hi, w_lo_last, w_hi_first;
-  row_range(len, n, over(min(w0, rows - 1), a.G), a.causal, a.window, w_lo, w_hi_first);
-  row_range(len, n, over(min(w0 + 31, rows - 1), a.G), a.causal, a.window, w_lo_last, w_hi);
+  row_range(a, len, n, over(min(w0, rows - 1), a.G), w_lo, w_hi_first);
+  row_range(a, len, n, over(min(w0 + 31, rows - 1), a.G), w_lo_last, w_hi);
   if (w0 >= rows) w_hi = 0;
   // its stages: a0 .. a1 - 1 (none: a0 == a1)
   const int a0 = min(max(t0, w_lo / kStage), t1);
@@ -1072,7 +1072,7 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
   int row0, n;
   kv_rows(a.s, b, row0, n);
   if (i >= n) return;
-  const int len = clamped_len(a, b);
+  const int len = length_of(a, b);
   // the row tile this row was in, as the split kernel saw it
   const int r = i * a.G + hq - over(hq, a.G) * a.G;
   const Parts pt = parts_of(a, len, n, over(r, a.tile_rows) * a.tile_rows);
@@ -1352,7 +1352,7 @@ extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_s
   a.q_f32 = t.q_dtype == MSQ_DTYPE_F32;
   a.out_f32 = t.out_dtype == MSQ_DTYPE_F32;
   a.causal = t.causal != 0;
-  a.window = std::min(t.window, 1 << 30);
+  a.window = t.window;
   a.nsplit = p.nsplit;
   a.span_tiles = p.span_tiles;
   a.row_tiles = p.row_tiles;

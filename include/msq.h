@@ -457,7 +457,8 @@ typedef struct {
   int32_t q_dtype;
   int32_t q_heads;         /* a multiple of kv_heads; query head h reads kv head
                               h / (q_heads / kv_heads) */
-  const int32_t *kv_len;   /* [batch]: tokens of each sequence in the cache */
+  const int32_t *kv_len;   /* [batch]: tokens of each sequence; those past its table are not
+                              seen, and its rows stand where they would with them.  Below 0: 0 */
   int64_t max_kv_len;      /* about the largest kv_len, for the split of the work (any value
                               gives right results); 0: table_width * block_tokens */
   float scale;             /* of the scores, finite and > 0; 0: 1 / sqrt(head_dim) */

@@ -91,3 +91,47 @@ def test_attention_one_token_at_scores_of_any_size(msq, D):
             size = 0.05 * np.abs(q.astype(np.float64)) @ np.abs(k)
             e = size * ((D + 32) * 2.0 ** -24 + 2.0 ** -22) + 2.0 ** -16
             assert (np.abs(lse.cpu().numpy() - 0.05 * (q.astype(np.float64) @ k)) <= e).all()
+
+
+# ---------------------------------------------------------------- lengths past the table
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_length_past_the_table(msq, D):
+    """A kv_len past what its table holds: the rows stand at its end all the same, and see those of
+    the tokens up to there that the table has."""
+    P, G, T = 32, 2, 96
+    table = np.array([[2, 0, 1]])
+    p = Pair(msq, 3, 1, D, P, seed=32)
+    p.write(table, [0], [T], torch.float32)
+    rng = np.random.default_rng(D)
+    k, v = (p.ref.values(name, table[0], 0, T) for name in "kv")
+    for n, L in ((1, 97), (1, 120), (50, 97), (50, 120), (50, 146), (50, 500), (50, 2 ** 31 - 1), (3, 2 ** 31 - 1)):
+        q, qt = rounded(rng.normal(size=(n, G, D)), torch.bfloat16)
+        pos = L - n + np.arange(n, dtype=np.int64)[:, None]
+        for window in (0, 40, 2 ** 31 - 1):
+            mask = np.arange(T)[None] <= pos
+            if window:
+                mask &= np.arange(T)[None] > pos - window
+            want, wl, absum, size, big = O.attention(q, k, v, mask, 1 / np.sqrt(D), p.ref.scale["v"][table[0][np.arange(T) // P]])
+            e = size * (D + 32) * 2.0 ** -24 + 2.0 ** -20
+            bound = absum * (2 * e + 2.0 ** -11 + 2.0 ** -18 + (T + 64) * 2.0 ** -24)[..., None] \
+                + (T * 2.0 ** -31 * 127 * big)[..., None] + 1e-37
+            calls = [(table, [L], [n])]
+            if n * G > 64:
+                calls.append(crowd(1, G, D, P, table, [L], [n], window if window < 1000 else 0))
+            for tb, lens, counts in calls:
+                print(f"D={D} n={n} L={L} window={window} batch={len(lens)}", flush=True)
+                got, lse = msq.kv_attention(qt, p.gpu, i32(tb), i32(lens), i32(offsets(counts)), max_count=n,
+                                            window=window, out_dtype=torch.float32, return_lse=True)
+                torch.cuda.synchronize()
+                got, lse = got.cpu().numpy(), lse.cpu().numpy()
+                assert (np.abs(got - want) <= bound).all()
+                none = ~mask.any(1)
+                assert (got[none] == 0).all() and np.isneginf(lse[none]).all() and np.isfinite(lse[~none]).all()
+    # nobody is masked without causal
+    q, qt = rounded(rng.normal(size=(2, G, D)), torch.bfloat16)
+    a = msq.kv_attention(qt, p.gpu, i32(table), i32([T]), causal=False)
+    b = msq.kv_attention(qt, p.gpu, i32(table), i32([2 ** 31 - 1]), causal=False)
+    c = msq.kv_attention(qt, p.gpu, i32(table), i32([-5]), causal=False)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and not bool(c.any())
