@@ -182,10 +182,13 @@ __device__ inline void query_fragments(const Raw8 (&raw)[N], int f32, half8 (&q)
 }
 
 // Log2 and inverse of a value scale; -inf and 0 for a block of zeros, whose
-// weights then come out 0.
+// weights then come out 0.  A block before a window may never have been written:
+// all its weights are of masked tokens, and no scale that it holds, an infinite
+// one among them, may make more of them than 0 (a written scale is at most 2^121).
 __device__ inline void value_scale(float s, float& lam, float& inv) {
-  lam = s >= kTiny ? log2_fast(s) : -INFINITY;
-  inv = s >= kTiny ? __builtin_amdgcn_rcpf(s) : 0.f;
+  const bool some = s >= kTiny && s < INFINITY;
+  lam = some ? log2_fast(s) : -INFINITY;
+  inv = some ? __builtin_amdgcn_rcpf(s) : 0.f;
 }
 
 // A score s * f, rounded (and no part of an fma).

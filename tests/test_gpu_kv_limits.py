@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 
-def ways(H, G, D, P, table, L, n):
+def ways(H, G, D, P, table, L, n, window=0):
     """(kv_attention's block table, kv_len, counts) of one sequence with n query rows, alone and
     so that the work is split; for more than 64 rows of a head also so that the kernel for
     many rows takes it, unsplit and split."""
@@ -19,8 +19,9 @@ def ways(H, G, D, P, table, L, n):
     yield table, [L], [n]
     yield wide(400), [L], [n]
     if n * G > 64:
-        yield crowd(H, G, D, P, table, [L], [n])
-        yield wide(450_000_000 // (H * -(-n * G // 16) * 2 * D * P) + 1), [L], [n]
+        yield crowd(H, G, D, P, table, [L], [n], window)
+        if not window:
+            yield wide(450_000_000 // (H * -(-n * G // 16) * 2 * D * P) + 1), [L], [n]
 
 
 # ---------------------------------------------------------------- scores of any finite size
@@ -135,3 +136,25 @@ def test_attention_length_past_the_table(msq, D):
     c = msq.kv_attention(qt, p.gpu, i32(table), i32([-5]), causal=False)
     torch.cuda.synchronize()
     assert torch.equal(a, b) and not bool(c.any())
+
+
+# ---------------------------------------------------------------- blocks that nothing was written to
+
+@pytest.mark.parametrize("fill", [float("inf"), float("nan"), 3e38, -1.0])
+@pytest.mark.parametrize("D,G", [(64, 3), (128, 2), (256, 2)])
+def test_attention_window_over_unwritten_blocks(msq, D, G, fill):
+    """A cache whose first blocks were never written (a sequence that came with a window): whatever
+    their scales hold, nothing of them is seen."""
+    P, L, n, w = 32, 256, 40, 50
+    table = np.array([[3, 1, 6, 0, 7, 2, 5, 4]])
+    p = Pair(msq, 8, 1, D, P, seed=33, fill=fill)
+    first = L - n - w + 1  # 167: in the second half of 64 tokens
+    p.write(table, [160], [L - 160], torch.float32)
+    assert first // 64 * 64 < 160 <= first
+    q, qt = rounded(np.random.default_rng(D).normal(size=(n, G, D)), torch.bfloat16)
+    for rows in (1, n):
+        for tb, lens, counts in ways(1, G, D, P, table, L, rows, w):
+            got, lse = msq.kv_attention(qt[-rows:], p.gpu, i32(tb), i32(lens), i32(offsets(counts)), max_count=rows,
+                                        window=w, out_dtype=torch.float32, return_lse=True)
+            torch.cuda.synchronize()
+            p.close(got, lse, q[-rows:], table[0], L, torch.bfloat16, True, w, 1 / np.sqrt(D))
