@@ -12,7 +12,9 @@
 // A block whose values are all 0 (or below 2^-93, which count as 0) adds to the
 // denominator only.  Whatever its scores, they say nothing of the size of O, so
 // its tokens have a reference Mz and a sum Lz of their own, joined to M and L at
-// the end.
+// the end.  The same goes for the denominator of a block whose scale is more than
+// 2^64 below the largest that its wavefront has met: at weights that its values
+// no longer reach, its scores can still be the ones that count.
 //
 // M is only moved when some weight would pass 2^14 (f16 ends at 2^16), and
 // then to 6 below the maximum: most tiles need neither the cross-lane maximum
@@ -63,6 +65,8 @@ constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100: value scales below 
 constexpr int kSpan = 32;          // tokens of a tile of k_kv_decode
 constexpr int kRowTile = 16;       // and its query rows
 constexpr int kMostParts = 64;     // parts of a row tile's tokens
+constexpr uint32_t kNoScale = 0x72000000;  // 2^101, inverse of less than any scale
+constexpr uint32_t kFaint = 64u << 23;  // 2^64, between the bit patterns of two scales' inverses
 constexpr float kTinyStep = 1e-37f;  // keeps -inf * step from being NaN where a step is 0
 
 struct AttnArgs {
@@ -217,8 +221,8 @@ __device__ inline float one_reference(float& M, float off, float& L) {
   return g;
 }
 
-// Scores s (times f; -inf where masked) of a block of zeros into Mz and Lz; the
-// lanes lane ^ kFirst * m have the same row.
+// Scores s (times f; -inf where masked) of a block of zeros, or a faint one, into Mz
+// and Lz; the lanes lane ^ kFirst * m have the same row.
 template <int kFirst, int N>
 __device__ inline void add_zeros(const float (&s)[N], float f, float& Mz, float& Lz) {
   float most = s[0];
@@ -232,6 +236,39 @@ __device__ inline void add_zeros(const float (&s)[N], float f, float& Mz, float&
   for (int e = 0; e < N; ++e) sum += exp2_fast(score_of(s[e], f) - m);
   Lz = fmaf(Lz, exp2_fast(Mz - m), sum);
   Mz = m;
+}
+
+// Blocks by the bits of their values' inverse scale, `in` (0: zeros), beside the least
+// so far, of the largest scale; all the same in a wavefront.  One comparison tells
+// a block of zeros, a faint one or a new least from all others.
+__device__ inline bool is_special(uint32_t in, uint32_t least) { return in - least > kFaint; }
+// Takes such a block in: its scores s (as for add_zeros) into Mz and Lz, or, where the
+// blocks before it are faint beside it, their sum L, a share of it in each of the
+// row's lanes.  Returns what its weights have in L: their factor 1 / s, or 0.
+template <int kFirst, int N>
+__device__ inline uint32_t add_special(uint32_t in, const float (&s)[N], float f, uint32_t& least,
+                                       float M, float off, float& L, float& Mz, float& Lz) {
+  if (in == 0 || in > least) {
+    add_zeros<kFirst>(s, f, Mz, Lz);
+    return 0;
+  }
+  if (least - in > kFaint) {
+    float l = L;
+#pragma unroll
+    for (int x = kFirst; x < 64; x <<= 1) l = fmaxf(l, __shfl_xor(l, x));
+    const float m = l > 0.f ? fmaxf(Mz, M + (off + log2_fast(l))) : Mz;
+    Lz = fmaf(Lz, exp2_fast(Mz - m), l > 0.f ? L * exp2_fast((M - m) + off) : L);
+    Mz = m;
+    L = 0.f;
+  }
+  least = in;
+  return in;
+}
+
+// l times 2^x in two steps: l may be as large as 2^x is small.
+__device__ inline float times_exp2(float l, float x) {
+  const float g = exp2_fast(0.5f * x);
+  return l * g * g;
 }
 
 // The sums of a row's lanes joined, and Mz and Lz joined to M and L; O is to be
@@ -423,6 +460,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   for (int d = 0; d < kTiles; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
   // limit: of the exponents x + log2 s, M + kTop; -inf for a row whose off is in use
   float M = kNone, off = 0.f, limit = kNone, L = 0.f, Mz = kNone, Lz = 0.f;
+  uint32_t least = kNoScale;
 
   // Lane j holds the block and the scales of this wavefront's j-th tile (of a
   // batch of 64), so that a tile's loads wait for no chain of their own.
@@ -449,7 +487,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
     // lane (col, g): scores of row col at tokens 4g + 0..3 and 16 + 4g + 0..3
     const float f = fmaxf(cq * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sk), j)), kTinyStep);
     const float lm = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lam), j));
-    const float in = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(inv), j));
+    const uint32_t in = __builtin_amdgcn_readlane(__float_as_int(inv), j);
     const int tok = t * kSpan;
     if (tok < lo1 || tok + kSpan > hi0) {
 #pragma unroll
@@ -459,9 +497,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
         if (p + 16 < my_lo || p + 16 >= my_hi) s1[e] = -INFINITY;
       }
     }
-    if (__float_as_int(in) == 0) {
+    uint32_t in_l = in;
+    if (is_special(in, least)) {
       const float z[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-      add_zeros<16>(z, f, Mz, Lz);
+      in_l = add_special<16>(in, z, f, least, M, off, L, Mz, Lz);
     }
     float most = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
                        fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
@@ -496,7 +535,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
       sum += w;
       p[e] = (_Float16)w;
     }
-    L = fmaf(sum, in, L);
+    L = fmaf(sum, __uint_as_float(in_l), L);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       const uint4 v = tl.v[c];
@@ -548,9 +587,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   for (int e = 0; e < kPer; ++e) x[e] = 0.f;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    const float f = exp2_fast(lo_m[w * 16 + rr] - m);
-    l += f * lo_l[w * 16 + rr];
-    const float fo = f * lo_g[w * 16 + rr];
+    const float up = lo_m[w * 16 + rr] - m;
+    l += times_exp2(lo_l[w * 16 + rr], up);
+    const float fo = exp2_fast(up) * lo_g[w * 16 + rr];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[e] += fo * lo_o[(w * 16 + rr) * kStride + d0 + e];
   }
@@ -612,7 +651,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = fmaxf(top, ml[j].x);
       const float al = exp2_fast(m - top);
-      l *= al;
+      l = times_exp2(l, m - top);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) x[e] *= al;
       m = top;
@@ -620,7 +659,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
       for (int j = 0; j < 4; ++j) {
         if (p0 + j >= parts) break;
         const float w = exp2_fast(ml[j].x - m);
-        l = fmaf(w, ml[j].y, l);
+        l += times_exp2(ml[j].y, ml[j].x - m);
 #pragma unroll
         for (int e = 0; e < kPer / 2; ++e) {
           x[2 * e] = fmaf(w, v[j][e].x, x[2 * e]);
@@ -750,6 +789,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   for (int d = 0; d < kTiles; ++d) o[d] = f32x16{};
   // limit: of the sums of weights; below all of them for a row whose off is in use
   float M = kNone, off = 0.f, limit = kTopWeight, L = 0.f, Mz = kNone, Lz = 0.f;
+  uint32_t least = kNoScale;
 
   // The strips' scales, held like their blocks and read a batch ahead.
   const int P = 1 << a.c.shift;
@@ -916,7 +956,15 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     use(15);
     // Every weight is below 2^kTop unless some lane's sum is not (a sum of NaN is
     // a row of NaN); only then is M moved and are the weights made again.
-    if (__float_as_int(inv) != 0 && __any(sum > limit)) {
+    const uint32_t in = __float_as_uint(inv);
+    uint32_t in_l = in;
+    if (is_special(in, least)) {
+      float z[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z[e] = s[e];
+      in_l = add_special<32>(in, z, f, least, M, off, L, Mz, Lz);
+    }
+    if (in != 0 && __any(sum > limit)) {
       float most = s[0];
 #pragma unroll
       for (int e = 1; e < 16; ++e) most = fmaxf(most, s[e]);
@@ -938,13 +986,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
         pairs[e >> 1][e & 1] = (_Float16)y;
       }
     }
-    if (__float_as_int(inv) == 0) {
-      float z[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) z[e] = s[e];
-      add_zeros<32>(z, f, Mz, Lz);
-    }
-    L = fmaf(sum, inv, L);
+    L = fmaf(sum, __uint_as_float(in_l), L);
     asm volatile("" : "+v"(L));
 #pragma unroll
     for (int e = 0; e < 16; ++e) p[e >> 3][e & 7] = pairs[e >> 1][e & 1];
@@ -1097,7 +1139,7 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
   const float f = exp2_fast(ml.x - m);
-  float l = f * ml.y;
+  float l = times_exp2(ml.y, ml.x - m);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
 #pragma unroll

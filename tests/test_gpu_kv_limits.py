@@ -158,3 +158,35 @@ def test_attention_window_over_unwritten_blocks(msq, D, G, fill):
                                         window=w, out_dtype=torch.float32, return_lse=True)
             torch.cuda.synchronize()
             p.close(got, lse, q[-rows:], table[0], L, torch.bfloat16, True, w, 1 / np.sqrt(D))
+
+
+# ---------------------------------------------------------------- value scales
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("low,high,gap", [(-85, 20, 20), (-85, 105, 20), (-85, 105, 90), (-85, -30, 40),
+                                          (-20, 50, 45), (-85, 105, 500), (-85, 105, 3000)])
+def test_attention_value_scales_far_apart_under_the_top_scores(msq, D, low, high, gap):
+    """Blocks of values near 2^low whose scores are e^gap above those of values near 2^high, up to
+    2^190 apart: the error stays relative to the largest contribution, whichever it is, and lse
+    is that of the scores; in any order, in one wavefront, in several, and in several parts."""
+    P, H, G = 32, 1, 2
+    rng = np.random.default_rng(D + gap)
+    unit = np.sign(rng.normal(size=D))
+    for blocks, lows in ((2, [0]), (2, [1]), (14, [0, 3, 4]), (14, [13]), (14, [0, 1, 2, 3, 5, 6, 8, 9, 10, 11, 12])):
+        L = blocks * P
+        table = rng.permutation(blocks)[None]
+        p = Pair(msq, blocks, H, D, P, seed=34)
+        k, v = rng.normal(size=(blocks, P, H, D)) * 0.01, p.tokens(L).reshape(blocks, P, H, D)
+        v *= 2.0 ** high
+        v[lows] *= 2.0 ** (low - high)
+        k[lows] += unit * gap / D
+        v = v.clip(-3e38, 3e38)
+        p.write(table, [0], [L], torch.float32, k=k.reshape(L, H, D), v=v.reshape(L, H, D))
+        for n in (1, 40):
+            q = unit + rng.normal(size=(n, G, D)) * 0.01
+            for tb, lens, counts in ways(H, G, D, P, table, L, n):
+                print(f"D={D} {low} {high} {gap} blocks={blocks} {lows} n={n} batch={len(lens)} "
+                      f"width={np.shape(tb)[1]}", flush=True)
+                full = np.zeros((sum(counts), G, D))
+                full[:n] = q
+                p.attend(full, tb, lens, counts, scale=1.0)
