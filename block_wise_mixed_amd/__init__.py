@@ -113,7 +113,19 @@ class _KvAttn(ctypes.Structure):
                 ("lse", ctypes.c_void_p)]
 
 
+_KV_CACHE = struct.Struct("@qiiiPPPP")  # the fields of _KvCache
 _KV_ATTN = struct.Struct("@PqqiiPqfiiPiP")  # the fields of _KvAttn
+_KV_CACHE_FIELDS = frozenset(("num_blocks", "kv_heads", "head_dim", "block_tokens", "k_codes",
+                              "v_codes", "k_scale", "v_scale"))
+
+
+def _pack(fields: struct.Struct, to, what: str, *values) -> None:
+    """All fields of a ctypes structure at once (a third of the time that its constructor takes);
+    values that do not fit raise instead of wrapping around."""
+    try:
+        fields.pack_into(to, 0, *values)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"{what}: {e}") from None
 
 
 def load_library():
@@ -518,7 +530,8 @@ KV_BLOCK_TOKENS = (32, 64, 128, 256)
 class KVCache:
     """Device buffers of an 8-bit key/value cache: blocks of block_tokens tokens, one fp32
     scale per block and head (layout and quantiser: include/msq.h).  Block tables say which
-    blocks a sequence has; handing blocks out is the caller's."""
+    blocks a sequence has; handing blocks out is the caller's.  Fields may be set anew (a
+    cache that grows or moves): the next call checks and uses them."""
     num_blocks: int
     kv_heads: int
     head_dim: int
@@ -529,17 +542,37 @@ class KVCache:
     v_scale: "object"
 
     def __post_init__(self):
-        d = _KvCache()
-        d.num_blocks, d.kv_heads = self.num_blocks, self.kv_heads
-        d.head_dim, d.block_tokens = self.head_dim, self.block_tokens
-        d.k_codes, d.v_codes = self.k_codes.data_ptr(), self.v_codes.data_ptr()
-        d.k_scale, d.v_scale = self.k_scale.data_ptr(), self.v_scale.data_ptr()
-        self._desc = d
-        self._index = self.k_codes.get_device()
-        self.device = self.k_codes.device
+        self.descriptor()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name in _KV_CACHE_FIELDS:
+            object.__setattr__(self, "_desc", None)
 
     def descriptor(self) -> _KvCache:
+        if self._desc is None:
+            torch = _torch()
+            scales = self.num_blocks * self.kv_heads
+            sizes = {"k_codes": scales * self.block_tokens * self.head_dim, "k_scale": scales}
+            index = self.k_codes.get_device()
+            for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+                t, codes = getattr(self, name), name.endswith("codes")
+                want, numel = (torch.uint8, sizes["k_codes"]) if codes else (torch.float32, sizes["k_scale"])
+                if t.dtype is not want or t.numel() != numel or not t.is_contiguous() or \
+                        t.get_device() != index or t.device.type != self.k_codes.device.type:
+                    raise ValueError(f"{name} must be contiguous {want} of {numel} values, on the "
+                                     "device of the other buffers")
+            d = _KvCache()
+            _pack(_KV_CACHE, d, "the cache's sizes", self.num_blocks, self.kv_heads, self.head_dim,
+                  self.block_tokens, self.k_codes.data_ptr(), self.v_codes.data_ptr(),
+                  self.k_scale.data_ptr(), self.v_scale.data_ptr())
+            self._index = index
+            self._desc = d
         return self._desc
+
+    @property
+    def device(self):
+        return self.k_codes.device
 
     @property
     def nbytes(self) -> int:
@@ -646,6 +679,7 @@ def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: i
     which is the number of tokens it has in the cache (negative: leave the sequence out).
     offset: int32 [batch + 1], sequence b's rows are offset[b] .. offset[b + 1] - 1; None:
     rows / batch each.  max_count: the largest sequence's rows, if known (else all rows)."""
+    desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
     if stream is not None or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (k, v, block_table, first, offset),
@@ -657,7 +691,7 @@ def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: i
         raise ValueError("k and v must have the same rows and type")
     s, keep = _kv_seqs(cache, block_table, offset, rows, max_count)
     first = _kv_index(first, "first", s.batch, index)
-    status = load_library().msq_kv_write(cache._desc, s, first.data_ptr(), k_at, k_st, k_sh, v_at,
+    status = load_library().msq_kv_write(desc, s, first.data_ptr(), k_at, k_st, k_sh, v_at,
                                          v_st, v_sh, code, cuda._cuda_getCurrentRawStream(index))
     if status:
         raise MsqError(status, "msq_kv_write")
@@ -668,6 +702,7 @@ def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int
     """Read positions first[b] .. first[b] + rows - 1 of every sequence back (msq_kv_read):
     (k, v), [total][kv_heads][head_dim] of dtype (bf16 unless given; or fp32), code * scale.
     offset as in kv_write, total its last entry; with offset None, total / batch rows each."""
+    desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
     if stream is not None or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (block_table, first, offset),
@@ -681,7 +716,7 @@ def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int
     code = _kv_dtype(dtype)
     k = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=dtype, device=cache.device)
     v = torch.empty_like(k)
-    status = load_library().msq_kv_read(cache._desc, s, first.data_ptr(), k.data_ptr(),
+    status = load_library().msq_kv_read(desc, s, first.data_ptr(), k.data_ptr(),
                                         v.data_ptr(), code, cuda._cuda_getCurrentRawStream(index))
     if status:
         raise MsqError(status, "msq_kv_read")
@@ -699,7 +734,8 @@ def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch:
     s = _KvSeqs(batch, width, None, 1, rows, max_count)  # of offset only whether it is there
     a = _KvAttn()
     a.q_heads, a.max_kv_len, a.causal, a.window = q_heads, max_kv_len, int(causal), window
-    return int(load_library().msq_kv_attention_workspace_bytes(cache._desc, s, a))
+    desc = cache._desc or cache.descriptor()
+    return int(load_library().msq_kv_attention_workspace_bytes(desc, s, a))
 
 
 def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count: int = 0,
@@ -716,6 +752,7 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     unless out or out_dtype says fp32), with return_lse also the fp32 [rows][q_heads] natural
     log of each row's softmax denominator.  A query that sees nothing gives zeros and -inf.
     workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
+    desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
     if stream is not None or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (q, block_table, kv_len, offset, out, workspace),
@@ -745,11 +782,11 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     except struct.error as e:
         raise ValueError(f"max_kv_len, scale or window: {e}") from None
     if workspace is None:
-        need = int(lib.msq_kv_attention_workspace_bytes(cache._desc, s, a))
+        need = int(lib.msq_kv_attention_workspace_bytes(desc, s, a))
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the cache's device")
-    status = lib.msq_kv_attention(cache._desc, s, a, workspace.data_ptr(),
+    status = lib.msq_kv_attention(desc, s, a, workspace.data_ptr(),
                                   workspace.numel() * workspace.element_size(),
                                   cuda._cuda_getCurrentRawStream(index))
     if status:

@@ -190,3 +190,25 @@ def test_attention_value_scales_far_apart_under_the_top_scores(msq, D, low, high
                 full = np.zeros((sum(counts), G, D))
                 full[:n] = q
                 p.attend(full, tb, lens, counts, scale=1.0)
+
+
+# ---------------------------------------------------------------- a cache whose buffers change
+
+def test_cache_that_grows(msq):
+    """Buffers set anew between calls are the ones that the next call uses."""
+    p = Pair(msq, 2, 2, 64, 32, seed=35)
+    p.write([[0, 1]], [0], [64])
+    old = p.gpu.k_codes, p.gpu.k_codes.clone()
+    k0, v0 = msq.kv_read(p.gpu, i32([[0, 1]]), i32([0]), total=64)
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        t = getattr(p.gpu, name)
+        setattr(p.gpu, name, torch.cat([torch.zeros_like(t), t]))
+    p.gpu.num_blocks = 4
+    k1, v1 = msq.kv_read(p.gpu, i32([[2, 3]]), i32([0]), total=64)
+    x = torch.randn(32, 2, 64, device="cuda")
+    msq.kv_write(p.gpu, x, x, i32([[1]]), i32([0]))
+    q = torch.randn(1, 4, 64, device="cuda")
+    a = msq.kv_attention(q, p.gpu, i32([[2, 3]]), i32([64]))
+    torch.cuda.synchronize()
+    assert torch.equal(k0, k1) and torch.equal(v0, v1)
+    assert torch.equal(*old) and bool(p.gpu.k_scale[1].any()) and bool(a.any())

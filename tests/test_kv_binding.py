@@ -1,0 +1,58 @@
+"""The Python binding of the key/value cache, without a GPU: its cache object and what it refuses."""
+import pytest
+
+import block_wise_mixed_amd as msq
+
+torch = pytest.importorskip("torch")
+
+
+def make(blocks=4, heads=2, dim=64, tokens=32):
+    return msq.allocate_kv_cache(blocks, heads, dim, tokens, device="cpu")
+
+
+def addresses(c):
+    d = c.descriptor()
+    return d.num_blocks, d.k_codes, d.v_codes, d.k_scale, d.v_scale
+
+
+def held(c):
+    return (c.num_blocks, c.k_codes.data_ptr(), c.v_codes.data_ptr(), c.k_scale.data_ptr(),
+            c.v_scale.data_ptr())
+
+
+def test_cache_fields_set_anew():
+    """A cache that grows: the descriptor follows the fields, and is not made again without need."""
+    c = make()
+    assert addresses(c) == held(c)
+    assert c.descriptor() is c.descriptor()
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        t = getattr(c, name)
+        setattr(c, name, torch.cat([t, torch.zeros_like(t)]))
+    c.num_blocks = 8
+    assert addresses(c) == held(c) and c.descriptor().num_blocks == 8
+    assert c.nbytes == 2 * 8 * 2 * 32 * 64 + 2 * 8 * 2 * 4
+    old = c.descriptor()
+    c.v_scale = c.v_scale.clone()
+    assert c.descriptor() is not old and addresses(c) == held(c)
+
+
+def test_cache_fields_that_do_not_fit():
+    c = make()
+    good = dict(num_blocks=4, kv_heads=2, head_dim=64, block_tokens=32, k_codes=c.k_codes,
+                v_codes=c.v_codes, k_scale=c.k_scale, v_scale=c.v_scale)
+    msq.KVCache(**good)
+    wide = torch.zeros(4, 2, 2 * 32 * 64, dtype=torch.uint8)
+    for bad in (dict(num_blocks=5), dict(kv_heads=3), dict(block_tokens=64), dict(head_dim=128),
+                dict(k_codes=c.k_codes[:3]), dict(v_codes=c.v_codes.to(torch.int8)),
+                dict(k_scale=c.k_scale[:3]), dict(v_scale=c.v_scale.double()),
+                dict(k_codes=wide[..., ::2]), dict(v_scale=torch.zeros(8, 2)[::2]),
+                dict(v_codes=c.v_codes.to("meta"))):
+        with pytest.raises(ValueError):
+            msq.KVCache(**{**good, **bad})
+        for name, value in bad.items():
+            d = make()
+            setattr(d, name, value)
+            with pytest.raises(ValueError):
+                d.descriptor()
+            with pytest.raises(ValueError):
+                msq.kv_attention_workspace_bytes(d, 4, 2, 4, 1, 100)
