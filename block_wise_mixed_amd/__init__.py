@@ -31,7 +31,7 @@ __all__ = ["MsqError", "PackedWeight", "plan", "quantize_pack", "allocate_packed
            "library_path", "load_library", "KERNELS", "FORMAT_VERSION", "GEMV_MAX_M",
            "allocate_bits", "alloc_workspace_bytes", "ALLOC_LEVELS", "reorder_channels",
            "KVCache", "allocate_kv_cache", "kv_write", "kv_read", "kv_attention",
-           "kv_attention_workspace_bytes", "KV_HEAD_DIMS", "KV_BLOCK_TOKENS"]
+           "kv_attention_workspace_bytes", "kv_attention_plan", "KV_HEAD_DIMS", "KV_BLOCK_TOKENS"]
 
 FORMAT_VERSION = 2
 GEMV_MAX_M = 64
@@ -113,6 +113,12 @@ class _KvAttn(ctypes.Structure):
                 ("lse", ctypes.c_void_p)]
 
 
+class _KvPlan(ctypes.Structure):
+    _fields_ = [("tile_rows", ctypes.c_int32), ("wavefronts", ctypes.c_int32),
+                ("parts", ctypes.c_int32), ("join", ctypes.c_int32),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 _KV_CACHE = struct.Struct("@qiiiPPPP")  # the fields of _KvCache
 _KV_ATTN = struct.Struct("@PqqiiPqfiiPiP")  # the fields of _KvAttn
 _KV_CACHE_FIELDS = frozenset(("num_blocks", "kv_heads", "head_dim", "block_tokens", "k_codes",
@@ -181,6 +187,8 @@ def load_library():
     lib.msq_kv_write.restype = ctypes.c_int
     lib.msq_kv_read.argtypes = [cache_p, seqs_p, vp, vp, vp, ctypes.c_int32, vp]
     lib.msq_kv_read.restype = ctypes.c_int
+    lib.msq_kv_attention_plan.argtypes = [cache_p, seqs_p, attn_p, ctypes.POINTER(_KvPlan)]
+    lib.msq_kv_attention_plan.restype = ctypes.c_int
     lib.msq_kv_attention_workspace_bytes.argtypes = [cache_p, seqs_p, attn_p]
     lib.msq_kv_attention_workspace_bytes.restype = sz
     lib.msq_kv_attention.argtypes = [cache_p, seqs_p, attn_p, vp, sz, vp]
@@ -736,6 +744,23 @@ def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch:
     a.q_heads, a.max_kv_len, a.causal, a.window = q_heads, max_kv_len, int(causal), window
     desc = cache._desc or cache.descriptor()
     return int(load_library().msq_kv_attention_workspace_bytes(desc, s, a))
+
+
+def kv_attention_plan(cache: KVCache, rows: int, q_heads: int, batch: int, table_entries: int,
+                      max_count: int = 0, max_kv_len: int = 0, causal: bool = True, window: int = 0,
+                      ragged: bool = True) -> dict:
+    """How kv_attention runs a call of these sizes (msq_kv_attention_plan): tile_rows and
+    wavefronts of its kernel's workgroups, the parts that a tile's tokens are split into, join
+    ("none", "inside" the launch or by a "launch" of its own) and workspace_bytes.  Arguments as
+    of kv_attention; ragged: whether it is given an offset."""
+    s = _KvSeqs(batch, table_entries, None, 1 if ragged else None, rows, max_count)
+    a = _KvAttn()
+    a.q_heads, a.max_kv_len, a.causal, a.window = q_heads, max_kv_len, int(causal), window
+    plan = _KvPlan()
+    _check(load_library().msq_kv_attention_plan(cache._desc or cache.descriptor(), s, a, plan),
+           "msq_kv_attention_plan")
+    return dict(tile_rows=plan.tile_rows, wavefronts=plan.wavefronts, parts=plan.parts,
+                join=("none", "inside", "launch")[plan.join], workspace_bytes=plan.workspace_bytes)
 
 
 def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count: int = 0,

@@ -1342,6 +1342,25 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
 
 using namespace msq;
 
+extern "C" msq_status msq_kv_attention_plan(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
+                                            const msq_kv_attn* attn, msq_kv_plan* plan) {
+  if (!attn || !plan) return MSQ_ERR_INVALID_ARG;
+  KvCacheView c;
+  KvSeqsView s;
+  AttnPlan p;
+  msq_status st = kv_views(cache, seqs, c, s);
+  if (st == MSQ_OK) st = plan_attn(c, s, *attn, cache->head_dim, p);
+  if (st != MSQ_OK) return st;
+  *plan = msq_kv_plan{};
+  if (p.blocks == 0) return MSQ_OK;
+  plan->tile_rows = p.tile_rows;
+  plan->wavefronts = p.waves ? p.waves : 4;
+  plan->parts = p.nsplit;
+  plan->join = p.nsplit == 1 ? 0 : p.tags_at ? 1 : 2;
+  plan->workspace_bytes = p.workspace;
+  return MSQ_OK;
+}
+
 extern "C" size_t msq_kv_attention_workspace_bytes(const msq_kv_cache* cache,
                                                    const msq_kv_seqs* seqs,
                                                    const msq_kv_attn* attn) {

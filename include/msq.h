@@ -471,6 +471,22 @@ typedef struct {
                               -inf for a row that sees nothing */
 } msq_kv_attn;
 
+/* How msq_kv_attention runs a call. */
+typedef struct {
+  int32_t tile_rows;  /* query rows of a head that a workgroup takes: 16 (few rows), or 32 for
+                         each of its wavefronts (many rows) */
+  int32_t wavefronts; /* of a workgroup */
+  int32_t parts;      /* workgroups that share the tokens of such a tile, at most */
+  int32_t join;       /* of their results: 0 none, 1 in the same launch, 2 a launch of its own */
+  size_t workspace_bytes; /* what this call needs */
+} msq_kv_plan;
+
+/* The plan of a call, from the sizes that msq_kv_attention_workspace_bytes looks
+ * at (an empty call: zeros).  No device is used.
+ * Errors: MSQ_ERR_INVALID_ARG, MSQ_ERR_SHAPE, MSQ_ERR_UNSUPPORTED. */
+msq_status msq_kv_attention_plan(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
+                                 const msq_kv_attn *attn, msq_kv_plan *plan);
+
 /* Bytes of device workspace msq_kv_attention needs (0 for arguments it
  * refuses and for calls that need none).  Only sizes are looked at: batch,
  * table_width, total, max_count, whether offset is null, q_heads, max_kv_len,
