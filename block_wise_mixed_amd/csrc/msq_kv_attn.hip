@@ -1197,9 +1197,126 @@ constexpr int kJoinInside = 16, kJoinFloats = 8192;
 constexpr int64_t decode_bytes(int D) { return D == 256 ? 240000000 : 400000000; }
 constexpr int kFewRows = 64;
 
-// Sizes only; MSQ_OK with blocks == 0 for an empty call.
+// A workgroup size of k_kv_prefill: wavefronts, workgroups that the GPU runs at once,
+// time of a stage, stages that its start and end take the time of, and the
+// stages of a sequence for which it is considered.
+//
+// With 8 wavefronts a strip is converted for twice the rows.  Head dim 128: two
+// wavefronts a SIMD either way, and workgroups of 4 only fill the GPU better
+// where sequences are short (4 and 8 wavefronts: 4 x 1024 rows of 8 heads on
+// 1500 tokens 94, 86 us, 1024 on 8192 166, 142; 256 on 512 22.1, 23.8).  64: three
+// workgroups of 4 a compute unit or one of 8, a tile 1.73 to 1 in time (2048 rows
+// of 128 heads on 16000 tokens 1337, 1180 us; 8 x 512 of 64 on 2000 158, 164).
+struct Way {
+  int waves;
+  int64_t slots;
+  double tile;
+  int64_t start, from, to;
+};
+constexpr int64_t kAny = (int64_t)1 << 40;
+constexpr Way kWays64[2] = {{4, 768, 1.73, 4, 1, kAny}, {8, 256, 1, 10, 1, kAny}};
+constexpr Way kWays128[2] = {{4, 512, 1, 4, 1, 16}, {8, 256, 1, 4, 17, kAny}};
+constexpr Way kWays256[2] = {{4, 256, 1, 4, 1, kAny}, {4, 256, 1, 4, kAny, 0}};
+const Way* ways_of(int D) { return D == 64 ? kWays64 : D == 128 ? kWays128 : kWays256; }
+
+// What the plans of a call's sizes have in common, for any length of its sequences.
+struct Shape {
+  int D;
+  int64_t rows, lists;  // query rows of a head, (sequence, kv head) pairs
+  int64_t outputs;      // (query row, head) pairs of all sequences
+  bool join;            // the join's grid of (sequence, row, head) fits one launch
+
+  int64_t all(int tile_rows) const { return lists * ((rows + tile_rows - 1) / tile_rows); }
+  // A tile's tokens may be in several parts where the most parts of all tiles fit one launch.
+  int64_t most_parts(int64_t items) const {
+    return join && items <= kMostThreads / 512 / kMostParts ? kMostParts : 1;
+  }
+  // k_kv_decode's tiles of 32 tokens of `tiles` in a part
+  int64_t decode_span(int64_t tiles) const {
+    const int64_t want = decode_parts();
+    return std::min<int64_t>(std::max<int64_t>(tiles <= 12 ? 12 : 4, (tiles + want - 1) / want), 256);
+  }
+  int64_t decode_fill() const { return D == 256 ? 256 : 512; }
+  int64_t decode_parts() const { return std::max<int64_t>(1, decode_fill() / all(kRowTile)); }
+  int64_t decode_tiles() const { return decode_bytes(D) / (2 * D * kSpan); }
+  // k_kv_prefill's cost of n parts: rounds of workgroups over the GPU (in fractions where three
+  // share a compute unit), each its stages and some more to start and end; where there are
+  // several parts, 3 for the join's launch and their traffic (8 MB in the time of a stage).
+  double rounds(const Way& w, int64_t n) const {
+    const int64_t work = all(32 * w.waves) * n;
+    return w.slots == 768 ? std::max(1., (double)work / 768) : (double)((work + w.slots - 1) / w.slots);
+  }
+  double joining(int64_t n) const { return n > 1 ? 3 + (double)outputs * D * 8 / 8e6 * (double)n : 0; }
+
+  size_t partials(int64_t parts) const {  // bytes of the parts' sums
+    return parts > 1 ? ((size_t)(outputs * parts) * D * 4 + 255) / 256 * 256 : 0;
+  }
+  size_t workspace(int64_t parts) const {  // and of M and L
+    return parts > 1 ? partials(parts) + (size_t)(outputs * parts) * 8 : 0;
+  }
+  int64_t tagged_parts() const {  // the most that the launch itself joins
+    return std::min<int64_t>(kJoinInside, kJoinFloats / (std::min<int64_t>(rows, kRowTile) * D));
+  }
+  size_t tags_at(int64_t parts) const { return (workspace(parts) + 255) / 256 * 256; }
+  size_t tags_end(int64_t parts) const {
+    return tags_at(parts) + (size_t)all(kRowTile) * kMostParts * 8;
+  }
+};
+
+// The most workspace that any plan for sequences of up to `longest` tokens needs: more
+// tokens can mean fewer parts, since a part's tokens are a whole number of tiles.
+size_t most_workspace(const Shape& z, int64_t longest) {
+  // k_kv_decode: as many parts as wanted or of 4 tiles, or those of 256 tiles
+  int64_t tiles = std::max<int64_t>(1, (longest + kSpan - 1) / kSpan);
+  if (z.rows > kFewRows) tiles = std::min(tiles, z.decode_tiles() / z.all(kRowTile));
+  int64_t parts = 1;
+  if (tiles > 12)
+    parts = std::max(std::min(z.decode_parts(), (tiles + 3) / 4), (tiles + 255) / 256);
+  parts = std::min(parts, z.most_parts(z.all(kRowTile)));
+  size_t most = z.workspace(parts);
+  if (const int64_t tagged = std::min(parts, z.tagged_parts()); tagged > 1)
+    most = std::max(most, z.tags_end(tagged));
+  if (z.rows <= kFewRows) return most;
+  // k_kv_prefill: the largest n whose cost is, for some number of stages x that is not
+  // beyond `longest`, not above that of any smaller m, with x / n for n's stages a part
+  // and (x + m - 1) / m for m's, the least and the most that they can be: each m
+  // leaves an interval of x.
+  const int64_t stages = std::max<int64_t>(1, (longest + 63) / 64);
+  const Way* ways = ways_of(z.D);
+  for (int i = 0; i < 2; ++i) {
+    const Way& w = ways[i];
+    const int64_t end = std::min(stages, w.to);
+    for (int64_t n = std::min(end, z.most_parts(z.all(32 * w.waves))); n > 1; --n) {
+      if (z.workspace(n) <= most) break;
+      double lo = (double)std::max(n, w.from), hi = (double)end;
+      const double slope = z.rounds(w, n) * w.tile / (double)n;
+      const double fixed = z.rounds(w, n) * (double)w.start * w.tile + z.joining(n);
+      for (int j = 0; j < 2 && lo <= hi; ++j) {
+        const Way& v = ways[j];
+        if ((double)v.from > lo || (double)v.to < hi) continue;
+        for (int64_t m = 1; m <= n && lo <= hi; ++m) {
+          if (i == j && m == n) continue;
+          const double a = slope - z.rounds(v, m) * v.tile / (double)m;
+          const double b = z.rounds(v, m) * ((double)(m - 1) / (double)m + (double)v.start) * v.tile +
+                           z.joining(m) - fixed + 1e-9 * fixed;
+          if (a > 0) hi = std::min(hi, b / a);
+          else if (a < 0) lo = std::max(lo, b / a);
+          else if (b < 0) hi = lo - 1;
+        }
+      }
+      if (lo <= hi) {
+        most = z.workspace(n);
+        break;
+      }
+    }
+  }
+  return most;
+}
+
+// Sizes only; MSQ_OK with blocks == 0 for an empty call.  most: also the most
+// workspace of calls with shorter sequences.
 msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_attn& t, int D,
-                     AttnPlan& p) {
+                     AttnPlan& p, size_t* most = nullptr) {
   p = AttnPlan{};
   if (t.q_heads < 1 || t.q_heads % c.H != 0 || t.window < 0 || t.max_kv_len < 0)
     return MSQ_ERR_SHAPE;
@@ -1212,15 +1329,16 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   int64_t longest = (int64_t)s.width << c.shift;
   if (t.max_kv_len > 0) longest = std::min(longest, t.max_kv_len);
   if (t.window > 0) longest = std::min<int64_t>(longest, (int64_t)t.window + s.max_count + kSpan);
-  const int64_t rows = s.max_count * G, lists = (int64_t)s.batch * c.H;
+  const Shape z{D, s.max_count * G, (int64_t)s.batch * c.H, (int64_t)s.total * t.q_heads,
+                (int64_t)s.batch * s.max_count * G <= kMostThreads / 256 / c.H};
   const int64_t most_blocks = kMostThreads / 512;
-  if (lists > most_blocks) return MSQ_ERR_SHAPE;
+  if (z.lists > most_blocks) return MSQ_ERR_SHAPE;
   int64_t items = 0, tiles = 0, span = 0;
   auto cut = [&](int tile_rows, int tile_tokens) {
     p.tile_rows = tile_rows;
     p.tile_tokens = tile_tokens;
-    p.row_tiles = (int)((rows + tile_rows - 1) / tile_rows);
-    items = lists * p.row_tiles;
+    p.row_tiles = (int)((z.rows + tile_rows - 1) / tile_rows);
+    items = z.all(tile_rows);
     tiles = std::max<int64_t>(1, (longest + tile_tokens - 1) / tile_tokens);
   };
   // k_kv_decode.  Parts: about two workgroups a compute unit (one at D = 256, whose
@@ -1232,65 +1350,34 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   // sequences of 2000 on 4 heads: 8 and 16 parts 15.5, 20.3 us.
   cut(kRowTile, kSpan);
   if (items > 16 * most_blocks) return MSQ_ERR_SHAPE;  // a sixteenth as many of k_kv_prefill are too
-  const int64_t fill = D == 256 ? 256 : 512;
-  const int64_t want = std::max<int64_t>(1, fill / items);
-  span = std::min<int64_t>(std::max<int64_t>(tiles <= 12 ? 12 : 4, (tiles + want - 1) / want), 256);
-  const int64_t at_work = std::max(fill, items * ((tiles + span - 1) / span));
-  p.waves = 0;
-  if (rows > kFewRows && at_work * std::min(span, tiles) > decode_bytes(D) / (2 * D * kSpan)) {
-    // k_kv_prefill.  Parts: the number that takes the least time, counted in tiles:
-    // rounds of workgroups over the GPU (in fractions where three share a compute
-    // unit), each its tiles and some more to start and end; where there are
-    // several parts, 3 for the join's launch and their traffic (8 MB in the time of
-    // a tile).
+  span = z.decode_span(tiles);
+  const int64_t at_work = std::max(z.decode_fill(), items * ((tiles + span - 1) / span));
+  if (z.rows > kFewRows && at_work * std::min(span, tiles) > z.decode_tiles()) {
+    // k_kv_prefill, with the parts that cost least
+    const int64_t stages = (longest + Prefill<128, 8>::kStage - 1) / Prefill<128, 8>::kStage;
     double least = 1e300;
-    auto consider = [&](int waves, int64_t slots, double tile, int64_t start) {
-      const int64_t rows_of = 32 * waves, all = lists * ((rows + rows_of - 1) / rows_of);
-      const int64_t stages = (longest + Prefill<128, 8>::kStage - 1) / Prefill<128, 8>::kStage;
-      const double traffic = (double)s.total * t.q_heads * D * 8 / 8e6;
-      for (int64_t n = 1; n <= std::min<int64_t>(kMostParts, stages); ++n) {
+    for (int i = 0; i < 2; ++i) {
+      const Way& w = ways_of(D)[i];
+      if (stages < w.from || stages > w.to) continue;
+      for (int64_t n = 1; n <= std::min(z.most_parts(z.all(32 * w.waves)), stages); ++n) {
         const int64_t each = (stages + n - 1) / n;
-        const double rounds = slots == 768 ? std::max(1., (double)(all * n) / 768)
-                                           : (double)((all * n + slots - 1) / slots);
-        const double cost = rounds * (double)(each + start) * tile + (n > 1 ? 3 + traffic * (double)n : 0);
-        if (cost < least) least = cost, p.waves = waves, span = each;
+        const double cost = z.rounds(w, n) * (double)(each + w.start) * w.tile + z.joining(n);
+        if (cost < least) least = cost, p.waves = w.waves, span = each;
       }
-    };
-    // With 8 wavefronts a strip is converted for twice the rows.  Head dim 128: two
-    // wavefronts a SIMD either way, and workgroups of 4 only fill the GPU better
-    // where sequences are short (4 and 8 wavefronts: 4 x 1024 rows of 8 heads on
-    // 1500 tokens 94, 86 us, 1024 on 8192 166, 142; 256 on 512 22.1, 23.8).  64: three
-    // workgroups of 4 a compute unit or one of 8, a tile 1.73 to 1 in time (2048 rows
-    // of 128 heads on 16000 tokens 1337, 1180 us; 8 x 512 of 64 on 2000 158, 164).
-    if (D == 64) {
-      consider(4, 768, 1.73, 4);
-      consider(8, 256, 1, 10);
-    } else if (D == 128 && longest > 1024) {
-      consider(8, 256, 1, 4);
-    } else {
-      consider(4, D == 128 ? 512 : 256, 1, 4);
     }
     cut(32 * p.waves, Prefill<128, 8>::kStage);
   }
-  p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, kMostParts);
-  // unsplit where the parts, or the join's grid of (sequence, row, head), would pass
-  // one launch
-  if (items * p.nsplit > most_blocks ||
-      (int64_t)s.batch * s.max_count * G > kMostThreads / 256 / c.H)
-    p.nsplit = 1;
+  p.nsplit = (int)std::min<int64_t>((tiles + span - 1) / span, z.most_parts(items));
   p.span_tiles = (int)((tiles + p.nsplit - 1) / p.nsplit);
   p.blocks = items * p.nsplit;
   if (p.blocks > most_blocks) return MSQ_ERR_SHAPE;
-  if (p.nsplit > 1) {
-    const size_t partials = (size_t)s.total * t.q_heads * p.nsplit;
-    p.ml_at = (partials * D * 4 + 255) / 256 * 256;
-    p.workspace = p.ml_at + partials * 8;
-    if (!p.waves && p.nsplit <= kJoinInside &&
-        std::min<int64_t>(rows, kRowTile) * p.nsplit * D <= kJoinFloats) {
-      p.tags_at = (p.workspace + 255) / 256 * 256;
-      p.workspace = p.tags_at + (size_t)items * kMostParts * 8;
-    }
+  p.ml_at = z.partials(p.nsplit);
+  p.workspace = z.workspace(p.nsplit);
+  if (!p.waves && p.nsplit > 1 && p.nsplit <= z.tagged_parts()) {
+    p.tags_at = z.tags_at(p.nsplit);
+    p.workspace = z.tags_end(p.nsplit);
   }
+  if (most) *most = std::max(p.workspace, most_workspace(z, longest));
   return MSQ_OK;
 }
 
@@ -1368,8 +1455,9 @@ extern "C" size_t msq_kv_attention_workspace_bytes(const msq_kv_cache* cache,
   KvSeqsView s;
   AttnPlan p;
   if (!attn || kv_views(cache, seqs, c, s) != MSQ_OK) return 0;
-  if (plan_attn(c, s, *attn, cache->head_dim, p) != MSQ_OK) return 0;
-  return p.workspace;
+  size_t most = 0;
+  if (plan_attn(c, s, *attn, cache->head_dim, p, &most) != MSQ_OK) return 0;
+  return most;
 }
 
 extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs,

@@ -487,11 +487,13 @@ typedef struct {
 msq_status msq_kv_attention_plan(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
                                  const msq_kv_attn *attn, msq_kv_plan *plan);
 
-/* Bytes of device workspace msq_kv_attention needs (0 for arguments it
- * refuses and for calls that need none).  Only sizes are looked at: batch,
- * table_width, total, max_count, whether offset is null, q_heads, max_kv_len,
- * causal and window.  Fewer sequences can need more, since theirs are split
- * further: a buffer for calls of several sizes takes the largest. */
+/* Bytes of device workspace that msq_kv_attention needs at most for calls of
+ * these sizes with a max_kv_len, table_width or window as given or smaller (0 for
+ * arguments it refuses and where none of them needs any).  Only sizes are
+ * looked at: batch, table_width, total, max_count, whether offset is null,
+ * q_heads, max_kv_len, causal and window.  Fewer sequences can need more, since
+ * theirs are split further: a buffer for calls of several batches takes the
+ * largest. */
 size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
                                         const msq_kv_attn *attn);
 
