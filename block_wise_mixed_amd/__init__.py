@@ -735,13 +735,13 @@ def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch:
                                  max_count: int, max_kv_len: int, causal: bool = True,
                                  window: int = 0) -> int:
     """Workspace of kv_attention for calls of these sizes (rows: query rows of all sequences)
-    whose block tables have no more entries than max_kv_len tokens need.  Fewer sequences can
-    need more, since theirs are split further: a buffer for calls of several sizes takes the
-    largest."""
-    width = max(1, -(-max_kv_len // cache.block_tokens))
+    whose block tables have no more entries than max_kv_len tokens need, whatever max_kv_len they
+    are given.  Fewer sequences can need more, since theirs are split further: a buffer for calls
+    of several batches takes the largest."""
+    width = max(1, -(-max_kv_len // cache.block_tokens))  # the table's length stands for max_kv_len
     s = _KvSeqs(batch, width, None, 1, rows, max_count)  # of offset only whether it is there
     a = _KvAttn()
-    a.q_heads, a.max_kv_len, a.causal, a.window = q_heads, max_kv_len, int(causal), window
+    a.q_heads, a.causal, a.window = q_heads, int(causal), window
     desc = cache._desc or cache.descriptor()
     return int(load_library().msq_kv_attention_workspace_bytes(desc, s, a))
 

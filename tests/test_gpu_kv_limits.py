@@ -212,3 +212,24 @@ def test_cache_that_grows(msq):
     torch.cuda.synchronize()
     assert torch.equal(k0, k1) and torch.equal(v0, v1)
     assert torch.equal(*old) and bool(p.gpu.k_scale[1].any()) and bool(a.any())
+
+
+# ---------------------------------------------------------------- the example's workspace
+
+@pytest.mark.parametrize("most", [2049, 2100, 130])
+def test_example_with_lengths_inside_a_block(msq, most):
+    """The example's decode steps with the workspace that it keeps, sized for tokens that end inside
+    a block: 4 sequences, 32 heads on 8 of 128."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import cached_attention as ex
+    layer = ex.CachedAttention(128, 32, 8, 128, 4, most)
+    layer(torch.randn(4 * 5, 128, device="cuda").bfloat16())
+    for _ in range(3):
+        x = torch.randn(4, 128, device="cuda").bfloat16()
+        y, q, a = layer(x, workspace=layer.workspace)
+        own = msq.kv_attention(q, layer.cache, layer.table, layer.length)
+        torch.cuda.synchronize()
+        assert torch.equal(a, own) and torch.isfinite(y).all()
+    assert layer.length.tolist() == [8] * 4

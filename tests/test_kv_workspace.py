@@ -42,3 +42,18 @@ def test_a_buffer_for_the_widest_window_serves_all(lib):
             assert lib.msq_kv_attention_plan(c, s, a, p) == 0
             need = max(need, p.workspace_bytes)
             assert lib.msq_kv_attention_workspace_bytes(c, s, a) >= need
+
+
+@pytest.mark.parametrize("batch,H,G,D", [(4, 8, 4, 128), (1, 8, 4, 128), (2, 4, 4, 256), (8, 2, 8, 64)])
+def test_binding_size_serves_calls_without_max_kv_len(batch, H, G, D):
+    """A buffer for max_kv_len tokens is enough for a call that leaves max_kv_len to the table, which
+    ends inside its last block; 2049 tokens with blocks of 64 among them."""
+    pytest.importorskip("torch")
+    for P in (64, 256):
+        c = msq.allocate_kv_cache(1, H, D, P, device="cpu")
+        for L in [2049, *range(1, 4200, 5)]:
+            size = msq.kv_attention_workspace_bytes(c, batch, H * G, batch, 1, L)
+            for given in (0, L, L // 2):
+                for ragged in (False, True):
+                    plan = msq.kv_attention_plan(c, batch, H * G, batch, -(-L // P), 1, given, ragged=ragged)
+                    assert size >= plan["workspace_bytes"], (L, given)
