@@ -13,6 +13,7 @@
 // bytes.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -191,6 +192,7 @@ struct WriteArgs {
   const void *k, *v;
   int64_t kts, khs, vts, vhs;
   int reach;
+  unsigned begin;  // task of the launch's first workgroup
 };
 
 // A wavefront takes 32 slots x E dims (64 where the workgroup's 16 wavefronts
@@ -202,7 +204,7 @@ template <int D, int E, typename T>
 __global__ __launch_bounds__(1024) void k_kv_write(WriteArgs a) {
   using Mp = Map<E>;
   __shared__ float part_max[16];
-  const Task tk = task_of(blockIdx.x, a.c.H, a.reach);
+  const Task tk = task_of(a.begin + blockIdx.x, a.c.H, a.reach);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -339,6 +341,7 @@ struct ReadArgs {
   const int32_t* first;
   void *k, *v;
   int reach;
+  unsigned begin;
 };
 
 __device__ inline void store8(uint16_t* p, const float* x) {
@@ -360,7 +363,7 @@ __device__ inline void store8(float* p, const float* x) {
 template <int D, typename T>
 __global__ __launch_bounds__(512) void k_kv_read(ReadArgs a) {
   using Mp = Map<D>;
-  const Task tk = task_of(blockIdx.x, a.c.H, a.reach);
+  const Task tk = task_of(a.begin + blockIdx.x, a.c.H, a.reach);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int P = 1 << a.c.shift;
@@ -439,28 +442,42 @@ int64_t reach_of(const KvSeqsView& s, int shift) {
   return (n + P - 2) / P + 1;
 }
 
+// One launch, or as many as it takes at fewer than 2^32 threads each.
+template <typename Args, typename Go>
+msq_status launch_all(Args& a, unsigned blocks, int threads, Go&& go) {
+  const unsigned most = (unsigned)(kMostThreads / threads);
+  for (unsigned done = 0; done < blocks; done += most) {
+    a.begin = done;
+    go(dim3(std::min(blocks - done, most)), dim3(threads));
+    if (hipGetLastError() != hipSuccess) return MSQ_ERR_HIP;
+    if (blocks - done <= most) break;
+  }
+  return MSQ_OK;
+}
+
 template <int D, typename T>
-void launch_write(unsigned blocks, const WriteArgs& a, hipStream_t stream) {
+msq_status launch_write(unsigned blocks, WriteArgs& a, hipStream_t stream) {
   const int strips = 1 << (a.c.shift - 5);
   auto go = [&](auto dims) {
     constexpr int E = decltype(dims)::value;
     const int waves = strips * (D / E);
-    hipLaunchKernelGGL((k_kv_write<D, E, T>), dim3(blocks), dim3(64 * waves),
-                       waves * Map<E>::kImage, stream, a);
+    return launch_all(a, blocks, 64 * waves, [&](dim3 grid, dim3 block) {
+      hipLaunchKernelGGL((k_kv_write<D, E, T>), grid, block, waves * Map<E>::kImage, stream, a);
+    });
   };
   // More wavefronts shorten the coding of a run (2011 tokens of 8 heads of 128:
   // 10.7 -> 7.9 us) and idle where a block gets a token or two (256 single
   // tokens: 10.9 -> 14.4 us).
   if (a.s.max_count >= 16 && strips * (D / 64) <= 16)
-    go(std::integral_constant<int, 64>{});
-  else
-    go(std::integral_constant<int, D < 128 ? 64 : 128>{});
+    return go(std::integral_constant<int, 64>{});
+  return go(std::integral_constant<int, D < 128 ? 64 : 128>{});
 }
 template <int D, typename T>
-void launch_read(unsigned blocks, const ReadArgs& a, hipStream_t stream) {
+msq_status launch_read(unsigned blocks, ReadArgs& a, hipStream_t stream) {
   const int waves = 1 << (a.c.shift - 5);
-  hipLaunchKernelGGL((k_kv_read<D, T>), dim3(blocks), dim3(64 * waves), waves * Map<D>::kImage,
-                     stream, a);
+  return launch_all(a, blocks, 64 * waves, [&](dim3 grid, dim3 block) {
+    hipLaunchKernelGGL((k_kv_read<D, T>), grid, block, waves * Map<D>::kImage, stream, a);
+  });
 }
 
 }  // namespace
@@ -515,10 +532,11 @@ msq_status kv_pointers(const msq_kv_cache* cache, const msq_kv_seqs* seqs) {
 
 namespace {
 
-// Checks that write and read share; *blocks: the launch's workgroups.
+// Checks that write and read share; *reach: the most blocks of a sequence that the call works
+// on (table_only: those that the table has), *blocks: its workgroups.
 msq_status kv_common(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const int32_t* first,
-                     const void* k, const void* v, int32_t dtype, KvCacheView& c, KvSeqsView& s,
-                     int64_t* reach, int64_t* blocks) {
+                     const void* k, const void* v, int32_t dtype, bool table_only, KvCacheView& c,
+                     KvSeqsView& s, int64_t* reach, int64_t* blocks) {
   msq_status st = kv_views(cache, seqs, c, s);
   if (st != MSQ_OK) return st;
   if (dtype != MSQ_DTYPE_BF16 && dtype != MSQ_DTYPE_F32) return MSQ_ERR_INVALID_ARG;
@@ -529,9 +547,9 @@ msq_status kv_common(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const i
   if (!first || !k || !v || !aligned_to(first, 4) || !aligned_to(k, 16) || !aligned_to(v, 16))
     return MSQ_ERR_INVALID_ARG;
   *reach = reach_of(s, c.shift);
+  if (table_only) *reach = std::min<int64_t>(*reach, s.width);
   const int64_t lists = (int64_t)s.batch * *reach;  // < 2^31 * 2^27
-  // workgroups of up to 1024 threads; a launch holds fewer than 2^32
-  if (lists > kMostThreads / 1024 / 2 / c.H) return MSQ_ERR_SHAPE;
+  if (lists > 0x7FFFFFFF / 2 / c.H) return MSQ_ERR_SHAPE;
   *blocks = lists * 2 * c.H;
   return MSQ_OK;
 }
@@ -547,7 +565,7 @@ extern "C" msq_status msq_kv_write(const msq_kv_cache* cache, const msq_kv_seqs*
                                    int64_t v_head_stride, int32_t dtype, hipStream_t stream) {
   WriteArgs a{};
   int64_t reach = 0, blocks = 0;
-  const msq_status st = kv_common(cache, seqs, first, k, v, dtype, a.c, a.s, &reach, &blocks);
+  const msq_status st = kv_common(cache, seqs, first, k, v, dtype, true, a.c, a.s, &reach, &blocks);
   if (st != MSQ_OK || blocks == 0) return st;
   const int64_t per16 = dtype == MSQ_DTYPE_F32 ? 4 : 8;
   if (k_token_stride % per16 || k_head_stride % per16 || v_token_stride % per16 ||
@@ -564,11 +582,10 @@ extern "C" msq_status msq_kv_write(const msq_kv_cache* cache, const msq_kv_seqs*
   const bool f32 = dtype == MSQ_DTYPE_F32;
   const unsigned n = (unsigned)blocks;
   switch (cache->head_dim) {
-    case 64: f32 ? launch_write<64, float>(n, a, stream) : launch_write<64, uint16_t>(n, a, stream); break;
-    case 128: f32 ? launch_write<128, float>(n, a, stream) : launch_write<128, uint16_t>(n, a, stream); break;
-    default: f32 ? launch_write<256, float>(n, a, stream) : launch_write<256, uint16_t>(n, a, stream); break;
+    case 64: return f32 ? launch_write<64, float>(n, a, stream) : launch_write<64, uint16_t>(n, a, stream);
+    case 128: return f32 ? launch_write<128, float>(n, a, stream) : launch_write<128, uint16_t>(n, a, stream);
+    default: return f32 ? launch_write<256, float>(n, a, stream) : launch_write<256, uint16_t>(n, a, stream);
   }
-  return hipGetLastError() == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
 }
 
 extern "C" msq_status msq_kv_read(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
@@ -576,7 +593,7 @@ extern "C" msq_status msq_kv_read(const msq_kv_cache* cache, const msq_kv_seqs* 
                                   hipStream_t stream) {
   ReadArgs a{};
   int64_t reach = 0, blocks = 0;
-  const msq_status st = kv_common(cache, seqs, first, k, v, dtype, a.c, a.s, &reach, &blocks);
+  const msq_status st = kv_common(cache, seqs, first, k, v, dtype, false, a.c, a.s, &reach, &blocks);
   if (st != MSQ_OK || blocks == 0) return st;
   a.first = first;
   a.k = k;
@@ -585,9 +602,8 @@ extern "C" msq_status msq_kv_read(const msq_kv_cache* cache, const msq_kv_seqs* 
   const bool f32 = dtype == MSQ_DTYPE_F32;
   const unsigned n = (unsigned)blocks;
   switch (cache->head_dim) {
-    case 64: f32 ? launch_read<64, float>(n, a, stream) : launch_read<64, uint16_t>(n, a, stream); break;
-    case 128: f32 ? launch_read<128, float>(n, a, stream) : launch_read<128, uint16_t>(n, a, stream); break;
-    default: f32 ? launch_read<256, float>(n, a, stream) : launch_read<256, uint16_t>(n, a, stream); break;
+    case 64: return f32 ? launch_read<64, float>(n, a, stream) : launch_read<64, uint16_t>(n, a, stream);
+    case 128: return f32 ? launch_read<128, float>(n, a, stream) : launch_read<128, uint16_t>(n, a, stream);
+    default: return f32 ? launch_read<256, float>(n, a, stream) : launch_read<256, uint16_t>(n, a, stream);
   }
-  return hipGetLastError() == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
 }

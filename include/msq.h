@@ -431,10 +431,11 @@ typedef struct {
  * first[b] + i; a sequence with first[b] < 0 is left out.  A block may be
  * written for one sequence only per call.  k, v: [total][kv_heads][head_dim]
  * of dtype, with token and head strides in elements (dims contiguous; 16-byte
- * aligned pointers and byte strides).  One launch, asynchronous.
+ * aligned pointers and byte strides).  One launch (more where 2^32 threads do not
+ * do), asynchronous.
  * Errors: MSQ_ERR_INVALID_ARG (null or misaligned pointer, unknown dtype),
  * MSQ_ERR_SHAPE (a size outside the ranges above, or batch * kv_heads *
- * blocks of max_count rows past what one launch takes, 2^21),
+ * blocks of max_count rows past 2^30; no more blocks than table_width count),
  * MSQ_ERR_UNSUPPORTED (head_dim or block_tokens not listed above),
  * MSQ_ERR_HIP. */
 msq_status msq_kv_write(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
@@ -444,8 +445,8 @@ msq_status msq_kv_write(const msq_kv_cache *cache, const msq_kv_seqs *seqs, cons
 
 /* Reads positions first[b] .. first[b] + count - 1 of every sequence back
  * into k and v ([total][kv_heads][head_dim] of dtype, contiguous, 16-byte
- * aligned): code * scale in fp32, rounded once more for bf16.  Errors as
- * msq_kv_write. */
+ * aligned): code * scale in fp32, rounded once more for bf16.  Launches and errors
+ * as msq_kv_write (all blocks of max_count rows count). */
 msq_status msq_kv_read(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
                        void *k, void *v, int32_t dtype, hipStream_t stream);
 

@@ -233,3 +233,32 @@ def test_example_with_lengths_inside_a_block(msq, most):
         torch.cuda.synchronize()
         assert torch.equal(a, own) and torch.isfinite(y).all()
     assert layer.length.tolist() == [8] * 4
+
+
+# ---------------------------------------------------------------- many sequences without max_count
+
+@pytest.mark.parametrize("D,P,H,batch,rows", [(64, 32, 1, 4096, 5), (256, 256, 2, 8192, 8)])
+def test_write_and_read_without_max_count(msq, D, P, H, batch, rows):
+    """Ragged batches that leave max_count to the rows of all sequences, which makes more workgroups
+    than one launch of 1024 threads each takes (and, for the second, more than one launch of
+    theirs): the same codes, scales and values as with max_count."""
+    width = -(-batch * rows // P) + 1
+    entry = np.arange(batch) % width
+    table = np.full((batch, width), -1)
+    table[np.arange(batch), entry] = np.random.default_rng(D).permutation(batch)
+    first, table = i32(entry * P + 5), i32(table)
+    offset = i32(np.arange(batch + 1) * rows)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    k, v = (torch.randn(batch * rows, H, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    a, b = (msq.allocate_kv_cache(batch, H, D, P) for _ in range(2))
+    for c in (a, b):
+        c.k_codes.zero_(), c.v_codes.zero_()
+    msq.kv_write(a, k, v, table, first, offset, max_count=rows)
+    msq.kv_write(b, k, v, table, first, offset)
+    want = msq.kv_read(a, table, first, offset, total=batch * rows, max_count=rows)
+    got = msq.kv_read(b, table, first, offset, total=batch * rows)
+    torch.cuda.synchronize()
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert float((got[0].float() - k.float()).abs().max()) <= float(a.k_scale.max()) * 0.51 + 2.0 ** -6
