@@ -668,6 +668,8 @@ def _kv_on(cache: KVCache, stream, tensors, call):
     """call() with the cache's device and the given stream current, so that what it allocates
     belongs to that stream; the tensors it was given are marked as used there."""
     torch = _torch()
+    if cache._index < 0:
+        raise ValueError(f"the cache is on {cache.device}: its operators run on a GPU")
     with torch.cuda.device(cache._index):
         with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream) as _:
             used = torch.cuda.current_stream()
@@ -689,7 +691,7 @@ def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: i
     rows / batch each.  max_count: the largest sequence's rows, if known (else all rows)."""
     desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
-    if stream is not None or cuda._cuda_getDevice() != index:
+    if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (k, v, block_table, first, offset),
                       lambda: kv_write(cache, k, v, block_table, first, offset, max_count))
     heads, dim = cache.kv_heads, cache.head_dim
@@ -712,7 +714,7 @@ def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int
     offset as in kv_write, total its last entry; with offset None, total / batch rows each."""
     desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
-    if stream is not None or cuda._cuda_getDevice() != index:
+    if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (block_table, first, offset),
                       lambda: kv_read(cache, block_table, first, offset, total, max_count, dtype))
     torch = _torch()
@@ -779,7 +781,7 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
     desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
-    if stream is not None or cuda._cuda_getDevice() != index:
+    if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
         return _kv_on(cache, stream, (q, block_table, kv_len, offset, out, workspace),
                       lambda: kv_attention(q, cache, block_table, kv_len, offset, max_count,
                                            max_kv_len, scale, causal, window, out, out_dtype,

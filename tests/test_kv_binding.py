@@ -56,3 +56,13 @@ def test_cache_fields_that_do_not_fit():
                 d.descriptor()
             with pytest.raises(ValueError):
                 msq.kv_attention_workspace_bytes(d, 4, 2, 4, 1, 100)
+
+
+def test_operators_refuse_a_cache_without_a_gpu():
+    c = make()
+    x, t = torch.zeros(2, 2, 64), torch.zeros(1, 2, dtype=torch.int32)
+    n = torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: msq.kv_write(c, x, x, t, n), lambda: msq.kv_read(c, t, n, total=2),
+                 lambda: msq.kv_attention(x, c, t, n)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
