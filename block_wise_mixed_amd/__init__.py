@@ -670,6 +670,8 @@ def _kv_on(cache: KVCache, stream, tensors, call):
     torch = _torch()
     if cache._index < 0:
         raise ValueError(f"the cache is on {cache.device}: its operators run on a GPU")
+    if stream is not None and stream.device_index != cache._index:
+        raise ValueError(f"the stream is on device {stream.device_index}, the cache on {cache.device}")
     with torch.cuda.device(cache._index):
         with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream) as _:
             used = torch.cuda.current_stream()

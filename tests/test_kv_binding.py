@@ -1,4 +1,6 @@
 """The Python binding of the key/value cache, without a GPU: its cache object and what it refuses."""
+import types
+
 import pytest
 
 import block_wise_mixed_amd as msq
@@ -65,4 +67,20 @@ def test_operators_refuse_a_cache_without_a_gpu():
     for call in (lambda: msq.kv_write(c, x, x, t, n), lambda: msq.kv_read(c, t, n, total=2),
                  lambda: msq.kv_attention(x, c, t, n)):
         with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+def test_operators_refuse_a_stream_of_another_device(monkeypatch):
+    """A cache that says it is on device 0 (its buffers are never reached) and a stream on 1."""
+    c = make()
+    monkeypatch.setattr(msq.KVCache, "device", torch.device("cuda", 0))
+    c.descriptor()
+    c._index = 0
+    stream = types.SimpleNamespace(device_index=1, cuda_stream=0)
+    x, t = torch.zeros(2, 2, 64), torch.zeros(1, 2, dtype=torch.int32)
+    n = torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: msq.kv_write(c, x, x, t, n, stream=stream),
+                 lambda: msq.kv_read(c, t, n, total=2, stream=stream),
+                 lambda: msq.kv_attention(x, c, t, n, stream=stream)):
+        with pytest.raises(ValueError, match="device 1"):
             call()
