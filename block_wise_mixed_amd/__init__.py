@@ -120,6 +120,7 @@ class _KvPlan(ctypes.Structure):
 
 
 _KV_CACHE = struct.Struct("@qiiiPPPP")  # the fields of _KvCache
+_KV_SEQS = struct.Struct("@iiPPqi")  # the fields of _KvSeqs
 _KV_ATTN = struct.Struct("@PqqiiPqfiiPiP")  # the fields of _KvAttn
 _KV_CACHE_FIELDS = frozenset(("num_blocks", "kv_heads", "head_dim", "block_tokens", "k_codes",
                               "v_codes", "k_scale", "v_scale"))
@@ -127,7 +128,7 @@ _KV_CACHE_FIELDS = frozenset(("num_blocks", "kv_heads", "head_dim", "block_token
 
 def _pack(fields: struct.Struct, to, what: str, *values) -> None:
     """All fields of a ctypes structure at once (a third of the time that its constructor takes);
-    values that do not fit raise instead of wrapping around."""
+    values that do not fit raise instead of wrapping around.  (The calls do the same in place.)"""
     try:
         fields.pack_into(to, 0, *values)
     except (struct.error, OverflowError) as e:
@@ -639,6 +640,15 @@ def _kv_rows(t, name, heads, dim, index):
     return t, shape[0], at, st, sh, code
 
 
+def _kv_seqs_struct(batch, width, table, offset, total, max_count) -> _KvSeqs:
+    s = _KvSeqs()
+    try:
+        _KV_SEQS.pack_into(s, 0, batch, width, table, offset, total, max_count)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"rows, max_count or block_table: {e}") from None
+    return s
+
+
 def _kv_index(t, name, count, index):
     """t as a contiguous int32 tensor of count entries on the cache's device."""
     if t.dtype is not _torch().int32 or t.dim() != 1 or t.numel() != count or t.get_device() != index:
@@ -658,9 +668,9 @@ def _kv_seqs(cache: KVCache, block_table, offset, total: int, max_count: int):
     if offset is None:
         if total % max(batch, 1) or (batch == 0 and total):
             raise ValueError("without offset every sequence has the same number of rows")
-        return _KvSeqs(batch, width, block_table.data_ptr(), None, total, max_count), block_table
+        return _kv_seqs_struct(batch, width, block_table.data_ptr(), 0, total, max_count), block_table
     offset = _kv_index(offset, "offset", batch + 1, cache._index)
-    return (_KvSeqs(batch, width, block_table.data_ptr(), offset.data_ptr(), total, max_count),
+    return (_kv_seqs_struct(batch, width, block_table.data_ptr(), offset.data_ptr(), total, max_count),
             (block_table, offset))
 
 
@@ -735,6 +745,14 @@ def kv_read(cache: KVCache, block_table, first, offset=None, total: Optional[int
     return k, v
 
 
+def _kv_sizes(rows, q_heads, batch, entries, max_count, max_kv_len, causal, window, ragged):
+    """What the size queries look at; of an offset only whether it is there."""
+    a = _KvAttn()
+    _pack(_KV_ATTN, a, "q_heads, max_kv_len or window", 0, 0, 0, 0, q_heads, 0, max_kv_len, 0.0,
+          1 if causal else 0, window, 0, 0, 0)
+    return _kv_seqs_struct(batch, entries, 0, 1 if ragged else 0, rows, max_count), a
+
+
 def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch: int,
                                  max_count: int, max_kv_len: int, causal: bool = True,
                                  window: int = 0) -> int:
@@ -743,9 +761,7 @@ def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch:
     are given.  Fewer sequences can need more, since theirs are split further: a buffer for calls
     of several batches takes the largest."""
     width = max(1, -(-max_kv_len // cache.block_tokens))  # the table's length stands for max_kv_len
-    s = _KvSeqs(batch, width, None, 1, rows, max_count)  # of offset only whether it is there
-    a = _KvAttn()
-    a.q_heads, a.causal, a.window = q_heads, int(causal), window
+    s, a = _kv_sizes(rows, q_heads, batch, width, max_count, 0, causal, window, True)
     desc = cache._desc or cache.descriptor()
     return int(load_library().msq_kv_attention_workspace_bytes(desc, s, a))
 
@@ -757,9 +773,7 @@ def kv_attention_plan(cache: KVCache, rows: int, q_heads: int, batch: int, table
     wavefronts of its kernel's workgroups, the parts that a tile's tokens are split into, join
     ("none", "inside" the launch or by a "launch" of its own) and workspace_bytes.  Arguments as
     of kv_attention; ragged: whether it is given an offset."""
-    s = _KvSeqs(batch, table_entries, None, 1 if ragged else None, rows, max_count)
-    a = _KvAttn()
-    a.q_heads, a.max_kv_len, a.causal, a.window = q_heads, max_kv_len, int(causal), window
+    s, a = _kv_sizes(rows, q_heads, batch, table_entries, max_count, max_kv_len, causal, window, ragged)
     plan = _KvPlan()
     _check(load_library().msq_kv_attention_plan(cache._desc or cache.descriptor(), s, a, plan),
            "msq_kv_attention_plan")
@@ -804,11 +818,11 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
         raise ValueError("out must be contiguous, [rows][q_heads][head_dim], on the cache's device")
     lse = torch.empty((rows, heads), dtype=torch.float32, device=cache.device) if return_lse else None
     a = _KvAttn()
-    try:  # all fields at once: a third of the time that the constructor takes
+    try:
         _KV_ATTN.pack_into(a, 0, q_at, q_st, q_sh, q_code, heads, kv_len.data_ptr(), max_kv_len,
                            scale, 1 if causal else 0, window, out.data_ptr(), _kv_dtype(out.dtype),
                            0 if lse is None else lse.data_ptr())
-    except struct.error as e:
+    except (struct.error, OverflowError) as e:
         raise ValueError(f"max_kv_len, scale or window: {e}") from None
     if workspace is None:
         need = int(lib.msq_kv_attention_workspace_bytes(desc, s, a))

@@ -84,3 +84,30 @@ def test_operators_refuse_a_stream_of_another_device(monkeypatch):
                  lambda: msq.kv_attention(x, c, t, n, stream=stream)):
         with pytest.raises(ValueError, match="device 1"):
             call()
+
+
+def test_sizes_that_do_not_fit_are_refused():
+    """Whole numbers past the C structs' fields raise; they do not wrap around."""
+    c = make()
+    table = torch.zeros(2, 3, dtype=torch.int32)
+    for n in (2 ** 32 + 5, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            msq._kv_seqs(c, table, None, 4, n)
+        for sizes in ((4, 2, 2, 1, 3, n), (4, 2, n, 1, 3, 1), (4, n, 2, 1, 3, 1)):
+            rows, heads, batch, count, entries, window = sizes
+            with pytest.raises(ValueError):
+                msq.kv_attention_plan(c, rows, heads, batch, entries, count, window=window)
+            with pytest.raises(ValueError):
+                msq.kv_attention_workspace_bytes(c, rows, heads, batch, count, 100, window=window)
+        with pytest.raises(ValueError):
+            msq.kv_attention_plan(c, 4, 2, 2, 3, n)
+    with pytest.raises(ValueError):
+        msq._kv_seqs(c, table, None, 2 ** 64, 0)
+    s, _ = msq._kv_seqs(c, table, None, 4, 2 ** 31 - 1)
+    assert (s.batch, s.table_width, s.total, s.max_count, s.offset) == (2, 3, 4, 2 ** 31 - 1, None)
+    o = torch.tensor([0, 1, 4], dtype=torch.int32)
+    s, _ = msq._kv_seqs(c, table, o, 4, 3)
+    assert (s.block_table, s.offset) == (table.data_ptr(), o.data_ptr())
+    assert msq._KV_SEQS.size <= 40 and msq._KV_ATTN.size <= 88 and msq._KV_CACHE.size == 56
+    with pytest.raises(ValueError):
+        msq._pack(msq._KV_ATTN, msq._KvAttn(), "scale", 0, 0, 0, 0, 2, 0, 0, "x", 1, 0, 0, 0, 0)
