@@ -252,7 +252,7 @@ __device__ inline uint32_t add_special(uint32_t in, const float (&s)[N], float f
     add_zeros<kFirst>(s, f, Mz, Lz);
     return 0;
   }
-  if (least - in > kFaint) {
+  if (least - in > kFaint && least != kNoScale) {
     float l = L;
 #pragma unroll
     for (int x = kFirst; x < 64; x <<= 1) l = fmaxf(l, __shfl_xor(l, x));
