@@ -201,15 +201,23 @@ __device__ inline float score_of(float s, float f) {
   return s * f;
 }
 
+// l times 2^x in two steps: l may be as large as 2^x is small.
+__device__ inline float times_exp2(float l, float x) {
+  const float g = exp2_fast(0.5f * x);
+  return l * g * g;
+}
+
 // Moves the reference of a row to the score `most` of a block whose values have
-// scale 2^lam; returns the factor of what was summed with the old one.
-__device__ inline float move_reference(float most, float lam, float& M, float& off, bool& far) {
+// scale 2^lam, and its sum L with it; returns the factor of O.
+__device__ inline float move_reference(float most, float lam, float& M, float& off, float& L,
+                                       bool& far) {
   far = fabsf(most) > kNear;
   const float m = far ? most : most + lam - kPlace, rest = far ? lam - kPlace : 0.f;
-  const float al = exp2_fast((M - m) + (off - rest));
+  const float up = (M - m) + (off - rest);
+  L = times_exp2(L, up);
   M = m;
   off = rest;
-  return al;
+  return exp2_fast(up);
 }
 
 // M + off as one number, M; what rounding takes from it goes to L and, as the
@@ -240,35 +248,13 @@ __device__ inline void add_zeros(const float (&s)[N], float f, float& Mz, float&
 
 // Blocks by the bits of their values' inverse scale, `in` (0: zeros), beside the least
 // so far, of the largest scale; all the same in a wavefront.  One comparison tells
-// a block of zeros, a faint one or a new least from all others.
+// a block of zeros, a faint one or a new least from all others; of these,
+// meet_scale returns true for the first two.
 __device__ inline bool is_special(uint32_t in, uint32_t least) { return in - least > kFaint; }
-// Takes such a block in: its scores s (as for add_zeros) into Mz and Lz, or, where the
-// blocks before it are faint beside it, their sum L, a share of it in each of the
-// row's lanes.  Returns what its weights have in L: their factor 1 / s, or 0.
-template <int kFirst, int N>
-__device__ inline uint32_t add_special(uint32_t in, const float (&s)[N], float f, uint32_t& least,
-                                       float M, float off, float& L, float& Mz, float& Lz) {
-  if (in == 0 || in > least) {
-    add_zeros<kFirst>(s, f, Mz, Lz);
-    return 0;
-  }
-  if (least - in > kFaint && least != kNoScale) {
-    float l = L;
-#pragma unroll
-    for (int x = kFirst; x < 64; x <<= 1) l = fmaxf(l, __shfl_xor(l, x));
-    const float m = l > 0.f ? fmaxf(Mz, M + (off + log2_fast(l))) : Mz;
-    Lz = fmaf(Lz, exp2_fast(Mz - m), l > 0.f ? L * exp2_fast((M - m) + off) : L);
-    Mz = m;
-    L = 0.f;
-  }
+__device__ inline bool meet_scale(uint32_t in, uint32_t& least) {
+  if (in == 0 || in > least) return true;
   least = in;
-  return in;
-}
-
-// l times 2^x in two steps: l may be as large as 2^x is small.
-__device__ inline float times_exp2(float l, float x) {
-  const float g = exp2_fast(0.5f * x);
-  return l * g * g;
+  return false;
 }
 
 // The sums of a row's lanes joined, and Mz and Lz joined to M and L; O is to be
@@ -497,10 +483,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
         if (p + 16 < my_lo || p + 16 >= my_hi) s1[e] = -INFINITY;
       }
     }
-    uint32_t in_l = in;
-    if (is_special(in, least)) {
+    uint32_t in_l = in;  // what its weights have in L
+    if (is_special(in, least) && meet_scale(in, least)) {
       const float z[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-      in_l = add_special<16>(in, z, f, least, M, off, L, Mz, Lz);
+      add_zeros<16>(z, f, Mz, Lz);
+      in_l = 0;
     }
     float most = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])),
                        fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
@@ -510,9 +497,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
       most = score_of(fmaxf(most, __shfl_xor(most, 32)), f);
       if ((most - M) + (lm - off) > kTop) {
         bool far;
-        const float al = move_reference(most, lm, M, off, far);
+        const float al = move_reference(most, lm, M, off, L, far);
         limit = far ? -INFINITY : M + kTop;
-        L *= al;
 #pragma unroll
         for (int d = 0; d < kTiles; ++d) o[d] *= al;
       }
@@ -957,13 +943,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     // Every weight is below 2^kTop unless some lane's sum is not (a sum of NaN is
     // a row of NaN); only then is M moved and are the weights made again.
     const uint32_t in = __float_as_uint(inv);
-    uint32_t in_l = in;
-    if (is_special(in, least)) {
-      float z[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) z[e] = s[e];
-      in_l = add_special<32>(in, z, f, least, M, off, L, Mz, Lz);
-    }
     if (in != 0 && __any(sum > limit)) {
       float most = s[0];
 #pragma unroll
@@ -971,9 +950,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
       most = score_of(fmaxf(most, __shfl_xor(most, 32)), f);
       if ((most - M) + (lam - off) > kPlace) {
         bool far;
-        const float al = move_reference(most, lam, M, off, far);
+        const float al = move_reference(most, lam, M, off, L, far);
         limit = far ? -1.f : kTopWeight;
-        L *= al;
 #pragma unroll
         for (int d = 0; d < kTiles; ++d) o[d] *= al;
       }
@@ -985,6 +963,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
         sum += y;
         pairs[e >> 1][e & 1] = (_Float16)y;
       }
+    }
+    uint32_t in_l = in;  // what its weights have in L
+    if (is_special(in, least) && meet_scale(in, least)) {
+      float z[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z[e] = s[e];
+      add_zeros<32>(z, f, Mz, Lz);
+      in_l = 0;
     }
     L = fmaf(sum, __uint_as_float(in_l), L);
     asm volatile("" : "+v"(L));
