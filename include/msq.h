@@ -505,8 +505,8 @@ size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_
  * weights are rounded to f16; scores, softmax statistics and sums are fp32.
  * Scores may have any size that log2(e) times fp32 holds: the weights are those of
  * the scores as rounded to fp32.  An fp32 query counts as rounded to f16 (11 bits of
- * each value of at least 2^-29 of the row's largest), which moves a score by up to
- * 2^-11 of scale * sum |q_d k_d|; bf16 queries lose nothing there.
+ * each value of at least 2^-28 of the row's largest), which moves a score by up to
+ * 2^-11 of scale * sum |q_d k_d|; bf16 queries are exact there.
  * Value scales below 2^-100 count as 0.  Rows outside every sequence are left
  * as they are.
  * workspace: msq_kv_attention_workspace_bytes, 256-byte aligned; calls that
