@@ -198,8 +198,9 @@ struct WriteArgs {
 // A wavefront takes 32 slots x E dims (64 where the workgroup's 16 wavefronts
 // allow it).  HBM bound on long runs (each value is read once and kept in
 // registers between the maximum and the coding): 16 sequences of 4097 to 8192
-// bf16 tokens, 8 heads of 128, 625 MB in 153 us, 4.1 TB/s.  A call of single tokens is a
-// chain of four dependent loads, 4.9 us from launch to launch for one token.
+// bf16 tokens, 8 heads of 128, 625 MB in 153 us, 4.1 TB/s, fp32 1.04 GB in 209 to 228, 4.6
+// to 5.0.  A call of single tokens is a chain of four dependent loads, 4.8 us from
+// launch to launch for one token.
 template <int D, int E, typename T>
 __global__ __launch_bounds__(1024) void k_kv_write(WriteArgs a) {
   using Mp = Map<E>;
@@ -359,7 +360,8 @@ __device__ inline void store8(float* p, const float* x) {
 }
 
 // HBM bound: codes in, values out, once each: 101700 tokens of 8 heads of 128 to
-// bf16, 625 MB in 119 to 133 us, 4.7 to 5.3 TB/s.
+// bf16, 625 MB in 118 to 133 us, 4.7 to 5.3 TB/s; to fp32, 1.04 GB in 254 to 263, 4.0 to
+// 4.1 (mostly writes).
 template <int D, typename T>
 __global__ __launch_bounds__(512) void k_kv_read(ReadArgs a) {
   using Mp = Map<D>;

@@ -32,7 +32,14 @@
 // Codes become f16 exactly: the bytes code + 128 under the exponent byte 0x64
 // are the f16 numbers 1024 + byte, and one packed subtraction of 1152 leaves
 // the code.  A query row is scaled by the power of two that puts its largest
-// value in [2^14, 2^15), so bf16 queries are exact down to 2^-21 of it.
+// value in [2^14, 2^15), so bf16 queries are exact down to 2^-28 of it; fp32 ones are
+// rounded to 11 bits.  That and the weights' rounding are the price of one matrix
+// instruction a product: of 64-bit results (128 dims, 700 tokens, score spreads of
+// 0.3 to 4) fp32 outputs of bf16 queries are 2e-4 or less away (rms), of fp32 queries
+// 1.6e-4 to 4.4e-4, where rounding to bf16 alone is 1.7e-3.  Denominators of the
+// rounded weights, which cancel some of it: 1.9e-4 -> 1.7e-4 and 1.2e-4 -> 0.7e-4, at 4%
+// of the time of many rows; not taken.  fp32 queries as two f16 terms: a third more
+// products, and more registers than three wavefronts a SIMD leave.
 #include <hip/hip_runtime.h>
 #include <unistd.h>
 
@@ -376,12 +383,15 @@ extern __shared__ __align__(16) unsigned char smem_kv[];
 // result registers are the B operand of O^T = V^T P^T: no LDS in the loop.
 //
 // Bound by HBM, 2 D bytes a token and kv head: 4 sequences of 131072 tokens, 64
-// query heads on 8 of 128, 1.07 GB in 190 us, 5.6 TB/s; 32 of up to 4097, 179 MB in
-// 43 us, 4.1 TB/s (their lengths differ, and each workgroup starts with a chain
-// of loads: lengths, table, codes).  Few tokens: that chain, 4.7 us from launch to
-// launch for one token on 1 to 128, 7.6 on 777.  Tiles of 32 rows halve what
-// more than 16 rows read but leave two wavefronts a SIMD instead of three (128
-// rows on 4096 tokens of 128 heads: 45 -> 54 us).
+// query heads on 8 of 128, 1.07 GB in 191 us, 5.6 TB/s; 32 of up to 4097, 179 MB in
+// 44 us, 4.1 TB/s (their lengths differ, and each workgroup starts with a chain
+// of loads: lengths, table, codes); heads of 256, 32 of 4096 tokens, 537 MB in 102
+// us.  Few tokens: that chain, 5.3 us from launch to launch for a prompt of 16, 7.9
+// for one token on 777; heads of 256, one wavefront a SIMD, 8 sequences of 2000
+// tokens, 33 MB, 15.8.  More than 16 rows read a sequence once for every 16: 20 rows
+// of heads of 64 on 1024 tokens of 8 sequences 9.1 us, 512 workgroups of some nine
+// tiles each.  Tiles of 32 rows halve that but leave two wavefronts a SIMD instead
+// of three (128 rows on 4096 tokens of 128 heads: 45 -> 54 us).
 template <int D>
 struct Tile {
   uint4 k[D / 32];  // [16-token half][64-dim chunk]
@@ -678,10 +688,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 //
 // Bound by the matrix and the vector instructions together, and by the clock
 // that the card holds under them (1.9 to 2.0 GHz): 2048 tokens, 64 query heads on
-// 8 of 128, on 32049 tokens, 2.08 Tflop in 1.85 ms (1.82 to 1.92 over cards), 1.1
-// Pflop/s; matrix units busy 58% of the time, vector units 59% (16 exponentials, at a
+// 8 of 128, on 32049 tokens, 2.08 Tflop in 1.84 to 1.91 ms over cards, 1.1
+// Pflop/s; matrix units busy 56% of the time, vector units 58% (16 exponentials, at a
 // quarter of the rate, and some 60 other instructions a strip and 16 products), the
-// LDS 36%, no bank conflicts.  Tried and slower: stages of 128 tokens (1900 ->
+// LDS 35%, no bank conflicts.  2048 on 16000, heads of 64 (128 of them) 1220 us,
+// matrix 35%, vector 62%; of 256 (32) 1084 us, 40% and 38%, LDS 30%, one wavefront a
+// SIMD.  A prompt from its start: 2048 tokens, 32 heads on 8 of 128, 63 us, 26 at the
+// matrix rate: its 256 workgroups, one a compute unit, have 1 to 32 stages, so the
+// units are at work half of the time.  Tried and slower: stages of 128 tokens (1900 ->
 // 1925 us), 4 or 8 operands read ahead instead of 2 (1%), two groups of wavefronts
 // that alternate between products and softmax (1972 -> 2090), 64 rows a
 // wavefront (1850 -> 2430: past 256 registers every operand is copied between the
@@ -1174,11 +1188,15 @@ bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p
 constexpr int kJoinInside = 16, kJoinFloats = 8192;
 // Bytes that k_kv_decode reads in all (the cache once for every 16 query rows,
 // mostly from the L2s) from which more than kFewRows rows take k_kv_prefill.
-// k_kv_decode and k_kv_prefill: head dim 128, 98 MB 17.7, 28.3 us; 268 MB 21.7, 37.5;
-// 393 MB 31.2, 33.3; 491 MB 45, 36; 1074 MB 75, 62; 64, 262 MB 30.3, 32.1; 524 MB 48.2,
-// 43.7; 256, 134 MB 16.7, 30.4; 246 MB 40.8, 36.9; 262 MB 37.3, 41.7; 268 MB 42.5,
-// 30.6; 319 MB 41.6, 37.5.  Up to kFewRows rows k_kv_decode keeps ahead or level at any
-// size (64 rows, 537 MB 49.6, 55.7; 2147 MB 180, 173).
+// k_kv_decode and k_kv_prefill (the better of its ways), us: head dim 128, 102 MB
+// 18.6, 20.5; 262 22.0, 27.2; 393 38.5, 35.6; 410 43.0, 32.8 and 39.3, 37.5; 537 30.1,
+// 29.7; 1208 53, 43; 64, 131 MB 19.2, 21.1; 205 29.9, 24.6 and 24.8, 27.4; 262 30.1,
+// 31.1; 256, 131 MB 27.6, 28.5; 164 36.0, 32.9 and 205 28.0, 31.4; 262 32.5, 38.8 and
+// 30.4, 40.3; 268 34.9, 30.2; 328 57, 42; 524 58, 48.  Around the limits the bytes alone
+// do not tell which is faster (how the tiles fill the GPU does too): the one
+// taken was up to 10% slower than the other at 128, 22% at 64, a third at 256.  Up
+// to kFewRows rows k_kv_decode keeps ahead or level at any size (64 rows, 537 MB 49.6,
+// 55.7; 2147 MB 180, 173).
 constexpr int64_t decode_bytes(int D) { return D == 256 ? 240000000 : 400000000; }
 constexpr int kFewRows = 64;
 
@@ -1188,10 +1206,14 @@ constexpr int kFewRows = 64;
 //
 // With 8 wavefronts a strip is converted for twice the rows.  Head dim 128: two
 // wavefronts a SIMD either way, and workgroups of 4 only fill the GPU better
-// where sequences are short (4 and 8 wavefronts: 4 x 1024 rows of 8 heads on
-// 1500 tokens 94, 86 us, 1024 on 8192 166, 142; 256 on 512 22.1, 23.8).  64: three
-// workgroups of 4 a compute unit or one of 8, a tile 1.73 to 1 in time (2048 rows
-// of 128 heads on 16000 tokens 1337, 1180 us; 8 x 512 of 64 on 2000 158, 164).
+// where sequences are short.  4 and 8 wavefronts, 32 heads on 8, us: prompts from
+// their start, 1024 tokens 29.9, 34.5; 1536 43.3, 47.3; 2048 58.3, 61.9; 3000 96.9, 94.9;
+// 4096 172, 150; two of 1024 34.5, 36.9, of 1536 60.7, 54.5; four of 1024 57.4, 52.4;
+// on longer sequences, 8 x 512 on 1000 73, 70, on 1500 106, 101; 64 heads, 1024 on 8192
+// 284, 262.  (The limit of 1024 tokens takes the slower one, by up to 10%, for single
+// prompts above it and batches below.)  64: three workgroups of 4 a compute unit or
+// one of 8, a tile 1.73 to 1 in time (2048 rows of 128 heads on 16000 tokens 1337,
+// 1180 us; 8 x 512 of 64 on 2000 158, 164).
 struct Way {
   int waves;
   int64_t slots;
