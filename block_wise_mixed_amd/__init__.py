@@ -794,10 +794,9 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     scale: of the scores (0: 1 / sqrt(head_dim)).  Returns out [rows][q_heads][head_dim] (bf16
     unless out or out_dtype says fp32), with return_lse also the fp32 [rows][q_heads] natural
     log of each row's softmax denominator.  A query that sees nothing gives zeros and -inf; rows
-    outside every sequence are not written.  Products are of f16 operands: fp32 queries count as
-    rounded to f16 (relative to their largest value) and so do the softmax weights, so fp32
-    results carry some 2^-12 of the values' size and more where scores are large
-    (include/msq.h).  workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
+    outside every sequence are not written.  Products are of f16 operands, the softmax weights
+    among them (some 2^-12 of the values' size in fp32 results); fp32 queries count by 22 bits
+    for fp32 results, by 11 for bf16 ones (include/msq.h).  workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
     desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
     if stream is not None or index < 0 or cuda._cuda_getDevice() != index:

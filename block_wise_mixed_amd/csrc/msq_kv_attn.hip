@@ -32,14 +32,16 @@
 // Codes become f16 exactly: the bytes code + 128 under the exponent byte 0x64
 // are the f16 numbers 1024 + byte, and one packed subtraction of 1152 leaves
 // the code.  A query row is scaled by the power of two that puts its largest
-// value in [2^14, 2^15), so bf16 queries are exact down to 2^-28 of it; fp32 ones are
-// rounded to 11 bits.  That and the weights' rounding are the price of one matrix
-// instruction a product: of 64-bit results (128 dims, 700 tokens, score spreads of
-// 0.3 to 4) fp32 outputs of bf16 queries are 2e-4 or less away (rms), of fp32 queries
-// 1.6e-4 to 4.4e-4, where rounding to bf16 alone is 1.7e-3.  Denominators of the
-// rounded weights, which cancel some of it: 1.9e-4 -> 1.7e-4 and 1.2e-4 -> 0.7e-4, at 4%
-// of the time of many rows; not taken.  fp32 queries as two f16 terms: a third more
-// products, and more registers than three wavefronts a SIMD leave.
+// value in [2^14, 2^15), so bf16 queries are exact down to 2^-28 of it.  fp32 ones are
+// rounded to 11 bits where the results are bf16; for fp32 results (kFine) what is left
+// of them goes through the products as a second f16 term, 22 bits in all.  The
+// weights are rounded to f16 either way, and L is the sum of the unrounded ones.
+// Against 64 bits (128 dims, 700 tokens, score spreads of 0.3 to 4) fp32 results are
+// 2e-4 or less away (rms), with fp32 queries in one term 1.6e-4 to 4.4e-4; rounding to
+// bf16 alone is 1.7e-3.  The second term costs 2 to 4% in k_kv_decode and 18 to 29%
+// in k_kv_prefill (2048 rows of 64 heads on 16000 tokens 941 -> 1215 us).  L of the
+// rounded weights, which cancels some of their rounding: 1.9e-4 -> 1.7e-4 and 1.2e-4 ->
+// 0.7e-4, at 4% of the time of many rows; not taken.
 #include <hip/hip_runtime.h>
 #include <unistd.h>
 
@@ -143,9 +145,11 @@ __device__ inline void row_scale(float amax, bool bad, float& up, float& down) {
 }
 
 // The f16 fragments of a query row, whose values the lanes lane ^ kFirst * m
-// hold between them, and the inverse of their scale.
-template <int N, int kFirst>
-__device__ inline void query_fragments(const Raw8 (&raw)[N], int f32, half8 (&q)[N], float& down) {
+// hold between them, and the inverse of their scale; of an fp32 row with kFine also
+// what f16 leaves of it, as f16 fragments rest.
+template <bool kFine, int N, int kFirst>
+__device__ inline void query_fragments(const Raw8 (&raw)[N], int f32, half8 (&q)[N],
+                                       half8 (&rest)[kFine ? N : 1], float& down) {
   typedef uint16_t pair __attribute__((ext_vector_type(2)));
   uint32_t most = 0;  // the largest magnitude, as an fp32 bit pattern
   if (f32) {
@@ -177,7 +181,11 @@ __device__ inline void query_fragments(const Raw8 (&raw)[N], int f32, half8 (&q)
       const uint32_t w[8] = {raw[s].a.x, raw[s].a.y, raw[s].a.z, raw[s].a.w,
                              raw[s].b.x, raw[s].b.y, raw[s].b.z, raw[s].b.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(__uint_as_float(w[e]) * up);
+      for (int e = 0; e < 8; ++e) {
+        const float x = __uint_as_float(w[e]) * up;
+        q[s][e] = (_Float16)x;
+        if constexpr (kFine) rest[s][e] = (_Float16)(x - (float)q[s][e]);
+      }
     }
   } else {
 #pragma unroll
@@ -412,7 +420,7 @@ __device__ inline void load_tile(Tile<D>& t, const KvCacheView& c, int id, int h
   for (int i = 0; i < D / 32; ++i) t.v[i] = v[64 * i];
 }
 
-template <int D>
+template <int D, bool kFine>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
   constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
   constexpr int kStride = D + 4;
@@ -446,7 +454,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
       raw[s] = load8(a.q, a.q_f32, at + 64 * (s >> 1) + 8 * (s & 1));
-    query_fragments<kSteps, 16>(raw, a.q_f32, q, down);
+    half8 rest[kFine ? kSteps : 1];
+    query_fragments<kFine, kSteps, 16>(raw, a.q_f32, q, rest, down);
+    if constexpr (kFine) {
+      // into the wavefront's part of what holds its results in the end, read again in
+      // every tile: in registers they would take a wavefront a SIMD
+      half8* to = reinterpret_cast<half8*>(reinterpret_cast<float*>(smem_kv) + wave * 16 * kStride) + lane;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) to[64 * s] = rest[s];
+    }
   }
   const float cq = a.c2 * down;
 
@@ -471,13 +487,25 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   auto work = [&](const Tile<D>& tl, int t, int j) {
     if (__builtin_amdgcn_readlane(id, j) < 0) return;  // an absent block
     f32x4 s0 = {0.f, 0.f, 0.f, 0.f}, s1 = s0;
+    const half8* rest = nullptr;
+    if constexpr (kFine) {
+      int at = wave * 16 * kStride * 4 + 16 * lane;
+      asm volatile("" : "+v"(at));  // not to be read ahead of the loop
+      rest = reinterpret_cast<const half8*>(smem_kv + at);
+    }
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const uint4 k0 = tl.k[c], k1 = tl.k[D / 64 + c];
-      s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.x, k0.y), q[2 * c], s0, 0, 0, 0);
-      s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.x, k1.y), q[2 * c], s1, 0, 0, 0);
-      s0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k0.z, k0.w), q[2 * c + 1], s0, 0, 0, 0);
-      s1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(k1.z, k1.w), q[2 * c + 1], s1, 0, 0, 0);
+      auto add = [&](f32x4& to, uint32_t w0, uint32_t w1, int step) {
+        const half8 k = codes_f16x8(w0, w1);
+        to = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[step], to, 0, 0, 0);
+        if constexpr (kFine)
+          to = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, rest[64 * step], to, 0, 0, 0);
+      };
+      add(s0, k0.x, k0.y, 2 * c);
+      add(s1, k1.x, k1.y, 2 * c);
+      add(s0, k0.z, k0.w, 2 * c + 1);
+      add(s1, k1.z, k1.w, 2 * c + 1);
     }
     // lane (col, g): scores of row col at tokens 4g + 0..3 and 16 + 4g + 0..3
     const float f = fmaxf(cq * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sk), j)), kTinyStep);
@@ -734,7 +762,7 @@ struct Prefill {
   }
 };
 
-template <int D, int W>
+template <int D, int W, bool kFine>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
   using C = Prefill<D, W>;
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
@@ -842,7 +870,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
 
   half8 q[kSteps];  // slots (half, e) of step s are dims 16 s + 8 half + e
   float down;
-  query_fragments<kSteps, 32>(qraw, a.q_f32, q, down);
+  half8 rest[kFine ? kSteps : 1];
+  query_fragments<kFine, kSteps, 32>(qraw, a.q_f32, q, rest, down);
 #ifdef __HIP_DEVICE_COMPILE__
   // Head dim 256: into the accumulation registers, from which the products read
   // them too (left to itself the compiler moves them there and back in every
@@ -922,9 +951,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
 #pragma unroll
     for (int m = 0; m < kProducts; ++m) {
       const int v = m - kSteps;
-      if (m < kSteps)
+      if (m < kSteps) {
         sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], q[m], sn, 0, 0, 0);
-      else
+        if constexpr (kFine)
+          sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], rest[m], sn, 0, 0, 0);
+      } else
         o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], pp[v / kTiles],
                                                                o[v % kTiles], 0, 0, 0);
       if (m + kAhead < kProducts)
@@ -1005,8 +1036,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     lds_barrier();
     sa = f32x16{};
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k)
+    for (int k = 0; k < kSteps; ++k) {
       sa = __builtin_amdgcn_mfma_f32_32x32x16_f16(operand(i0 - 1, k), q[k], sa, 0, 0, 0);
+      if constexpr (kFine)
+        sa = __builtin_amdgcn_mfma_f32_32x32x16_f16(operand(i0 - 1, k), rest[k], sa, 0, 0, 0);
+    }
     lds_barrier();  // the first stage's conversion takes the place of these keys
     auto next_batch = [&](int t) {
       if (kStrips * t - batch == 64) {
@@ -1404,12 +1438,12 @@ uint64_t next_call() {
   return n ? n : start + count.fetch_add(1, std::memory_order_relaxed);
 }
 
-template <int D>
+template <int D, bool kFine>
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if (p.waves) {
     auto prefill = [&](auto w) {
       using C = Prefill<D, decltype(w)::value>;
-      hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves>), dim3((unsigned)p.blocks), dim3(C::kThreads),
+      hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves, kFine>), dim3((unsigned)p.blocks), dim3(C::kThreads),
                          C::kLds, stream, a);
     };
     if constexpr (D != 256)
@@ -1417,7 +1451,7 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
     if (p.waves == 4) prefill(std::integral_constant<int, 4>{});
   } else {
     const size_t lds = 4 * kRowTile * (D + 4 + 3) * 4;
-    hipLaunchKernelGGL((k_kv_decode<D>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
+    hipLaunchKernelGGL((k_kv_decode<D, kFine>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
   }
   if (p.nsplit > 1 && !p.tags_at) {
     const int rows = a.s.batch * a.s.max_count * a.Hq;
@@ -1518,11 +1552,12 @@ extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_s
   a.tile_rows = p.tile_rows;
   a.tile_shift = p.tile_tokens == 64 ? 6 : 5;
   a.c2 = (t.scale > 0.f ? t.scale : 1.f / std::sqrt((float)D)) * kLog2e;
+  const bool fine = a.q_f32 && a.out_f32;
   hipError_t e;
   switch (D) {
-    case 64: e = launch_attn<64>(a, p, stream); break;
-    case 128: e = launch_attn<128>(a, p, stream); break;
-    default: e = launch_attn<256>(a, p, stream); break;
+    case 64: e = fine ? launch_attn<64, true>(a, p, stream) : launch_attn<64, false>(a, p, stream); break;
+    case 128: e = fine ? launch_attn<128, true>(a, p, stream) : launch_attn<128, false>(a, p, stream); break;
+    default: e = fine ? launch_attn<256, true>(a, p, stream) : launch_attn<256, false>(a, p, stream); break;
   }
   return e == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
 }

@@ -504,9 +504,10 @@ size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_
  * exact there, the query row is scaled by a power of two and the softmax
  * weights are rounded to f16; scores, softmax statistics and sums are fp32.
  * Scores may have any size that log2(e) times fp32 holds: the weights are those of
- * the scores as rounded to fp32.  An fp32 query counts as rounded to f16 (11 bits of
- * each value of at least 2^-28 of the row's largest), which moves a score by up to
- * 2^-11 of scale * sum |q_d k_d|; bf16 queries are exact there.
+ * the scores as rounded to fp32.  bf16 queries lose nothing in values of at least
+ * 2^-28 of their row's largest, and fp32 ones go by 22 bits there where the results
+ * are fp32; where they are bf16, fp32 queries count as rounded to f16 (11 bits), which
+ * moves a score by up to 2^-11 of scale * sum |q_d k_d|.
  * Value scales below 2^-100 count as 0.  Rows outside every sequence are left
  * as they are.
  * workspace: msq_kv_attention_workspace_bytes, 256-byte aligned; calls that

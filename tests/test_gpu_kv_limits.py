@@ -94,6 +94,46 @@ def test_attention_one_token_at_scores_of_any_size(msq, D):
             assert (np.abs(lse.cpu().numpy() - 0.05 * (q.astype(np.float64) @ k)) <= e).all()
 
 
+# ---------------------------------------------------------------- fp32 queries
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_fp32_queries_for_fp32_results(msq, D):
+    """Queries whose rounding to f16 moves two scores of some hundreds apart by up to a half: fp32
+    results go by 22 bits of the query (2^-22 of each term of a score beside 2 D fp32 sums).
+    One token has keys where the rounding is down, one where it is up; others are random."""
+    P, L, H, G = 32, 96, 1, 2
+    rng = np.random.default_rng(D)
+    table = np.array([[2, 0, 1]])
+    p = Pair(msq, 3, H, D, P, seed=36)
+    k = rng.normal(size=(L, H, D)) * 0.02
+    half = np.arange(D) % 2
+    k[20, 0], k[70, 0] = half, 1 - half
+    p.write(table, [0], [L], torch.float32, k=k)
+    kk, vv = (p.ref.values(name, table[0], 0, L) for name in "kv")
+    step = p.ref.scale["v"][table[0][np.arange(L) // P]]
+    mask = np.ones((1, L), bool)
+    moved = 0
+    for n in (1, 40):
+        up = 1 + 2.0 ** -11 + (2 * half - 1) * 2.0 ** -14   # to 1 + 2^-10 where half, to 1 elsewhere
+        q = up * 2.0 ** rng.integers(-2, 1, size=(n, G, 1))
+        q, qt = rounded(q, torch.float32)
+        scale = 1280.0 / D
+        want, wl, absum, size, big = O.attention(q, kk, vv, np.repeat(mask, n, 0), scale, step)
+        old, *_ = O.attention(q.astype(np.float16), kk, vv, np.repeat(mask, n, 0), scale, step)
+        e = size * (2.0 ** -22 + (2 * D + 32) * 2.0 ** -24) + 2.0 ** -20
+        bound = absum * (2 * e + 2.0 ** -11 + 2.0 ** -18 + (L + 64) * 2.0 ** -24)[..., None] \
+            + (L * 2.0 ** -31 * 127 * big)[..., None] + 1e-37
+        moved += int((np.abs(old - want) > 2 * bound).sum())
+        for tb, lens, counts in ways(H, G, D, P, table, L, n):
+            got, lse = msq.kv_attention(qt, p.gpu, i32(tb), i32(lens), i32(offsets(counts)), max_count=n,
+                                        scale=scale, causal=False, out_dtype=torch.float32, return_lse=True)
+            torch.cuda.synchronize()
+            assert (np.abs(got.cpu().numpy() - want) <= bound).all(), len(lens)
+            lb = e + np.abs(wl) * 2.0 ** -22 + (L + 64) * 2.0 ** -24
+            assert (np.abs(lse.cpu().numpy() - wl) <= lb).all()
+    assert moved > 100  # what rounded queries give is far outside
+
+
 # ---------------------------------------------------------------- lengths past the table
 
 @pytest.mark.parametrize("D", [64, 128, 256])

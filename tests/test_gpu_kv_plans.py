@@ -62,3 +62,4 @@ def test_every_kernel(msq, D, tile, waves, join, H, G, lens, counts, way):
     call = steered(msq, p, H * G, table, lens, counts, (tile, waves, join), causal, window)
     p.attend(q, *call, causal=causal, window=window)
     p.attend(q, *call, causal=causal, window=window, dtype=torch.float32, out=torch.bfloat16)
+    p.attend(q, *call, causal=causal, window=window, dtype=torch.float32)
