@@ -514,8 +514,11 @@ size_t msq_kv_attention_workspace_bytes(const msq_kv_cache *cache, const msq_kv_
  * share one must be ordered on one stream, and it may hold anything before a
  * call.  One launch; where a sequence's tokens are split over workgroups, their
  * parts are joined inside it (few of them) or by one more.  Asynchronous, and
- * the same bits every time.  Errors as msq_kv_write, plus
- * MSQ_ERR_BUFFER_TOO_SMALL. */
+ * the same bits every time.  Errors: MSQ_ERR_INVALID_ARG (also a scale that is
+ * negative or not finite, a window without causal), MSQ_ERR_SHAPE (also total *
+ * q_heads past 2^31 - 1, or more than 2^27 - 16 tiles of 16 of the max_count *
+ * q_heads / kv_heads query rows of each sequence and kv head), MSQ_ERR_UNSUPPORTED
+ * and MSQ_ERR_HIP as msq_kv_write, MSQ_ERR_BUFFER_TOO_SMALL. */
 msq_status msq_kv_attention(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
                             const msq_kv_attn *attn, void *workspace, size_t workspace_bytes,
                             hipStream_t stream);
