@@ -388,7 +388,8 @@ extern __shared__ __align__(16) unsigned char smem_kv[];
 // tokens in turn, straight from HBM into registers (the cache order is the
 // operand order), the next tile's loads in flight during the current one's
 // products.  S^T = K Q^T (16 x 16 x 32, tokens down, rows across), whose
-// result registers are the B operand of O^T = V^T P^T: no LDS in the loop.
+// result registers are the B operand of O^T = V^T P^T: no LDS in the loop, but for
+// the second term of fp32 queries.
 //
 // Bound by HBM, 2 D bytes a token and kv head: 4 sequences of 131072 tokens, 64
 // query heads on 8 of 128, 1.07 GB in 191 us, 5.6 TB/s; 32 of up to 4097, 179 MB in
