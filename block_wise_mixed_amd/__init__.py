@@ -31,7 +31,9 @@ __all__ = ["MsqError", "PackedWeight", "plan", "quantize_pack", "allocate_packed
            "library_path", "load_library", "KERNELS", "FORMAT_VERSION", "GEMV_MAX_M",
            "allocate_bits", "alloc_workspace_bytes", "ALLOC_LEVELS", "reorder_channels",
            "KVCache", "allocate_kv_cache", "kv_write", "kv_read", "kv_attention",
-           "kv_attention_workspace_bytes", "kv_attention_plan", "KV_HEAD_DIMS", "KV_BLOCK_TOKENS"]
+           "kv_attention_workspace_bytes", "kv_attention_plan", "KV_HEAD_DIMS", "KV_BLOCK_TOKENS",
+           "Rotary", "rotary_frequencies", "rotary", "kv_append", "draft_tree", "verify_draft",
+           "verify_draft_workspace_bytes", "DRAFT_MAX_ROWS"]
 
 FORMAT_VERSION = 2
 GEMV_MAX_M = 64
@@ -119,9 +121,45 @@ class _KvPlan(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _Rotary(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_double)]
+
+
+class _RotaryRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _KvNew(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v", ctypes.c_void_p),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("kv_rows", ctypes.c_int64),
+                ("source", ctypes.c_void_p), ("count", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("rot", _Rotary), ("q", _RotaryRows)]
+
+
+class _Draft(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("offset", ctypes.c_void_p), ("total", ctypes.c_int64),
+                ("max_count", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("tokens", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("target", ctypes.c_void_p), ("target_stride", ctypes.c_int64),
+                ("draft", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("uniform", ctypes.c_void_p),
+                ("token", ctypes.c_void_p), ("taken", ctypes.c_void_p), ("path", ctypes.c_void_p)]
+
+
 _KV_CACHE = struct.Struct("@qiiiPPPP")  # the fields of _KvCache
 _KV_SEQS = struct.Struct("@iiPPqi")  # the fields of _KvSeqs
 _KV_ATTN = struct.Struct("@PqqiiPqfiiPiP")  # the fields of _KvAttn
+_ROTARY = struct.Struct("@Piid")  # the fields of _Rotary
+_ROTARY_ROWS = struct.Struct("@PqqPqqiiii")  # the fields of _RotaryRows
+_KV_NEW = struct.Struct("@PqqPqqiqPPPPiidPqqPqqiiii")  # the fields of _KvNew
+_DRAFT = struct.Struct("@iPqiiPPPqPqiPPPP")  # the fields of _Draft
 _KV_CACHE_FIELDS = frozenset(("num_blocks", "kv_heads", "head_dim", "block_tokens", "k_codes",
                               "v_codes", "k_scale", "v_scale"))
 
@@ -194,6 +232,19 @@ def load_library():
     lib.msq_kv_attention_workspace_bytes.restype = sz
     lib.msq_kv_attention.argtypes = [cache_p, seqs_p, attn_p, vp, sz, vp]
     lib.msq_kv_attention.restype = ctypes.c_int
+    i32 = ctypes.c_int32
+    lib.msq_kv_attention_tree.argtypes = [cache_p, seqs_p, attn_p, vp, i32, vp, sz, vp]
+    lib.msq_kv_attention_tree.restype = ctypes.c_int
+    lib.msq_rotary_apply.argtypes = [ctypes.POINTER(_Rotary), ctypes.POINTER(_RotaryRows), vp, i64, vp]
+    lib.msq_rotary_apply.restype = ctypes.c_int
+    lib.msq_kv_append.argtypes = [cache_p, seqs_p, vp, ctypes.POINTER(_KvNew), vp]
+    lib.msq_kv_append.restype = ctypes.c_int
+    lib.msq_draft_tree.argtypes = [vp, vp, i32, i64, i32, vp, vp, i32, vp, vp]
+    lib.msq_draft_tree.restype = ctypes.c_int
+    lib.msq_verify_draft.argtypes = [ctypes.POINTER(_Draft), vp, sz, vp]
+    lib.msq_verify_draft.restype = ctypes.c_int
+    lib.msq_verify_draft_workspace_bytes.argtypes = [ctypes.POINTER(_Draft)]
+    lib.msq_verify_draft_workspace_bytes.restype = sz
     lib.msq_status_string.argtypes = [ctypes.c_int]
     lib.msq_status_string.restype = ctypes.c_char_p
     lib.msq_format_version.argtypes = []
@@ -674,22 +725,27 @@ def _kv_seqs(cache: KVCache, block_table, offset, total: int, max_count: int):
             (block_table, offset))
 
 
-def _kv_on(cache: KVCache, stream, tensors, call):
-    """call() with the cache's device and the given stream current, so that what it allocates
+def _on(index: int, device, what: str, stream, tensors, call):
+    """call() with device `index` and the given stream current, so that what it allocates
     belongs to that stream; the tensors it was given are marked as used there."""
     torch = _torch()
-    if cache._index < 0:
-        raise ValueError(f"the cache is on {cache.device}: its operators run on a GPU")
-    if stream is not None and stream.device_index != cache._index:
-        raise ValueError(f"the stream is on device {stream.device_index}, the cache on {cache.device}")
-    with torch.cuda.device(cache._index):
+    if index < 0:
+        raise ValueError(f"{what} is on {device}: its operators run on a GPU")
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"the stream is on device {stream.device_index}, {what} on {device}")
+    with torch.cuda.device(index):
         with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream) as _:
             used = torch.cuda.current_stream()
             result = call()
-    for t in (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, *tensors):
+    for t in tensors:
         if t is not None and t.is_cuda:
             t.record_stream(used)
     return result
+
+
+def _kv_on(cache: KVCache, stream, tensors, call):
+    return _on(cache._index, cache.device, "the cache", stream,
+               (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, *tensors), call)
 
 
 def kv_write(cache: KVCache, k, v, block_table, first, offset=None, max_count: int = 0,
@@ -783,7 +839,8 @@ def kv_attention_plan(cache: KVCache, rows: int, q_heads: int, batch: int, table
 
 def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count: int = 0,
                  max_kv_len: int = 0, scale: float = 0.0, causal: bool = True, window: int = 0,
-                 out=None, out_dtype=None, return_lse: bool = False, workspace=None, stream=None):
+                 out=None, out_dtype=None, return_lse: bool = False, workspace=None, stream=None,
+                 tree=None):
     """Attention of new tokens' queries over the cache (msq_kv_attention).
 
     q: [rows][q_heads][head_dim] bf16 or fp32, q_heads a multiple of kv_heads.  kv_len: int32
@@ -796,14 +853,18 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
     log of each row's softmax denominator.  A query that sees nothing gives zeros and -inf; rows
     outside every sequence are not written.  Products are of f16 operands, the softmax weights
     among them (some 2^-12 of the values' size in fp32 results); fp32 queries count by 22 bits
-    for fp32 results, by 11 for bf16 ones (include/msq.h).  workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes."""
+    for fp32 results, by 11 for bf16 ones (include/msq.h).  workspace: uint8 tensor to reuse, of kv_attention_workspace_bytes.
+
+    tree: int32 [rows][words] from draft_tree, or any such sets: of the call's own tokens a query
+    sees those in its set (bit j % 32 of word j / 32: the sequence's row j), of the earlier ones all,
+    with a window the last `window` of them together (msq_kv_attention_tree; causal only)."""
     desc = cache._desc or cache.descriptor()
     index, cuda = cache._index, _torch()._C
     if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
-        return _kv_on(cache, stream, (q, block_table, kv_len, offset, out, workspace),
+        return _kv_on(cache, stream, (q, block_table, kv_len, offset, out, workspace, tree),
                       lambda: kv_attention(q, cache, block_table, kv_len, offset, max_count,
                                            max_kv_len, scale, causal, window, out, out_dtype,
-                                           return_lse, workspace))
+                                           return_lse, workspace, tree=tree))
     torch = _torch()
     lib = load_library()
     if q.dim() != 3:
@@ -831,9 +892,294 @@ def kv_attention(q, cache: KVCache, block_table, kv_len, offset=None, max_count:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the cache's device")
-    status = lib.msq_kv_attention(desc, s, a, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(),
-                                  cuda._cuda_getCurrentRawStream(index))
+    if tree is None:
+        status = lib.msq_kv_attention(desc, s, a, workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(),
+                                      cuda._cuda_getCurrentRawStream(index))
+    else:
+        if tree.dtype is not torch.int32 or tree.dim() != 2 or tree.size(0) != rows or \
+                tree.get_device() != index:
+            raise ValueError(f"tree must be int32 [{rows}][words] on the cache's device")
+        tree = tree if tree.is_contiguous() else tree.contiguous()
+        status = lib.msq_kv_attention_tree(desc, s, a, tree.data_ptr(), tree.size(1),
+                                           workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(),
+                                           cuda._cuda_getCurrentRawStream(index))
     if status:
         raise MsqError(status, "msq_kv_attention")
     return (out, lse) if return_lse else out
+
+
+# ---- rotary positions ----------------------------------------------------------------
+def rotary_frequencies(dims: int, base: float = 10000.0, factor: float = 1.0, original: int = 0,
+                       slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """float64 [dims / 2] radians a position: f_i = base^(-2 i / dims), for contexts `factor` times
+    as long as those a model was trained on (`original` tokens).  original 0: f_i / factor.
+    Else by how many turns r = original f_i / 2 pi a frequency makes in the original length:
+    unchanged from `fast` turns on, divided by factor up to `slow`, a linear blend in r between.
+    (Any other rule: give Rotary its frequencies.)"""
+    torch = _torch()
+    if dims < 2 or dims % 2 or not base > 0 or not factor > 0 or original < 0 or (original and not slow < fast):
+        raise ValueError("dims even, base and factor positive, slow below fast")
+    f = float(base) ** (-np.arange(0, dims, 2, dtype=np.float64) / dims)
+    if original:
+        keep = np.clip((original * f / (2 * np.pi) - slow) / (fast - slow), 0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    else:
+        f = f / factor
+    return torch.from_numpy(f).to(device)
+
+
+@dataclass
+class Rotary:
+    """How positions are put into queries and keys (msq_rotary in include/msq.h): frequencies,
+    float64 [dims / 2] on the device, for the first dims values of each head (a multiple of 16);
+    pairs are the dims i and dims / 2 + i, or neighbours (interleaved); cosine and sine are
+    multiplied by amplitude."""
+    frequencies: "object"
+    interleaved: bool = False
+    amplitude: float = 1.0
+
+    def __post_init__(self):
+        f = self.frequencies
+        if f.dtype is not _torch().float64 or f.dim() != 1 or f.numel() < 8 or f.numel() % 8 or \
+                not f.is_contiguous():
+            raise ValueError("frequencies must be contiguous float64 [dims / 2], dims a multiple of 16")
+        if not np.isfinite(self.amplitude) or self.amplitude == 0:
+            raise ValueError("amplitude must be finite and not 0")
+
+    def fields(self, index: int):
+        """Its fields in the C structs, for a call on device `index`."""
+        f = self.frequencies
+        if f.get_device() != index:
+            raise ValueError("frequencies must be on the call's device")
+        return f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0, self.amplitude
+
+
+def _rotary_out(x, out, out_dtype, name, index):
+    """The tensor that takes x rotated, and its fields."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or out.get_device() != index or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"{name} must have the shape of what is rotated, on its device")
+    code = _kv_dtype(out.dtype)
+    st, sh, sd = out.stride()
+    per16 = 4 if code else 8
+    if out.numel() and (sd != 1 or st % per16 or sh % per16 or out.data_ptr() % 16):
+        raise ValueError(f"{name}: dims contiguous, strides and address multiples of 16 bytes")
+    return out, out.data_ptr(), st, sh, code
+
+
+def rotary(x, positions, rot: Rotary, out=None, out_dtype=None, stream=None):
+    """x [rows][heads][head_dim] (bf16 or fp32) rotated to positions, int32 [rows]
+    (msq_rotary_apply).  Returns out, of x's type unless out or out_dtype says otherwise; out may
+    be x itself.  Negated positions rotate back: the gradient of rotary(x, p, rot) is
+    rotary(gradient, -p, rot)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [rows][heads][head_dim]")
+    index, cuda = x.get_device(), _torch()._C
+    if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
+        return _on(index, x.device, "x", stream, (x, positions, rot.frequencies, out),
+                   lambda: rotary(x, positions, rot, out, out_dtype))
+    rows, heads, dim = x.shape
+    given = x
+    x, _, at, st, sh, code = _kv_rows(x, "x", heads, dim, index)
+    if out is given and x is not given:
+        raise ValueError("in place: dims contiguous, strides and address multiples of 16 bytes")
+    positions = _kv_index(positions, "positions", rows, index)
+    out, o_at, o_st, o_sh, o_code = _rotary_out(x, out, out_dtype, "out", index)
+    r, v = _Rotary(), _RotaryRows()
+    _ROTARY.pack_into(r, 0, *rot.fields(index))
+    _pack(_ROTARY_ROWS, v, "x", at, st, sh, o_at, o_st, o_sh, code, o_code, heads, dim)
+    status = load_library().msq_rotary_apply(r, v, positions.data_ptr(), rows,
+                                             cuda._cuda_getCurrentRawStream(index))
+    if status:
+        raise MsqError(status, "msq_rotary_apply")
+    return out
+
+
+def kv_append(cache: KVCache, k, v, block_table, first, rot: Optional[Rotary] = None, q=None,
+              positions=None, offset=None, max_count: int = 0, source=None, count=None, q_out=None,
+              q_dtype=None, stream=None):
+    """kv_write of keys rotated on the way, and of values (msq_kv_append); with q [rows][q_heads]
+    [head_dim] also the same tokens' queries, rotated: returned (into q_out, or of q's type or
+    q_dtype; rows outside every sequence are not written), else None.
+
+    positions: int32 [rows], what the rows are rotated to (None: their positions in the cache,
+    first[b] + i).  rot None: no rotation.  source: int32 [rows], the row of k and v that each row
+    of the call takes, and count: int32 [batch], how many of a sequence's rows are taken: with
+    verify_draft's path and taken the drafted tokens that stay are written one after another over
+    the drafts.  The other arguments as in kv_write."""
+    desc = cache._desc or cache.descriptor()
+    index, cuda = cache._index, _torch()._C
+    if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
+        return _kv_on(cache, stream, (k, v, block_table, first, rot and rot.frequencies, q, positions,
+                                      offset, source, count, q_out),
+                      lambda: kv_append(cache, k, v, block_table, first, rot, q, positions, offset,
+                                        max_count, source, count, q_out, q_dtype))
+    heads, dim = cache.kv_heads, cache.head_dim
+    k, kv_rows, k_at, k_st, k_sh, code = _kv_rows(k, "k", heads, dim, index)
+    v, v_rows, v_at, v_st, v_sh, v_code = _kv_rows(v, "v", heads, dim, index)
+    if v_rows != kv_rows or v_code != code:
+        raise ValueError("k and v must have the same rows and type")
+    rows = kv_rows
+    if source is not None:
+        rows = source.numel()
+        source = _kv_index(source, "source", rows, index)
+        if q is not None:
+            raise ValueError("q goes with the rows of k and v, not with a source")
+        if rows and not kv_rows:
+            raise ValueError("source needs rows of k and v")
+    s, keep = _kv_seqs(cache, block_table, offset, rows, max_count)
+    first = _kv_index(first, "first", s.batch, index)
+    if positions is not None:
+        positions = _kv_index(positions, "positions", rows, index)
+    if count is not None:
+        count = _kv_index(count, "count", s.batch, index)
+    queries = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    if q is not None:
+        if q.dim() != 3 or q.size(0) != rows:
+            raise ValueError(f"q must be [{rows}][q_heads][{dim}]")
+        given, q_heads = q, q.size(1)
+        q, _, q_at, q_st, q_sh, q_code = _kv_rows(q, "q", q_heads, dim, index)
+        if q_out is given and q is not given:
+            raise ValueError("in place: dims contiguous, strides and address multiples of 16 bytes")
+        q_out, o_at, o_st, o_sh, o_code = _rotary_out(q, q_out, q_dtype, "q_out", index)
+        queries = (q_at, q_st, q_sh, o_at, o_st, o_sh, q_code, o_code, q_heads, dim)
+    n = _KvNew()
+    _pack(_KV_NEW, n, "the rows", k_at, k_st, k_sh, v_at, v_st, v_sh, code, kv_rows,
+          0 if source is None else source.data_ptr(), 0 if count is None else count.data_ptr(),
+          0 if positions is None else positions.data_ptr(),
+          *((0, 0, 0, 0.0) if rot is None else rot.fields(index)), *queries)
+    status = load_library().msq_kv_append(desc, s, first.data_ptr(), n,
+                                          cuda._cuda_getCurrentRawStream(index))
+    if status:
+        raise MsqError(status, "msq_kv_append")
+    return q_out if q is not None else None
+
+
+# ---- drafted tokens ------------------------------------------------------------------
+DRAFT_MAX_ROWS = 1024
+
+
+def _draft_rows(total, offset, batch, max_count, index):
+    """(offset, batch, the most rows of a sequence) of a call on drafted tokens."""
+    if offset is not None:
+        if offset.dim() != 1 or offset.numel() < 1:
+            raise ValueError("offset must be int32 [batch + 1]")
+        batch = offset.numel() - 1
+        offset = _kv_index(offset, "offset", batch + 1, index)
+        most = min(max_count, total) if max_count else total
+        if max_count > DRAFT_MAX_ROWS:
+            raise ValueError(f"at most {DRAFT_MAX_ROWS} rows a sequence")
+        return offset, batch, min(most, DRAFT_MAX_ROWS)
+    if batch < 0 or total % max(batch, 1) or (batch == 0 and total):
+        raise ValueError("without offset every sequence has the same number of rows")
+    most = total // max(batch, 1)
+    if most > DRAFT_MAX_ROWS:
+        raise ValueError(f"at most {DRAFT_MAX_ROWS} rows a sequence")
+    return None, batch, most
+
+
+def draft_tree(parents, offset=None, first=None, max_count: int = 0, batch: int = 1, stream=None):
+    """(sets, positions) of drafted tokens (msq_draft_tree): int32 [rows][words], which of its
+    sequence's rows each row sees (itself and its ancestors, row j as bit j % 32 of word j / 32),
+    and int32 [rows], first[b] (0 without first) + its depth.  parents: int32 [rows], the row's
+    parent counted in its sequence, below its own number; -1 for a root.  offset: int32
+    [batch + 1], rows of each sequence (None: rows / batch each).  max_count: the largest
+    sequence's rows, if known (it sets the words); at most DRAFT_MAX_ROWS."""
+    index, cuda = parents.get_device(), _torch()._C
+    if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
+        return _on(index, parents.device, "parents", stream, (parents, offset, first),
+                   lambda: draft_tree(parents, offset, first, max_count, batch))
+    torch = _torch()
+    total = parents.numel()
+    parents = _kv_index(parents, "parents", total, index)
+    offset, batch, most = _draft_rows(total, offset, batch, max_count, index)
+    if first is not None:
+        first = _kv_index(first, "first", batch, index)
+    words = max(1, (most + 31) // 32)
+    sets = torch.empty((total, words), dtype=torch.int32, device=parents.device)
+    positions = torch.empty_like(parents)
+    status = load_library().msq_draft_tree(
+        parents.data_ptr(), 0 if offset is None else offset.data_ptr(), batch, total, max_count,
+        0 if first is None else first.data_ptr(), sets.data_ptr(), words, positions.data_ptr(),
+        cuda._cuda_getCurrentRawStream(index))
+    if status:
+        raise MsqError(status, "msq_draft_tree")
+    return sets, positions
+
+
+def verify_draft_workspace_bytes(rows: int, batch: int, vocab: int, max_count: int = 0,
+                                 greedy: bool = False) -> int:
+    """Workspace of verify_draft for calls of these sizes or a smaller vocab or fewer rows; greedy:
+    without uniform."""
+    d = _Draft()
+    _pack(_DRAFT, d, "sizes", batch, 1, rows, max_count, vocab, 0, 0, 0, 0, 0, 0, 0,
+          0 if greedy else 1, 0, 0, 0)
+    return int(load_library().msq_verify_draft_workspace_bytes(d))
+
+
+def verify_draft(tokens, target, offset=None, parents=None, draft=None, uniform=None,
+                 max_count: int = 0, batch: int = 1, workspace=None, stream=None):
+    """Which drafted tokens the target keeps, and the next token of each sequence (msq_verify_draft;
+    the rule is in include/msq.h).
+
+    Rows are nodes: row 0 of a sequence is its last certain token, the others are drafted, each
+    below its parent.  tokens: int32 [rows]; parents: int32 [rows] as in draft_tree (None:
+    chains).  target: [rows][vocab] bf16 or fp32, the large model's probabilities after each
+    row; draft: likewise, what the children of each row were drawn from (None: chosen, not
+    drawn).  uniform: fp32 [rows] in [0, 1), a row's number decides on its token, row 0's draws
+    the next one; None: by target's largest entries, which may be logits then.  Returns int32
+    tensors: token [batch], taken [batch] (rows kept, row 0 among them) and path [rows] (these
+    rows, from each sequence's first on, then -1).  offset, max_count, batch as in draft_tree;
+    workspace: uint8 tensor to reuse, of verify_draft_workspace_bytes."""
+    index, cuda = target.get_device(), _torch()._C
+    if stream is not None or index < 0 or cuda._cuda_getDevice() != index:
+        return _on(index, target.device, "target", stream,
+                   (tokens, target, offset, parents, draft, uniform, workspace),
+                   lambda: verify_draft(tokens, target, offset, parents, draft, uniform, max_count,
+                                        batch, workspace))
+    torch = _torch()
+    lib = load_library()
+    if target.dim() != 2 or target.size(1) < 1:
+        raise ValueError("target must be [rows][vocab]")
+    total, vocab = target.shape
+    code = _kv_dtype(target.dtype)
+    tokens = _kv_index(tokens, "tokens", total, index)
+    if parents is not None:
+        parents = _kv_index(parents, "parents", total, index)
+    if target.stride(1) != 1 and vocab > 1 or target.stride(0) < vocab:
+        target = target.contiguous()
+    d_at = d_st = 0
+    if draft is not None:
+        if draft.shape != target.shape or draft.dtype != target.dtype or draft.get_device() != index:
+            raise ValueError("draft must have target's shape and type, on its device")
+        if draft.stride(1) != 1 and vocab > 1 or draft.stride(0) < vocab:
+            draft = draft.contiguous()
+        d_at, d_st = draft.data_ptr(), draft.stride(0)
+    if uniform is not None:
+        if uniform.dtype is not torch.float32 or uniform.dim() != 1 or uniform.numel() != total or \
+                uniform.get_device() != index:
+            raise ValueError(f"uniform must be float32 [{total}] on target's device")
+        uniform = uniform if uniform.is_contiguous() else uniform.contiguous()
+    offset, batch, _ = _draft_rows(total, offset, batch, max_count, index)
+    token, taken = (torch.empty(batch, dtype=torch.int32, device=target.device) for _ in range(2))
+    path = torch.empty_like(tokens)
+    d = _Draft()
+    _pack(_DRAFT, d, "sizes", batch, 0 if offset is None else offset.data_ptr(), total, max_count,
+          vocab, tokens.data_ptr(), 0 if parents is None else parents.data_ptr(), target.data_ptr(),
+          max(target.stride(0), vocab), d_at, max(d_st, vocab), code,
+          0 if uniform is None else uniform.data_ptr(), token.data_ptr(), taken.data_ptr(),
+          path.data_ptr())
+    if workspace is None:
+        need = int(lib.msq_verify_draft_workspace_bytes(d))
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=target.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on target's device")
+    status = lib.msq_verify_draft(d, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  cuda._cuda_getCurrentRawStream(index))
+    if status:
+        raise MsqError(status, "msq_verify_draft")
+    return token, taken, path

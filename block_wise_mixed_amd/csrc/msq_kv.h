@@ -51,4 +51,10 @@ msq_status kv_views(const msq_kv_cache* cache, const msq_kv_seqs* seqs, KvCacheV
 // The pointers of both structs: present and aligned.
 msq_status kv_pointers(const msq_kv_cache* cache, const msq_kv_seqs* seqs);
 
+
+// A number for one call (msq_kv_attn.hip): never 0, and from a start that depends on the
+// time, the process and where it was loaded, so that no call finds its number in what a
+// workspace held before.
+uint64_t next_call();
+
 }  // namespace msq

@@ -95,6 +95,8 @@ struct AttnArgs {
   int span_tiles;  // tiles of one such part (more where nsplit parts cannot cover the range)
   int row_tiles, tile_rows, tile_shift;  // tiles of tile_rows x 2^tile_shift tokens
   float c2;        // scale * log2 e
+  const uint32_t* sets;  // [total][words]: which of the call's rows a row sees (kTree)
+  int words;
 };
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -303,6 +305,62 @@ __device__ inline void row_range(const AttnArgs& a, int len, int n, int i, int& 
   hi = min(hi, a.s.width << a.c.shift);
 }
 
+// The same for rows that see, of their call's n rows, those of a set: from lo on, and of
+// the call's own (at positions len - n + j) those that the set has.  A window counts
+// from the end of what a row sees, so lo is the first of the set that it still holds, or
+// as far before the call's rows as the set leaves of it.
+__device__ inline void tree_range(const AttnArgs& a, int len, int n, int row, int& lo, int& hi) {
+  lo = 0;
+  hi = min(len, a.s.width << a.c.shift);
+  if (a.window <= 0) return;
+  const uint32_t* set = a.sets + (int64_t)row * a.words;
+  const int words = min(a.words, (n + 31) >> 5);
+  auto word = [&](int w) { return n - 32 * w >= 32 ? set[w] : set[w] & ((1u << (n - 32 * w)) - 1); };
+  int size = 0;
+  for (int w = 0; w < words; ++w) size += __popc(word(w));
+  lo = max(len - n + size - a.window, 0);
+  if (size <= a.window) return;
+  for (int w = 0, skip = size - a.window; w < words; ++w) {
+    uint32_t m = word(w);
+    const int here = __popc(m);
+    if (skip >= here) {
+      skip -= here;
+      continue;
+    }
+    for (; skip > 0; --skip) m &= m - 1;
+    lo = max(len - n + 32 * w + __ffs(m) - 1, 0);
+    return;
+  }
+}
+// Bits of the tokens tok .. tok + 31 that a row with this set sees, as far as the set says.
+__device__ inline uint32_t tree_bits(const AttnArgs& a, const uint32_t* set, int x) {  // x = tok - (len - n)
+  if (x <= -32) return ~0u;
+  if (x < 0) return set[0] << -x | ((1u << -x) - 1);
+  const int w = x >> 5;
+  const uint32_t low = w < a.words ? set[w] : 0, high = w + 1 < a.words ? set[w + 1] : 0;
+  return (uint32_t)(((uint64_t)high << 32 | low) >> (x & 31));
+}
+
+// What the rows i .. j of n see: from lo to hi - 1 between them, and from lo_last to
+// hi_first - 1 every one of them.
+template <bool kTree>
+__device__ inline void rows_range(const AttnArgs& a, int len, int n, int i, int j, int& lo, int& hi_first,
+                                  int& lo_last, int& hi) {
+  if constexpr (kTree) {
+    const int before = len - n;
+    hi = min(len, a.s.width << a.c.shift);
+    hi_first = min(max(before, 0), hi);
+    lo = lo_last = 0;
+    if (a.window > 0) {
+      lo = max(before - a.window, 0);
+      lo_last = max(a.window < n ? len : len - a.window, 0);
+    }
+  } else {
+    row_range(a, len, n, i, lo, hi_first);
+    row_range(a, len, n, j, lo_last, hi);
+  }
+}
+
 __device__ inline int length_of(const AttnArgs& a, int b) { return max(a.kv_len[b], 0); }
 
 __device__ inline void write_row(const AttnArgs& a, int64_t at, int n, const float* x) {
@@ -336,11 +394,11 @@ struct Parts {
   int span, parts;     // tiles per part, parts that have tiles
 };
 __device__ inline int over(int x, int y) { return (int)((unsigned)x / (unsigned)y); }
+template <bool kTree>
 __device__ inline Parts parts_of(const AttnArgs& a, int len, int n, int r0) {
   Parts p;
   const int last = min(r0 + a.tile_rows, n * a.G) - 1;
-  row_range(a, len, n, over(r0, a.G), p.lo, p.hi_first);
-  row_range(a, len, n, over(last, a.G), p.lo_last, p.hi);
+  rows_range<kTree>(a, len, n, over(r0, a.G), over(last, a.G), p.lo, p.hi_first, p.lo_last, p.hi);
   p.first = p.lo >> a.tile_shift;
   p.end = max(p.first, (p.hi + (1 << a.tile_shift) - 1) >> a.tile_shift);
   p.span = max(a.span_tiles, p.end - p.first);
@@ -421,7 +479,7 @@ __device__ inline void load_tile(Tile<D>& t, const KvCacheView& c, int id, int h
   for (int i = 0; i < D / 32; ++i) t.v[i] = v[64 * i];
 }
 
-template <int D, bool kFine>
+template <int D, bool kFine, bool kTree>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
   constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
   constexpr int kStride = D + 4;
@@ -434,7 +492,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   kv_rows(a.s, b, row0, n);
   const int rows = n * a.G, r0 = tile_row * kRowTile;
   if (r0 >= rows) return;
-  const Parts pt = parts_of(a, len, n, r0);
+  const Parts pt = parts_of<kTree>(a, len, n, r0);
   const int lo1 = pt.lo_last, hi0 = pt.hi_first;
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   const int parts = pt.parts;
@@ -444,7 +502,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   const int r = min(r0 + col, rows - 1);
   const int i = over(r, a.G), hq = h * a.G + r - i * a.G;
   int my_lo, my_hi;
-  row_range(a, len, n, i, my_lo, my_hi);
+  if constexpr (kTree)
+    tree_range(a, len, n, row0 + i, my_lo, my_hi);
+  else
+    row_range(a, len, n, i, my_lo, my_hi);
 
   // query fragments: slots (g, e) of step 2c + u are dims 64c + 16g + 8u + e
   half8 q[kSteps];
@@ -519,6 +580,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
         const int p = tok + 4 * g + e;
         if (p < my_lo || p >= my_hi) s0[e] = -INFINITY;
         if (p + 16 < my_lo || p + 16 >= my_hi) s1[e] = -INFINITY;
+      }
+      if constexpr (kTree) {
+        const uint32_t seen = tree_bits(a, a.sets + (int64_t)(row0 + i) * a.words, tok - (len - n)) >> 4 * g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!(seen >> e & 1)) s0[e] = -INFINITY;
+          if (!(seen >> (e + 16) & 1)) s1[e] = -INFINITY;
+        }
       }
     }
     uint32_t in_l = in;  // what its weights have in L
@@ -763,7 +832,7 @@ struct Prefill {
   }
 };
 
-template <int D, int W, bool kFine>
+template <int D, int W, bool kFine, bool kTree>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
   using C = Prefill<D, W>;
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
@@ -789,7 +858,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   kv_rows(a.s, b, row0, n);
   const int rows = n * a.G, r0 = tile_row * C::kRows;
   if (r0 >= rows) return;
-  const Parts pt = parts_of(a, len, n, r0);
+  const Parts pt = parts_of<kTree>(a, len, n, r0);
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   if (t0 >= t1 && a.nsplit > 1) return;
   if (t0 != guess) id0 = blocks_at(t0), id1 = blocks_at(t0 + kBatch), id2 = blocks_at(t0 + 2 * kBatch);
@@ -803,10 +872,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   for (int s = 0; s < kSteps; ++s)
     qraw[s] = load8(a.q, a.q_f32, (int64_t)(row0 + i) * a.qts + (int64_t)hq * a.qhs + 8 * half + 16 * s);
   int my_lo, my_hi;
-  row_range(a, len, n, i, my_lo, my_hi);
+  const int i_row = i;
+  if constexpr (kTree)
+    tree_range(a, len, n, row0 + i, my_lo, my_hi);
+  else
+    row_range(a, len, n, i, my_lo, my_hi);
   int w_lo, w_hi, w_lo_last, w_hi_first;
-  row_range(a, len, n, over(min(w0, rows - 1), a.G), w_lo, w_hi_first);
-  row_range(a, len, n, over(min(w0 + 31, rows - 1), a.G), w_lo_last, w_hi);
+  rows_range<kTree>(a, len, n, over(min(w0, rows - 1), a.G), over(min(w0 + 31, rows - 1), a.G), w_lo, w_hi_first,
+                    w_lo_last, w_hi);
   if (w0 >= rows) w_hi = 0;
   // its stages: a0 .. a1 - 1 (none: a0 == a1)
   const int a0 = min(max(t0, w_lo / kStage), t1);
@@ -931,6 +1004,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
       for (int e = 0; e < 16; ++e) {
         const int at = tok + 8 * (e >> 3) + 4 * half + (e & 3) + 16 * ((e >> 2) & 1);
         if (at < my_lo || at >= my_hi || gone) s[e] = -INFINITY;
+      }
+      if constexpr (kTree) {
+        const uint32_t seen = tree_bits(a, a.sets + (int64_t)(row0 + i_row) * a.words, tok - (len - n)) >> 4 * half;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (!(seen >> (8 * (e >> 3) + (e & 3) + 16 * ((e >> 2) & 1)) & 1)) s[e] = -INFINITY;
       }
     }
     const float add = lam - M;
@@ -1138,7 +1217,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
 // parts, in order, and with four of them one another's sums.  Bound by its
 // chain of loads (lengths, M and L, partial sums), 2 to 3 us, or for many rows by
 // the partials' traffic, 4 D bytes a row and part.
-template <int D, int kWaves>
+template <int D, int kWaves, bool kTree>
 __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
   constexpr int kPer = D / 64;
   __shared__ float sums[kWaves == 4 ? 4 : 1][D];
@@ -1154,7 +1233,7 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
   const int len = length_of(a, b);
   // the row tile this row was in, as the split kernel saw it
   const int r = i * a.G + hq - over(hq, a.G) * a.G;
-  const Parts pt = parts_of(a, len, n, over(r, a.tile_rows) * a.tile_rows);
+  const Parts pt = parts_of<kTree>(a, len, n, over(r, a.tile_rows) * a.tile_rows);
   const int parts = pt.parts;
   const int64_t orow = (int64_t)(row0 + i) * a.Hq + hq, step = (int64_t)a.s.total * a.Hq;
   const float2 ml = lane < parts ? a.part_ml[lane * step + orow] : make_float2(kNone, 0.f);
@@ -1423,9 +1502,35 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   return MSQ_OK;
 }
 
-// A number for one call: never 0, and from a start that depends on the time, the
-// process and where it was loaded, so that no call finds its number in what a
-// workspace held before.
+template <int D, bool kFine, bool kTree>
+hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  if (p.waves) {
+    auto prefill = [&](auto w) {
+      using C = Prefill<D, decltype(w)::value>;
+      hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves, kFine, kTree>), dim3((unsigned)p.blocks), dim3(C::kThreads),
+                         C::kLds, stream, a);
+    };
+    if constexpr (D != 256)
+      if (p.waves == 8) prefill(std::integral_constant<int, 8>{});
+    if (p.waves == 4) prefill(std::integral_constant<int, 4>{});
+  } else {
+    const size_t lds = 4 * kRowTile * (D + 4 + 3) * 4;
+    hipLaunchKernelGGL((k_kv_decode<D, kFine, kTree>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
+  }
+  if (p.nsplit > 1 && !p.tags_at) {
+    const int rows = a.s.batch * a.s.max_count * a.Hq;
+    // few rows: four wavefronts each (64 rows of 60 parts: 12.1 -> 9.6 us; 4800 rows of 17
+    // parts: 34.7 -> 43.1)
+    if (rows <= 1024)
+      hipLaunchKernelGGL((k_kv_join<D, 4, kTree>), dim3((unsigned)rows), dim3(256), 0, stream, a, rows);
+    else
+      hipLaunchKernelGGL((k_kv_join<D, 1, kTree>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, rows);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
 uint64_t next_call() {
   static std::atomic<uint64_t> count{0};
   static const uint64_t start = [] {
@@ -1439,34 +1544,6 @@ uint64_t next_call() {
   return n ? n : start + count.fetch_add(1, std::memory_order_relaxed);
 }
 
-template <int D, bool kFine>
-hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  if (p.waves) {
-    auto prefill = [&](auto w) {
-      using C = Prefill<D, decltype(w)::value>;
-      hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves, kFine>), dim3((unsigned)p.blocks), dim3(C::kThreads),
-                         C::kLds, stream, a);
-    };
-    if constexpr (D != 256)
-      if (p.waves == 8) prefill(std::integral_constant<int, 8>{});
-    if (p.waves == 4) prefill(std::integral_constant<int, 4>{});
-  } else {
-    const size_t lds = 4 * kRowTile * (D + 4 + 3) * 4;
-    hipLaunchKernelGGL((k_kv_decode<D, kFine>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
-  }
-  if (p.nsplit > 1 && !p.tags_at) {
-    const int rows = a.s.batch * a.s.max_count * a.Hq;
-    // few rows: four wavefronts each (64 rows of 60 parts: 12.1 -> 9.6 us; 4800 rows of 17
-    // parts: 34.7 -> 43.1)
-    if (rows <= 1024)
-      hipLaunchKernelGGL((k_kv_join<D, 4>), dim3((unsigned)rows), dim3(256), 0, stream, a, rows);
-    else
-      hipLaunchKernelGGL((k_kv_join<D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, rows);
-  }
-  return hipGetLastError();
-}
-
-}  // namespace
 }  // namespace msq
 
 using namespace msq;
@@ -1502,9 +1579,13 @@ extern "C" size_t msq_kv_attention_workspace_bytes(const msq_kv_cache* cache,
   return most;
 }
 
-extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
-                                       const msq_kv_attn* attn, void* workspace,
-                                       size_t workspace_bytes, hipStream_t stream) {
+namespace {
+
+// Both attentions; sets null: no tree.
+template <bool kTree>
+msq_status attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const msq_kv_attn* attn,
+                     const uint32_t* sets, int words, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream) {
   if (!attn) return MSQ_ERR_INVALID_ARG;
   AttnArgs a{};
   msq_status st = kv_views(cache, seqs, a.c, a.s);
@@ -1553,12 +1634,33 @@ extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_s
   a.tile_rows = p.tile_rows;
   a.tile_shift = p.tile_tokens == 64 ? 6 : 5;
   a.c2 = (t.scale > 0.f ? t.scale : 1.f / std::sqrt((float)D)) * kLog2e;
+  a.sets = sets;
+  a.words = words;
   const bool fine = a.q_f32 && a.out_f32;
   hipError_t e;
   switch (D) {
-    case 64: e = fine ? launch_attn<64, true>(a, p, stream) : launch_attn<64, false>(a, p, stream); break;
-    case 128: e = fine ? launch_attn<128, true>(a, p, stream) : launch_attn<128, false>(a, p, stream); break;
-    default: e = fine ? launch_attn<256, true>(a, p, stream) : launch_attn<256, false>(a, p, stream); break;
+    case 64: e = fine ? launch_attn<64, true, kTree>(a, p, stream) : launch_attn<64, false, kTree>(a, p, stream); break;
+    case 128: e = fine ? launch_attn<128, true, kTree>(a, p, stream) : launch_attn<128, false, kTree>(a, p, stream); break;
+    default: e = fine ? launch_attn<256, true, kTree>(a, p, stream) : launch_attn<256, false, kTree>(a, p, stream); break;
   }
   return e == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" msq_status msq_kv_attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
+                                       const msq_kv_attn* attn, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream) {
+  return attention<false>(cache, seqs, attn, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+extern "C" msq_status msq_kv_attention_tree(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
+                                            const msq_kv_attn* attn, const uint32_t* sets, int32_t words,
+                                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!attn || !attn->causal) return MSQ_ERR_INVALID_ARG;
+  if (seqs && (seqs->batch == 0 || seqs->total == 0))  // nothing to do: no pointer is looked at
+    return attention<true>(cache, seqs, attn, nullptr, 0, workspace, workspace_bytes, stream);
+  if (words < 1) return MSQ_ERR_SHAPE;
+  if (!sets || !aligned_to(sets, 4)) return MSQ_ERR_INVALID_ARG;
+  return attention<true>(cache, seqs, attn, sets, words, workspace, workspace_bytes, stream);
 }

@@ -523,6 +523,158 @@ msq_status msq_kv_attention(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
                             const msq_kv_attn *attn, void *workspace, size_t workspace_bytes,
                             hipStream_t stream);
 
+/* ---- rotary positions -------------------------------------------------------
+ * Queries and keys are rotated by their positions before a layer's attention: of
+ * the first dims values of a head, the values a, b of pair i become
+ *     a cos - b sin,  b cos + a sin     with the angle position * freq[i],
+ * the others stay.  Pairs are the dims i and dims / 2 + i, or 2 i and 2 i + 1
+ * (interleaved).  The frequencies are the caller's, so that any rule for long
+ * contexts can be had.  In detail, so that results can be told bit for bit: the
+ * angle is rounded to fp64; its cosine and sine are taken in fp64 (2 units in the
+ * last place), times amplitude, and rounded to fp32; products, sum and difference are
+ * fp32 with one rounding an operation; a bf16 result is rounded once more.  Exact
+ * for |angle| up to 2^32; past that the angles (not the memory accesses) may be
+ * anything.  Negated positions give the inverse rotation, which is also the rotation's
+ * transpose (its gradient), amplitude included. */
+typedef struct {
+  const double *freq;  /* device, [dims / 2], 8-byte aligned: radians a position */
+  int32_t dims;        /* rotated values of a head: a multiple of 16 */
+  int32_t interleaved; /* nonzero: neighbours are pairs */
+  double amplitude;    /* of cosine and sine, finite; 0: 1 */
+} msq_rotary;
+
+/* Rows [rows][heads][head_dim] and where they go; x == out with the same strides and
+ * type rotates in place, other overlaps are not allowed. */
+typedef struct {
+  const void *x;           /* of x_dtype, 16-byte aligned, dims contiguous */
+  int64_t x_token_stride;  /* in elements; byte strides multiples of 16 */
+  int64_t x_head_stride;
+  void *out;               /* of out_dtype, likewise */
+  int64_t out_token_stride;
+  int64_t out_head_stride;
+  int32_t x_dtype, out_dtype;
+  int32_t heads;           /* >= 1 */
+  int32_t head_dim;        /* a multiple of 16, 16 to MSQ_ROTARY_MAX_DIM */
+} msq_rotary_rows;
+#define MSQ_ROTARY_MAX_DIM 1024
+
+/* Rotates row i to position positions[i] (device int32 [rows]).  One launch (more where
+ * 2^32 threads do not do), asynchronous.  rows == 0 is a no-op.  Errors:
+ * MSQ_ERR_INVALID_ARG (null or misaligned pointer, unknown dtype, an amplitude that is
+ * not finite), MSQ_ERR_SHAPE (heads or head_dim outside the ranges above, dims no
+ * positive multiple of 16 or above head_dim, rows negative or past 2^31 - 1),
+ * MSQ_ERR_HIP. */
+msq_status msq_rotary_apply(const msq_rotary *rot, const msq_rotary_rows *x, const int32_t *positions,
+                            int64_t rows, hipStream_t stream);
+
+/* New tokens of msq_kv_append. */
+typedef struct {
+  const void *k;            /* [kv_rows][kv_heads][head_dim] of dtype, strides as msq_kv_write's */
+  int64_t k_token_stride, k_head_stride;
+  const void *v;
+  int64_t v_token_stride, v_head_stride;
+  int32_t dtype;
+  int64_t kv_rows;          /* rows that k and v have, 1 .. 2^31 - 1; without source at least total */
+  const int32_t *source;    /* [total]: the row of k and v that each row of the call takes (entries
+                               are clamped to 0 .. kv_rows - 1); null: its own */
+  const int32_t *count;     /* [batch]: of sequence b's rows only the first count[b]; null: all */
+  const int32_t *positions; /* [total]: what the rows are rotated to; null: their positions in the cache */
+  msq_rotary rot;           /* of k and q; dims 0: none of either */
+  msq_rotary_rows q;        /* queries of the call's rows, [total]; x null: none.  heads any, head_dim the
+                               cache's */
+} msq_kv_new;
+
+/* msq_kv_write of rotated keys and of values, and the rotation of the same tokens'
+ * queries.  The keys enter the quantiser as the fp32 results of the rotation.  With
+ * source and count, rows that were written before are written again: the drafted tokens
+ * that msq_verify_draft keeps (its path and taken) then stand in the cache one after
+ * another.  Query rows of sequences with first < 0, past count or outside every
+ * sequence are left as they are.  Launches and errors as msq_kv_write and
+ * msq_rotary_apply; MSQ_ERR_INVALID_ARG also for queries together with source. */
+msq_status msq_kv_append(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
+                         const msq_kv_new *rows, hipStream_t stream);
+
+/* ---- drafted tokens ---------------------------------------------------------
+ * A small model drafts tokens of a sequence, as a chain or a tree; the large one
+ * takes all of them in one call, and as many are kept as its probabilities allow.
+ * The rows of a sequence in that call are nodes: row 0 is the last token that is
+ * certain, every other row a drafted one below its parent, parents[row] (counted in the
+ * sequence, smaller than its own number).  A parent below 0, or not smaller, makes the
+ * row a root of its own. */
+#define MSQ_DRAFT_MAX_ROWS 1024 /* of a sequence: rows past it are not processed */
+
+/* For every row the set of the sequence's rows that it sees, itself and its ancestors (row j
+ * is bit j % 32 of word j / 32), and its position, first[b] and its depth.  offset, total,
+ * max_count as in msq_kv_seqs; sets: device uint32 [total][words]; positions: device
+ * int32 [total] or null; first: device int32 [batch] or null (0).  Rows past
+ * max_count or MSQ_DRAFT_MAX_ROWS, or outside every sequence, are left as they are.  words
+ * must hold the smaller of max_count and MSQ_DRAFT_MAX_ROWS.  One launch, asynchronous.
+ * Errors: MSQ_ERR_INVALID_ARG, MSQ_ERR_SHAPE (also words too small), MSQ_ERR_HIP. */
+msq_status msq_draft_tree(const int32_t *parents, const int32_t *offset, int32_t batch, int64_t total,
+                          int32_t max_count, const int32_t *first, uint32_t *sets, int32_t words,
+                          int32_t *positions, hipStream_t stream);
+
+/* msq_kv_attention for such rows: row i of n sees the cached tokens before the call's own
+ * (positions up to kv_len - n) and of these, at positions kv_len - n + j, the rows j
+ * that its set has (device uint32 [total][words]; rows past 32 * words are in no set);
+ * with a window the last window of them all.  Any sets will do, also empty ones and
+ * ones without the row itself.  attn->causal must be set.  Plan, workspace and errors
+ * as msq_kv_attention's; MSQ_ERR_INVALID_ARG also for null or misaligned sets,
+ * MSQ_ERR_SHAPE for words < 1. */
+msq_status msq_kv_attention_tree(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const msq_kv_attn *attn,
+                                 const uint32_t *sets, int32_t words, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/* One verification. */
+typedef struct {
+  int32_t batch;          /* sequences, >= 0 */
+  const int32_t *offset;  /* [batch + 1] or null, as in msq_kv_seqs */
+  int64_t total;          /* rows of all sequences, 0 .. 2^31 - 1 */
+  int32_t max_count;      /* at least the largest sequence's rows; 0: total / batch with a null
+                             offset, else total.  Rows past it or MSQ_DRAFT_MAX_ROWS count as not there */
+  int32_t vocab;          /* entries of a distribution, >= 1 */
+  const int32_t *tokens;  /* [total]: the drafted tokens (those of rows 0 are not looked at) */
+  const int32_t *parents; /* [total] or null: a chain, the row before */
+  const void *target;     /* [total][vocab] of dtype, the large model's entries after each row */
+  int64_t target_stride;  /* of a row, in elements, >= vocab */
+  const void *draft;      /* likewise what the children of each row were drawn from; null: tokens chosen
+                             otherwise than by chance */
+  int64_t draft_stride;
+  int32_t dtype;          /* of target and draft, element-aligned */
+  const float *uniform;   /* [total] numbers in [0, 1): row i's decides on its token, row 0's is the number
+                             the next token is drawn with; null: by the largest entries */
+  int32_t *token;         /* [batch]: the next token; -1 for a sequence without rows or a distribution
+                             without any mass */
+  int32_t *taken;         /* [batch]: rows kept, row 0 among them */
+  int32_t *path;          /* [total]: those rows, counted in the call, from the sequence's first row on;
+                             -1 behind them */
+} msq_draft;
+
+/* Which drafted tokens the target's probabilities keep, and the next token.  From row 0 on,
+ * the rows below the row c reached are looked at in their order; the first that is taken
+ * becomes the row reached.  Where none is, the walk ends.
+ *   By chance: r is the target's distribution after c and m = 1.  A row with token x
+ *   and number u is taken if u * q(x) * m < r(x), q the draft's distribution after c;
+ *   if not, r becomes max(r / m - q, 0) and m its sum.  Without draft: q(x) = 1, r(x)
+ *   becomes 0, and m falls by it.  In the end the next token is the first whose
+ *   running sum of r passes u times the sum of all r, u row 0's number; r as at the
+ *   start if that sum is 0.  So every token comes out as likely as the target makes it
+ *   if siblings were drawn from q one after another, or, without draft, are distinct.
+ *   By the largest entries (uniform null; draft is not looked at): a row is taken if its
+ *   token is the target's largest entry after c (of equal ones the first; NaN is none),
+ *   which else is the next token.  Entries may be logits here.
+ * Entries that are negative, NaN or infinite count as 0 by chance; a number outside [0, 1]
+ * or NaN as the nearer end or 0; a token outside 0 .. vocab - 1 is not taken.  All
+ * arithmetic is fp64.  Rows outside every sequence: path is left as it is.
+ * workspace: msq_verify_draft_workspace_bytes, 256-byte aligned, holding anything; calls that
+ * share one must be ordered on one stream.  One launch, or by the largest entries two.
+ * Asynchronous, and the same results every time.  Errors: MSQ_ERR_INVALID_ARG,
+ * MSQ_ERR_SHAPE, MSQ_ERR_BUFFER_TOO_SMALL, MSQ_ERR_HIP. */
+msq_status msq_verify_draft(const msq_draft *d, void *workspace, size_t workspace_bytes, hipStream_t stream);
+/* Bytes that it needs at most for calls of these sizes (batch, total, max_count, vocab, whether
+ * offset, parents, draft and uniform are null) or a smaller vocab or total; 0 for sizes that it refuses. */
+size_t msq_verify_draft_workspace_bytes(const msq_draft *d);
+
 /* Static English text for a status code; never NULL.  Takes an int so that
  * any value a caller holds, including one outside the enum, is defined input
  * ("unknown status"). */
