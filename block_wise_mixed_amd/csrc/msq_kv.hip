@@ -53,9 +53,9 @@ __global__ __launch_bounds__(1024) void k_kv_write(WriteArgs a) {
   const T* src = reinterpret_cast<const T*>(tk.values ? a.v : a.k) +
                  tk.h * (tk.values ? a.vhs : a.khs);
   const int64_t ts = tk.values ? a.vts : a.kts;
+  const int lane = threadIdx.x & 63;
   write_block<D, E, Raw8<T>>(
-      a.c, tk.values, (int64_t)sp.id * a.c.H + tk.h, sp.lo, sp.hi, part_max, [&](Raw8<T>(&raw)[Mp::kRows]) {
-        const int lane = threadIdx.x & 63;
+      a.c, tk.values, (int64_t)sp.id * a.c.H + tk.h, sp.lo, sp.hi, part_max, lane, [&](Raw8<T>(&raw)[Mp::kRows]) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int s0 = 32 * (wave / (D / E)), part = wave % (D / E) * (E / 8) + Mp::part(lane);
 #pragma unroll

@@ -47,25 +47,22 @@ __device__ inline int64_t source_of(const AppendArgs& a, int64_t row) {
   return a.source ? min(max(a.source[row], 0), a.kv_rows - 1) : row;
 }
 
-// A lane's pieces of rotated keys: raw values and, where they are rotated in halves, the
-// ones they are paired with; then the results in fp32.
+// The keys of one block, some heads one after another.  A lane reads its pieces and,
+// where they are rotated in halves, the ones that these are paired with.  kTable: the
+// turns of all new slots fit the LDS; else each lane makes its own (slower: blocks of
+// 256 tokens with more than 128 rotated dims of heads of 256 only).
 template <int D, int E, typename T, bool kTable>
 __device__ __forceinline__ void append_keys(const AppendArgs& a, const Span& sp, int h0, int heads,
                                             float (&part_max)[2][16]) {
   using Mp = Map<E>;
-  const int lane = threadIdx.x & 63;
+  constexpr int kAtOnce = Mp::kRows * (int)sizeof(T) > 16 ? 8 / (int)sizeof(T) : Mp::kRows;  // rows read before the first is rotated
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int s0 = 32 * (wave / (D / E)), part = wave % (D / E) * (E / 8) + Mp::part(lane);
-  const int half = a.r.half;
-  // dims 8 part .. : rotated in halves (mate: the paired dims), with their neighbours, or not
-  const bool turned = 8 * part < 2 * half, split = turned && !a.r.interleaved;
-  const bool high = split && 8 * part >= half;
-  const int mate = high ? 8 * part - half : 8 * part + half;
-  const int pair0 = split ? (high ? mate : 8 * part) : 4 * part;
+  const int s0 = 32 * (wave / (D / E)), half = a.r.half;
   auto position = [&](int slot) { return a.positions ? a.positions[sp.row + slot] : (int)(sp.base + slot); };
   float2* const turns = reinterpret_cast<float2*>(smem_codes);  // [slot - lo][half]
   if constexpr (kTable) {
-    for (unsigned n = threadIdx.x; n < (unsigned)((sp.hi - sp.lo) * half); n += blockDim.x) {
+    const unsigned all = (unsigned)((sp.hi - sp.lo) * half);
+    for (unsigned n = threadIdx.x; n < all; n += blockDim.x) {
       const int slot = (int)(n / (unsigned)half), pair = (int)(n - slot * (unsigned)half);
       turns[n] = turn_of(position(sp.lo + slot), a.r.freq[pair], a.r.amplitude);
     }
@@ -74,51 +71,64 @@ __device__ __forceinline__ void append_keys(const AppendArgs& a, const Span& sp,
   for (int j = 0; j < heads; ++j) {
     const int h = h0 + j;
     const T* src = reinterpret_cast<const T*>(a.k) + h * a.khs;
+    // (what follows from the lane is not to be kept from head to head: the registers do not hold it)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    // dims 8 part .. : rotated in halves (mate: the paired dims), with their neighbours, or not
+    const int part = wave % (D / E) * (E / 8) + Mp::part(lane);
+    const bool turned = 8 * part < 2 * half, split = turned && !a.r.interleaved;
+    const bool high = split && 8 * part >= half;
+    const int mate = high ? 8 * part - half : 8 * part + half;
+    const int pair0 = split ? (high ? mate : 8 * part) : 4 * part;
     write_block<D, E, Raw8<float>>(
-        a.c, false, (int64_t)sp.id * a.c.H + h, sp.lo, sp.hi, part_max[j & 1], [&](Raw8<float>(&out)[Mp::kRows]) {
-          Raw8<T> own[Mp::kRows], other[Mp::kRows];
+        a.c, false, (int64_t)sp.id * a.c.H + h, sp.lo, sp.hi, part_max[j & 1], lane, [&](Raw8<float>(&out)[Mp::kRows]) {
 #pragma unroll
-          for (int u = 0; u < Mp::kRows; ++u) {
-            const int slot = s0 + Mp::row(lane, u);
-            if (slot < sp.lo || slot >= sp.hi) continue;
-            const T* p = src + source_of(a, sp.row + slot) * a.kts;
-            own[u].load(p + 8 * part);
-            if (split) other[u].load(p + mate);
-          }
+          for (int u0 = 0; u0 < Mp::kRows; u0 += kAtOnce) {
+            Raw8<T> own[kAtOnce], other[kAtOnce];
 #pragma unroll
-          for (int u = 0; u < Mp::kRows; ++u) {
-            const int slot = s0 + Mp::row(lane, u);
-            if (slot < sp.lo || slot >= sp.hi) continue;
-            float x[8];
-            own[u].get(x);
-            if (turned) {
-              float2 t[8];
-              if constexpr (kTable) {
-                const float4* from = reinterpret_cast<const float4*>(turns + (slot - sp.lo) * half + pair0);
-                reinterpret_cast<float4*>(t)[0] = from[0];
-                reinterpret_cast<float4*>(t)[1] = from[1];
-                if (split) {
-                  reinterpret_cast<float4*>(t)[2] = from[2];
-                  reinterpret_cast<float4*>(t)[3] = from[3];
-                }
-              } else {
-                const int at = position(slot);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (i < 4 || split) t[i] = turn_of(at, a.r.freq[pair0 + i], a.r.amplitude);
-              }
-              if (split) {
-                float y[8];
-                other[u].get(y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = high ? turned_high(x[i], y[i], t[i]) : turned_low(x[i], y[i], t[i]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], t[i]);
-              }
+            for (int u = 0; u < kAtOnce; ++u) {
+              const int slot = s0 + Mp::row(lane, u0 + u);
+              if (slot < sp.lo || slot >= sp.hi) continue;
+              const T* p = src + source_of(a, sp.row + slot) * a.kts;
+              own[u].load(p + 8 * part);
+              if (split) other[u].load(p + mate);
             }
-            out[u].a = make_float4(x[0], x[1], x[2], x[3]);
-            out[u].b = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+              const int slot = s0 + Mp::row(lane, u0 + u);
+              if (slot < sp.lo || slot >= sp.hi) continue;
+              float x[8];
+              own[u].get(x);
+              if (turned) {
+                float2 t[8];
+                if constexpr (kTable) {
+                  const float4* at = reinterpret_cast<const float4*>(turns + (slot - sp.lo) * half + pair0);
+                  reinterpret_cast<float4*>(t)[0] = at[0];
+                  reinterpret_cast<float4*>(t)[1] = at[1];
+                  if (split) {
+                    reinterpret_cast<float4*>(t)[2] = at[2];
+                    reinterpret_cast<float4*>(t)[3] = at[3];
+                  }
+                } else {
+                  const int at = position(slot);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (i < 4 || split) t[i] = turn_of(at, a.r.freq[pair0 + i], a.r.amplitude);
+                }
+                if (split) {
+                  float y[8];
+                  other[u].get(y);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    x[i] = high ? turned_high(x[i], y[i], t[i]) : turned_low(x[i], y[i], t[i]);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], t[i]);
+                }
+              }
+              out[u0 + u].a = make_float4(x[0], x[1], x[2], x[3]);
+              out[u0 + u].b = make_float4(x[4], x[5], x[6], x[7]);
+            }
           }
         });
   }
@@ -155,9 +165,9 @@ __global__ __launch_bounds__(1024) void k_kv_append(AppendArgs a) {
     return;
   }
   const T* src = reinterpret_cast<const T*>(a.v) + set * a.vhs;
+  const int lane = threadIdx.x & 63;
   write_block<D, E, Raw8<T>>(
-      a.c, true, (int64_t)sp.id * a.c.H + set, sp.lo, sp.hi, part_max[0], [&](Raw8<T>(&raw)[Mp::kRows]) {
-        const int lane = threadIdx.x & 63;
+      a.c, true, (int64_t)sp.id * a.c.H + set, sp.lo, sp.hi, part_max[0], lane, [&](Raw8<T>(&raw)[Mp::kRows]) {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int s0 = 32 * (wave / (D / E)), part = wave % (D / E) * (E / 8) + Mp::part(lane);
 #pragma unroll
@@ -168,23 +178,21 @@ __global__ __launch_bounds__(1024) void k_kv_append(AppendArgs a) {
       });
 }
 
-// Most LDS for a table of turns: two workgroups a compute unit.
-constexpr size_t kMostTable = 64 << 10;
+// Most LDS for a table of turns (a compute unit has 160 KB).
+constexpr size_t kMostTable = 128 << 10;
 
 template <int D, typename T>
 msq_status launch_append(AppendArgs& a, int64_t lists, bool queries, hipStream_t stream) {
   const int strips = 1 << (a.c.shift - 5), P = 1 << a.c.shift;
   const bool wide = a.s.max_count >= 16 && strips * (D / 64) <= 16;
   const int waves = strips * (D / (wide || D == 64 ? 64 : 128)), threads = 64 * waves;
-  const int tokens = std::min(P, a.s.max_count);
-  size_t table = (size_t)tokens * a.r.half * sizeof(float2);
-  const bool in_lds = table <= kMostTable;
-  if (!in_lds) table = 0;
+  const size_t table = (size_t)std::min(P, a.s.max_count) * a.r.half * sizeof(float2);
+  const bool fits = table <= kMostTable;
   // Heads of a workgroup of keys: more share the turns, fewer fill the GPU.
-  a.heads = in_lds ? (int)std::clamp<int64_t>(lists * a.c.H / 1024, 1, a.c.H) : 1;
+  a.heads = fits ? (int)std::clamp<int64_t>(lists * a.c.H / 1024, 1, a.c.H) : 1;
   a.groups = (a.c.H + a.heads - 1) / a.heads;
   int64_t query_sets = 0;
-  size_t lds = std::max(table, (size_t)waves * (wide || D == 64 ? Map<64>::kImage : Map<128>::kImage));
+  size_t lds = std::max(fits ? table : 0, (size_t)waves * (wide || D == 64 ? Map<64>::kImage : Map<128>::kImage));
   if (queries) {
     // four units of 16 values a thread, if there are as many
     const int row_units = a.q.units * a.q.heads;
@@ -203,14 +211,11 @@ msq_status launch_append(AppendArgs& a, int64_t lists, bool queries, hipStream_t
                          stream, a);
     });
   };
-  auto with = [&](auto in_table) {
-    if constexpr (D != 64)
-      if (!wide) return go(std::integral_constant<int, 128>{}, in_table);
-    return go(std::integral_constant<int, 64>{}, in_table);
-  };
-  if constexpr (D != 64)  // whose tables all fit
-    if (!in_lds) return with(std::false_type{});
-  return with(std::true_type{});
+  if constexpr (D == 256)
+    if (!fits) return go(std::integral_constant<int, 128>{}, std::false_type{});  // blocks of 256: not wide
+  if constexpr (D != 64)
+    if (!wide) return go(std::integral_constant<int, 128>{}, std::true_type{});
+  return go(std::integral_constant<int, 64>{}, std::true_type{});
 }
 
 }  // namespace

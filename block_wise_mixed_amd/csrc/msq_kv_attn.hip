@@ -41,7 +41,8 @@
 // bf16 alone is 1.7e-3.  The second term costs 2 to 4% in k_kv_decode and 18 to 29%
 // in k_kv_prefill (2048 rows of 64 heads on 16000 tokens 941 -> 1215 us).  L of the
 // rounded weights, which cancels some of their rounding: 1.9e-4 -> 1.7e-4 and 1.2e-4 ->
-// 0.7e-4, at 4% of the time of many rows; not taken.
+// 0.7e-4, at 4% of the time of many rows; not taken.  Attention by sets (kTree) has
+// both in two terms where the results are fp32, which are then some 1e-6 away.
 #include <hip/hip_runtime.h>
 #include <unistd.h>
 
@@ -198,6 +199,7 @@ __device__ inline void query_fragments(const Raw8 (&raw)[N], int f32, half8 (&q)
         q[s][2 * e] = (_Float16)(__uint_as_float(w[e] << 16) * up);
         q[s][2 * e + 1] = (_Float16)(__uint_as_float(w[e] & 0xFFFF0000u) * up);
       }
+      if constexpr (kFine) rest[s] = half8{};
     }
   }
 }
@@ -482,6 +484,7 @@ __device__ inline void load_tile(Tile<D>& t, const KvCacheView& c, int id, int h
 template <int D, bool kFine, bool kTree>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
   constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
+  constexpr bool kTwo = kFine && kTree;  // weights in two f16 terms
   constexpr int kStride = D + 4;
   const Place at_wg = place_of(a.c.H, a.nsplit, a.row_tiles);
   const int h = at_wg.h, sp = at_wg.part, tile_row = at_wg.low, b = at_wg.high;
@@ -621,20 +624,25 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
       }
     }
     float sum = 0.f;
-    half8 p;
+    half8 p, low;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float w = exp2_fast(fmaf(e < 4 ? s0[e & 3] : s1[e & 3], ff, add));
       sum += w;
       p[e] = (_Float16)w;
+      if constexpr (kTwo) low[e] = (_Float16)(w - (float)p[e]);
     }
     L = fmaf(sum, __uint_as_float(in_l), L);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       const uint4 v = tl.v[c];
-      o[2 * c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.x, v.y), p, o[2 * c], 0, 0, 0);
-      o[2 * c + 1] =
-          __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16x8(v.z, v.w), p, o[2 * c + 1], 0, 0, 0);
+      const half8 v0 = codes_f16x8(v.x, v.y), v1 = codes_f16x8(v.z, v.w);
+      o[2 * c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p, o[2 * c], 0, 0, 0);
+      o[2 * c + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p, o[2 * c + 1], 0, 0, 0);
+      if constexpr (kTwo) {
+        o[2 * c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, low, o[2 * c], 0, 0, 0);
+        o[2 * c + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, low, o[2 * c + 1], 0, 0, 0);
+      }
     }
   };
   for (int tb = t0 + wave; tb < t1; tb += 64 * kWaves) {
@@ -838,6 +846,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
   constexpr int kProducts = C::kProducts, kAhead = C::kAhead, kStrips = C::kStrips;
   constexpr int kRing = 2 * kStrips, kBatch = 64 / kStrips;
+  constexpr bool kTwo = kFine && kTree;  // weights in two f16 terms
+  constexpr int kTerms = kTwo ? 4 : 2;   // a strip's weights: the first terms, then what they leave
   const Place at_wg = place_of(a.c.H, a.nsplit, a.s.batch);
   const int h = at_wg.h, sp = at_wg.part, b = at_wg.low;
   const int tile_row = a.row_tiles - 1 - at_wg.high;  // the longest rows first
@@ -984,16 +994,19 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     return m < kSteps ? kl[m * 64] : vl[(2 * (v % kTiles) + v / kTiles) * 64];
   };
   half8 fr[kAhead];
-  auto values = [&](int i, const half8 (&p)[2]) {
+  auto values = [&](int i, const half8 (&p)[kTerms]) {
 #pragma unroll
-    for (int v = 0; v < 2 * kTiles; ++v)
-      o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-          operand(i + 1, kSteps + v), p[v / kTiles], o[v % kTiles], 0, 0, 0);
+    for (int v = 0; v < 2 * kTiles; ++v) {
+      const half8 x = operand(i + 1, kSteps + v);
+      o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, p[v / kTiles], o[v % kTiles], 0, 0, 0);
+      if constexpr (kTwo)
+        o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, p[2 + v / kTiles], o[v % kTiles], 0, 0, 0);
+    }
   };
   // Strip i: its scores s -> weights p; scores sn of strip i + 1; values of strip
   // i - 1 by their weights pp.  Lane (col, half), register e: row col, token
   // 8 (e / 8) + 4 half + e % 4 + 16 (e / 4 % 2).
-  auto strip = [&](int i, f32x16& s, f32x16& sn, half8 (&p)[2], const half8 (&pp)[2], auto which) {
+  auto strip = [&](int i, f32x16& s, f32x16& sn, half8 (&p)[kTerms], const half8 (&pp)[kTerms], auto which) {
     constexpr int kWhich = decltype(which)::value;  // of its stage
     const int tok = 32 * i;
     const bool gone = __builtin_amdgcn_readlane(id0, i - batch) < 0;
@@ -1014,7 +1027,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     }
     const float add = lam - M;
     float w[16], sum = 0.f;
-    half2v pairs[8];
+    half2v pairs[8], low[kTwo ? 8 : 1];
     sn = f32x16{};
     // (the empty asm statements keep each result at its place in this order)
     auto use = [&](int e) {
@@ -1023,6 +1036,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
       if (e & 1) {
         pairs[e >> 1] = half2v{(_Float16)w[e - 1], (_Float16)w[e]};
         asm volatile("" : "+v"(pairs[e >> 1]));
+        if constexpr (kTwo) {
+          low[e >> 1] = half2v{(_Float16)(w[e - 1] - (float)pairs[e >> 1][0]), (_Float16)(w[e] - (float)pairs[e >> 1][1])};
+          asm volatile("" : "+v"(low[e >> 1]));
+        }
       }
     };
     // A product, the read of a later one's operand, and a share of the vector
@@ -1035,9 +1052,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
         sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], q[m], sn, 0, 0, 0);
         if constexpr (kFine)
           sn = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], rest[m], sn, 0, 0, 0);
-      } else
+      } else {
         o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], pp[v / kTiles],
                                                                o[v % kTiles], 0, 0, 0);
+        if constexpr (kTwo)
+          o[v % kTiles] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[m % kAhead], pp[2 + v / kTiles],
+                                                                 o[v % kTiles], 0, 0, 0);
+      }
       if (m + kAhead < kProducts)
         fr[m % kAhead] = operand(i, m + kAhead);
       else if (kWhich < kStrips - 1)
@@ -1086,6 +1107,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
         const float y = exp2_fast(x);
         sum += y;
         pairs[e >> 1][e & 1] = (_Float16)y;
+        if constexpr (kTwo) low[e >> 1][e & 1] = (_Float16)(y - (float)pairs[e >> 1][e & 1]);
       }
     }
     uint32_t in_l = in;  // what its weights have in L
@@ -1099,13 +1121,17 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
     L = fmaf(sum, __uint_as_float(in_l), L);
     asm volatile("" : "+v"(L));
 #pragma unroll
-    for (int e = 0; e < 16; ++e) p[e >> 3][e & 7] = pairs[e >> 1][e & 1];
+    for (int e = 0; e < 16; ++e) {
+      p[e >> 3][e & 7] = pairs[e >> 1][e & 1];
+      if constexpr (kTwo) p[2 + (e >> 3)][e & 7] = low[e >> 1][e & 1];
+    }
   };
 
   if (t0 < t1) {
     f32x16 sa, sb;
-    half8 pa[2], pb[2];
-    pa[0] = pa[1] = pb[0] = pb[1] = half8{};
+    half8 pa[kTerms], pb[kTerms];
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) pa[k] = pb[k] = half8{};
     convert(st0, i0 - kStrips + 1, i0 - 1);
 #pragma unroll
     for (int u = 0; u < C::kUnits; ++u)
@@ -1636,7 +1662,7 @@ msq_status attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const m
   a.c2 = (t.scale > 0.f ? t.scale : 1.f / std::sqrt((float)D)) * kLog2e;
   a.sets = sets;
   a.words = words;
-  const bool fine = a.q_f32 && a.out_f32;
+  const bool fine = (a.q_f32 || kTree) && a.out_f32;
   hipError_t e;
   switch (D) {
     case 64: e = fine ? launch_attn<64, true, kTree>(a, p, stream) : launch_attn<64, false, kTree>(a, p, stream); break;

@@ -179,12 +179,11 @@ extern __shared__ __align__(16) unsigned char smem_codes[];
 // The slots lo .. hi - 1 that a call writes of one block and head: fill(raw) gives a
 // lane its kRows pieces of the new tokens (slots in that range only), which are
 // coded here, with the block's scale.  values: of the values, else of the keys.
-// part_max: of the workgroup, one for each wavefront.
+// part_max: of the workgroup, one for each wavefront; lane: threadIdx.x & 63.
 template <int D, int E, typename Held, typename Fill>
 __device__ __forceinline__ void write_block(const KvCacheView& c, bool values, int64_t hb, int lo, int hi,
-                                            float* part_max, Fill&& fill) {
+                                            float* part_max, int lane, Fill&& fill) {
   using Mp = Map<E>;
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int P = 1 << c.shift;
