@@ -33,7 +33,8 @@ struct AppendArgs {
   unsigned keys, values;  // workgroups of these kinds
   RotaryView r;
   RotaryRowsView q;
-  int q_rows, q_chunks;  // query rows of a workgroup; such workgroups of a sequence
+  int q_rows, q_heads;   // query rows and heads of a workgroup
+  int q_chunks, q_parts;  // such workgroups of a sequence, and of their heads
   unsigned begin;
 };
 
@@ -141,12 +142,14 @@ __global__ __launch_bounds__(1024) void k_kv_append(AppendArgs a) {
   unsigned id = a.begin + blockIdx.x;
   if (id >= a.keys + a.values) {  // queries
     id -= a.keys + a.values;
-    const int b = (int)(id / (unsigned)a.q_chunks), i0 = (int)(id - b * (unsigned)a.q_chunks) * a.q_rows;
+    const unsigned list = id / (unsigned)a.q_parts;
+    const int h0 = (int)(id - list * a.q_parts) * a.q_heads;
+    const int b = (int)(list / (unsigned)a.q_chunks), i0 = (int)(list - b * (unsigned)a.q_chunks) * a.q_rows;
     const int f = a.first[b];
     int row0, count;
     rows_of(a, b, row0, count);
     if (f < 0 || i0 >= count) return;
-    rotate_rows(a.q, a.r, row0 + i0, min(a.q_rows, count - i0), 0, a.q.heads,
+    rotate_rows(a.q, a.r, row0 + i0, min(a.q_rows, count - i0), h0, min(a.q_heads, a.q.heads - h0),
                 reinterpret_cast<float2*>(smem_codes),
                 [&](int i) { return a.positions ? a.positions[row0 + i0 + i] : f + i0 + i; });
     return;
@@ -194,11 +197,12 @@ msq_status launch_append(AppendArgs& a, int64_t lists, bool queries, hipStream_t
   int64_t query_sets = 0;
   size_t lds = std::max(fits ? table : 0, (size_t)waves * (wide || D == 64 ? Map<64>::kImage : Map<128>::kImage));
   if (queries) {
-    // four units of 16 values a thread, if there are as many
-    const int row_units = a.q.units * a.q.heads;
-    a.q_rows = std::clamp(4 * threads / row_units, 1, std::min(8, std::max(1, a.s.max_count)));
+    const RotaryShare share = rotary_share(a.q, threads, a.s.total);
+    a.q_rows = std::min(share.rows, a.s.max_count);
+    a.q_heads = share.heads;
+    a.q_parts = share.parts;
     a.q_chunks = (a.s.max_count + a.q_rows - 1) / a.q_rows;
-    query_sets = (int64_t)a.s.batch * a.q_chunks;
+    query_sets = (int64_t)a.s.batch * a.q_chunks * a.q_parts;
     lds = std::max(lds, (size_t)a.q_rows * a.r.half * sizeof(float2));
   }
   const int64_t all = lists * (a.groups + a.c.H) + query_sets;

@@ -78,128 +78,152 @@ struct RotaryRowsView {
   int x_f32, out_f32;
 };
 
-// A unit: 16 values of a head as two groups of 8, pairs 8 u .. 8 u + 7 for u < half / 8
-// (in halves, groups at 8 u and half + 8 u), else values that stay.
-struct Unit {
-  uint4 w[4];  // bf16: w[0], w[2]
-};
-__device__ inline void unit_at(const RotaryView& r, int u, int& lo, int& hi) {
-  const bool split = !r.interleaved && 8 * u < r.half;
-  lo = split ? 8 * u : 16 * u;
-  hi = split ? r.half + 8 * u : 16 * u + 8;
-}
-__device__ inline void load_unit(const RotaryRowsView& v, const RotaryView& r, int64_t row, int h, int u, Unit& t) {
-  int lo, hi;
-  unit_at(r, u, lo, hi);
-  const int64_t at = row * v.xts + (int64_t)h * v.xhs;
-  if (v.x_f32) {
-    const float* p = reinterpret_cast<const float*>(v.x) + at;
-    const uint4 *a = reinterpret_cast<const uint4*>(p + lo), *b = reinterpret_cast<const uint4*>(p + hi);
-    t.w[0] = a[0], t.w[1] = a[1], t.w[2] = b[0], t.w[3] = b[1];
-  } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(v.x) + at;
-    t.w[0] = *reinterpret_cast<const uint4*>(p + lo);
-    t.w[2] = *reinterpret_cast<const uint4*>(p + hi);
-  }
-}
-__device__ inline void eight(const uint4* w, int f32, float* x) {
-  const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-  if (f32) {
-    const uint32_t b[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(a[i]), x[4 + i] = __uint_as_float(b[i]);
-  } else {
+// A unit: two groups of 8 values of a head, half of the rotated dims apart (which are the
+// pairs of a rotation in halves), or half of the others: either way neighbouring
+// units are contiguous in memory.  (Reads and writes past the caches' order of use, where
+// these runs are whole lines: 28704 rows of 32 bf16 heads of 128, 470 MB, 81 -> 78 us, but
+// the next kernel took as much longer.)
+typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+template <typename T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
+  words4 w;
+  __device__ void load(const uint16_t* p) { w = *reinterpret_cast<const words4*>(p); }
+  __device__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(a[i] << 16);
-      x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
-}
-__device__ inline void put_eight(void* out, int f32, int64_t at, const float* x) {
-  if (f32) {
-    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at);
-    p[0] = make_float4(x[0], x[1], x[2], x[3]);
-    p[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
+  __device__ static void put(uint16_t* p, const float (&x)[8]) {
     union {
       __bf16 b[8];
-      uint4 u;
+      words4 w;
     } o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o.b[i] = (__bf16)x[i];
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + at) = o.u;
+    *reinterpret_cast<words4*>(p) = o.w;
   }
-}
-// turns: of this row, [half]
-__device__ inline void finish_unit(const RotaryRowsView& v, const RotaryView& r, int64_t row, int h, int u,
-                                   const Unit& t, const float2* turns) {
-  float a[8], b[8];
-  eight(t.w, v.x_f32, a);
-  eight(t.w + 2, v.x_f32, b);
-  if (8 * u < r.half) {
-    float2 c[8];
+};
+template <>
+struct Eight<float> {
+  words4 a, b;
+  __device__ void load(const float* p) { a = reinterpret_cast<const words4*>(p)[0], b = reinterpret_cast<const words4*>(p)[1]; }
+  __device__ void get(float (&x)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<float4*>(c)[i] = reinterpret_cast<const float4*>(turns + 8 * u)[i];
-    if (r.interleaved) {
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(a[i]), x[4 + i] = __uint_as_float(b[i]);
+  }
+  __device__ static void put(float* p, const float (&x)[8]) {
+    words4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = __float_as_uint(x[i]), b[i] = __float_as_uint(x[4 + i]);
+    reinterpret_cast<words4*>(p)[0] = a;
+    reinterpret_cast<words4*>(p)[1] = b;
+  }
+};
+
+// Where a thread's unit is: of row `row`, from dim lo on.
+struct UnitPlace {
+  bool on;
+  int row, lo, apart;
+  int64_t from, to;
+};
+
+template <typename TX, typename TO, bool kPairs, typename Turns>
+__device__ __forceinline__ void rotate_unit(const RotaryRowsView& v, const RotaryView& r, const UnitPlace& p,
+                                            const float2* turns, Turns&& make_turns) {
+  Eight<TX> ra, rb;
+  if (p.on) {
+    const TX* x = reinterpret_cast<const TX*>(v.x) + p.from;
+    ra.load(x);
+    rb.load(x + p.apart);
+  }
+  make_turns();
+  if (!p.on) return;
+  float a[8], b[8];
+  ra.get(a);
+  rb.get(b);
+  if (p.lo < r.half) {
+    const float2* t = turns + p.row * r.half;
+    float2 c[8];
+    if (kPairs) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        reinterpret_cast<float4*>(c)[i] = reinterpret_cast<const float4*>(t + p.lo / 2)[i];
+        reinterpret_cast<float4*>(c)[2 + i] = reinterpret_cast<const float4*>(t + (p.lo + r.half) / 2)[i];
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) turn(a[2 * i], a[2 * i + 1], c[i]), turn(b[2 * i], b[2 * i + 1], c[4 + i]);
     } else {
 #pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4*>(c)[i] = reinterpret_cast<const float4*>(t + p.lo)[i];
+#pragma unroll
       for (int i = 0; i < 8; ++i) turn(a[i], b[i], c[i]);
     }
   }
-  int lo, hi;
-  unit_at(r, u, lo, hi);
-  const int64_t at = row * v.ots + (int64_t)h * v.ohs;
-  put_eight(v.out, v.out_f32, at + lo, a);
-  put_eight(v.out, v.out_f32, at + hi, b);
+  TO* y = reinterpret_cast<TO*>(v.out) + p.to;
+  Eight<TO>::put(y, a);
+  Eight<TO>::put(y + p.apart, b);
 }
 
-// Rows row0 .. row0 + rows - 1 of all heads by one workgroup; position(i) that of row
-// row0 + i, turns: LDS, [rows][half].  Units are read four at a time; the first ones
-// are on their way while the turns are made.
+// Rows row0 .. row0 + rows - 1 of the heads h0 .. by one workgroup, a unit a thread (rows *
+// heads * units are at most its threads); position(i) that of row row0 + i, turns: LDS,
+// [rows][half].  The values are on their way while the turns are made, whose positions
+// and frequencies are read before them, for loads return in order.
 template <typename Position>
 __device__ inline void rotate_rows(const RotaryRowsView& v, const RotaryView& r, int64_t row0, int rows, int h0,
                                    int heads, float2* turns, Position&& position) {
-  constexpr int kAtOnce = 4;
-  const unsigned threads = blockDim.x, units = v.units, row_units = units * heads, all = row_units * rows;
-  Unit t[kAtOnce];
-  auto place = [&](unsigned n, int& i, int& h, int& u) {
-    i = (int)(n / row_units);
-    const unsigned m = n - i * row_units;
-    h = (int)(m / units);
-    u = (int)(m - h * units);
-    h += h0;
-  };
-  auto load = [&](unsigned n0) {
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const unsigned n = n0 + k * threads;
-      if (n >= all) break;
-      int i, h, u;
-      place(n, i, h, u);
-      load_unit(v, r, row0 + i, h, u, t[k]);
-    }
-  };
-  load(threadIdx.x);
-  for (unsigned n = threadIdx.x; n < (unsigned)(rows * r.half); n += threads) {
-    const int i = (int)(n / (unsigned)r.half), pair = (int)(n - i * (unsigned)r.half);
-    turns[n] = turn_of(position(i), r.freq[pair], r.amplitude);
+  const unsigned tid = threadIdx.x, units = v.units, all = (unsigned)(rows * r.half);
+  int at = 0;
+  double f = 0.0;
+  if (tid < all) {
+    const unsigned i = tid / (unsigned)r.half;
+    at = position((int)i);
+    f = r.freq[tid - i * (unsigned)r.half];
   }
-  __syncthreads();
-  for (unsigned n0 = threadIdx.x; n0 < all; n0 += kAtOnce * threads) {
-    if (n0 != threadIdx.x) load(n0);
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const unsigned n = n0 + k * threads;
-      if (n >= all) break;
-      int i, h, u;
-      place(n, i, h, u);
-      finish_unit(v, r, row0 + i, h, u, t[k], turns + (int64_t)i * r.half);
+  const unsigned slot = tid / units, row = slot / (unsigned)heads;
+  const int u = (int)(tid - slot * units), h = h0 + (int)(slot - row * heads), turned = r.half >> 3;
+  UnitPlace p;
+  p.on = row < (unsigned)rows;
+  p.row = (int)row;
+  p.lo = u < turned ? 8 * u : 2 * r.half + 8 * (u - turned);
+  p.apart = u < turned ? r.half : 8 * (int)units - r.half;
+  p.from = (row0 + row) * v.xts + h * v.xhs + p.lo;
+  p.to = (row0 + row) * v.ots + h * v.ohs + p.lo;
+  auto make_turns = [&] {
+    if (tid < all) turns[tid] = turn_of(at, f, r.amplitude);
+    for (unsigned n = tid + blockDim.x; n < all; n += blockDim.x) {
+      const unsigned i = n / (unsigned)r.half;
+      turns[n] = turn_of(position((int)i), r.freq[n - i * (unsigned)r.half], r.amplitude);
     }
-  }
+    __syncthreads();
+  };
+  auto go = [&](auto x, auto y) {
+    using X = decltype(x);
+    using Y = decltype(y);
+    r.interleaved ? rotate_unit<X, Y, true>(v, r, p, turns, make_turns)
+                  : rotate_unit<X, Y, false>(v, r, p, turns, make_turns);
+  };
+  if (v.x_f32)
+    v.out_f32 ? go(float{}, float{}) : go(float{}, uint16_t{});
+  else
+    v.out_f32 ? go(uint16_t{}, float{}) : go(uint16_t{}, uint16_t{});
+}
+
+// Rows and heads of a workgroup of `threads`, workgroups that share its rows' heads.
+struct RotaryShare {
+  int rows, heads, parts;
+};
+inline RotaryShare rotary_share(const RotaryRowsView& v, int threads, int64_t rows) {
+  RotaryShare s;
+  s.heads = v.heads < threads / v.units ? v.heads : threads / v.units;
+  s.parts = (v.heads + s.heads - 1) / s.heads;
+  const int most = threads / (v.units * s.heads);
+  s.rows = (int)(rows < most ? (rows < 1 ? 1 : rows) : most);
+  return s;
 }
 
 // Host checks of a rotation (dims 0 allowed where none) and of its rows; fills the views.

@@ -94,12 +94,10 @@ extern "C" msq_status msq_rotary_apply(const msq_rotary* rot, const msq_rotary_r
   if (!positions || !aligned_to(positions, 4)) return MSQ_ERR_INVALID_ARG;
   a.positions = positions;
   a.rows = (int)rows;
-  // Units of a workgroup: 1024, four a thread, or fewer where that leaves compute units idle.
-  const int64_t units = rows * a.v.heads * a.v.units;
-  const int64_t want = std::clamp<int64_t>(units / 512, 128, 1024);
-  a.heads = (int)std::clamp<int64_t>(want / a.v.units, 1, a.v.heads);
-  a.parts = (a.v.heads + a.heads - 1) / a.heads;
-  a.each = (int)std::clamp<int64_t>(want / ((int64_t)a.v.units * a.v.heads), 1, 16);
+  const RotaryShare share = rotary_share(a.v, 256, rows);
+  a.heads = share.heads;
+  a.parts = share.parts;
+  a.each = share.rows;
   const int64_t blocks = (rows + a.each - 1) / a.each * a.parts;
   const size_t lds = (size_t)a.each * a.r.half * sizeof(float2);
   const int64_t most = kMostThreads / 256;
