@@ -13,6 +13,8 @@ namespace {
 
 constexpr int kMostRows = MSQ_DRAFT_MAX_ROWS;
 constexpr int kNobody = 0x7FFFFFFF;
+constexpr int kFill = 1024;  // workgroups that the verifications aim at
+static_assert(kMostRows <= kFill);
 
 // The rows of the sequences of a call; those of one: row0 .. row0 + count - 1, of which
 // the first n are looked at.
@@ -77,41 +79,60 @@ struct VerifyArgs {
   int64_t ts, ds;  // row strides
   const float* uniform;
   int32_t *token, *taken, *path;
-  int parts;     // workgroups of a sequence (by chance), of a row (by the largest entries)
-  int slice;     // entries of a wavefront's share, of a workgroup's
-  int aligned;   // rows can be read four entries at a time
-  double* sums;  // [batch][4 parts]
-  uint64_t* tags;  // [batch][parts]
+  int parts;       // workgroups of a sequence (by chance), of a row (by the largest entries)
+  int slice;       // entries of a slice (by chance), of a workgroup's share
+  int slices;      // of a row
+  double* sums;    // [batch][slices]
+  uint64_t* best;  // [batch][most][parts]: an entry (high word) and its number
+  uint64_t* tags;  // [batch][parts] or [batch][most][parts]: which of this call are there
   uint64_t call;
-  float* top;    // [total * parts], and beside it the entries' numbers
-  int32_t* top_at;
 };
 
 __device__ inline float entry(const float* p) { return *p; }
 __device__ inline float entry(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 
-// Entries v .. v + 3 of a row, `none` past its end.
+// Rows begin anywhere; groups of four entries begin at -lead, 4 - lead .. so that they can be
+// read at once.
 template <typename T>
-__device__ inline void load4(const T* row, int v, int V, bool aligned, float none, float (&x)[4]) {
-  if (aligned && v + 4 <= V) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(row + v);
-      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(row + v);
-      x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
-    }
-    return;
+__device__ inline int lead_of(const T* row) {
+  return (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T) & 3);
+}
+// Entries v .. v + 3 of a row, v + lead a multiple of 4, all of them in it.
+template <typename T>
+__device__ inline void load4(const T* row, int v, float (&x)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 f = *reinterpret_cast<const float4*>(row + v);
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + v);
+    x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
   }
+}
+// Those of a wavefront's tile of 256 from v on, `none` outside the row.
+template <typename T>
+__device__ inline void load_tile(const T* row, int v, int V, bool aligned, int lane, float none, float (&x)[4]) {
+  if (aligned && v >= 0 && v + 256 <= V) {
+    load4(row, v + 4 * lane, x);
+  } else if (v >= V) {
+    x[0] = x[1] = x[2] = x[3] = none;
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = v + e < V ? entry(row + v + e) : none;
+    for (int e = 0; e < 4; ++e) {
+      const int i = v + 4 * lane + e;
+      const float t = entry(row + min(max(i, 0), V - 1));
+      x[e] = i >= 0 && i < V ? t : none;
+    }
+  }
 }
 
 // A probability: what is negative, NaN or infinite counts as 0.
-__device__ inline double mass(float x) { return x > 0.f && x < INFINITY ? (double)x : 0.0; }
+__device__ inline double mass(float x) {
+  const float p = fmaxf(x, 0.f);  // 0 of a NaN
+  return (double)(p < INFINITY ? p : 0.f);
+}
 // A random number in [0, 1].
-__device__ inline double number(float u) { return u > 0.f ? (double)fminf(u, 1.f) : 0.0; }
+__device__ inline double number(float u) { return (double)fminf(fmaxf(u, 0.f), 1.f); }
 
 __device__ inline double wave_sum(double x) {
 #pragma unroll
@@ -128,51 +149,78 @@ __device__ inline double wave_scan(double x, int lane) {
   return x;
 }
 
-// What is left of the target's distribution after row `at` once the rows in gone were not
-// taken: with draft by the sums m of what was left before each of them, else without
-// their tokens.
-struct Left {
+// How the children of a row came about: chosen; drawn, one of each row; drawn, siblings
+// one after another.
+enum Drafts { kChosen, kDrawnOne, kDrawn };
+
+// The row that the walk has reached, and the rows that it has not taken there: count of them
+// from `first` on, each with the next one, its token (kChosen) and the sum m of what was
+// left before it (kDrawn; 1 for the first).
+template <typename T>
+struct Row {
+  const T *p, *q;
+  int V, lead;
+  bool aligned;
+  int count, first;
+  const int *next, *token;
   const double* m;
-  const int* gone;
-  int count;
 };
-template <bool kDraft>
-__device__ inline double left_of(const Left& l, double p, double q) {
-  if constexpr (kDraft) {
-    for (int k = 0; k < l.count; ++k) {
-      const double m = l.m[k];
-      p = fmax((k == 0 || m <= 0.0 ? p : p / m) - q, 0.0);
+
+// What is left there of N tiles from v on (v + lead a multiple of 4), all read at once.
+template <typename T, Drafts kWay, int N>
+__device__ inline void left_at(const Row<T>& row, int v, int lane, double (&r)[N][4]) {
+  float x[N][4], y[N][4];
+#pragma unroll
+  for (int k = 0; k < N; ++k) load_tile(row.p, v + 256 * k, row.V, row.aligned, lane, 0.f, x[k]);
+  if (kWay != kChosen && row.count > 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) load_tile(row.q, v + 256 * k, row.V, row.aligned, lane, 0.f, y[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[k][e] = mass(x[k][e]);
+  if (row.count == 0) return;
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(r[k][e], y[k][e], 256 * k + e);
+  };
+  if constexpr (kWay == kChosen) {
+#pragma unroll 1
+    for (int k = 0, j = row.first; k < row.count; ++k, j = row.next[j]) {
+      const int t = __builtin_amdgcn_readfirstlane(row.token[j]) - v;
+      if (t < 0 || t >= 256 * N) continue;
+      each([&](double& p, float, int at) { p = t - 4 * lane == at ? 0.0 : p; });
+    }
+  } else {
+    each([&](double& p, float q, int) { p = fmax(p - mass(q), 0.0); });
+    if constexpr (kWay == kDrawn) {
+#pragma unroll 1
+      for (int k = 1, j = row.first; k < row.count; ++k) {
+        j = row.next[j];
+        const double m = row.m[j] > 0.0 ? row.m[j] : 1.0;
+        each([&](double& p, float q, int) { p = fmax(p / m - mass(q), 0.0); });
+      }
     }
   }
-  return p;
 }
 
-// Four entries of what is left.
-template <typename T, bool kDraft>
-__device__ inline void left4(const VerifyArgs& a, const Left& l, const T* p, const T* q, int v, double (&r)[4]) {
-  float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
-  load4(p, v, a.V, a.aligned, 0.f, x);
-  if (kDraft && l.count > 0) load4(q, v, a.V, a.aligned, 0.f, y);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) r[e] = left_of<kDraft>(l, mass(x[e]), mass(y[e]));
-  if constexpr (!kDraft) {
-    for (int k = 0; k < l.count; ++k) {
-      const int t = l.gone[k] - v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (t == e) r[e] = 0.0;
-    }
-  }
-}
-
-// Its sum over the entries lo .. hi - 1 by one wavefront.
-template <typename T, bool kDraft>
-__device__ inline double left_sum(const VerifyArgs& a, const Left& l, const T* p, const T* q, int lo, int hi, int lane) {
+// The sum of what is left in the slice from lo on, by one wavefront.  (A kernel's code is fetched
+// as it goes: with tiles unrolled wherever they are looked at, 50 KB, a call took twice as
+// long as with a tile at a time.)
+constexpr int kSlice = 1024, kMostSlices = 256;
+template <typename T, Drafts kWay>
+__device__ inline double left_sum(const Row<T>& row, int64_t lo, int size, int lane) {
   double sum = 0.0;
-  for (int v = lo + 4 * lane; v < hi; v += 256) {
-    double r[4];
-    left4<T, kDraft>(a, l, p, q, v, r);
-    sum += (r[0] + r[1]) + (r[2] + r[3]);
+  const int64_t hi = min(lo + size, (int64_t)row.V);
+#pragma unroll 1
+  for (; lo < hi; lo += kSlice) {
+    double r[4][4];
+    left_at<T, kWay>(row, (int)lo, lane, r);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum += (r[k][0] + r[k][1]) + (r[k][2] + r[k][3]);
   }
   return wave_sum(sum);
 }
@@ -183,13 +231,15 @@ __device__ inline double left_sum(const VerifyArgs& a, const Left& l, const T* p
 // up their slices of what is left at the row where the walk ends; the workgroup that
 // comes last (tags as in the cache attention's join) finds the slice in which the
 // running sum passes the number, and the entry in it.
-template <typename T, bool kDraft>
+template <typename T, Drafts kWay>
 __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
   constexpr int kWaves = 4;
-  __shared__ int parent[kMostRows], token[kMostRows], path[kMostRows], gone[kMostRows];
+  constexpr bool kDraft = kWay != kChosen;
+  __shared__ int parent[kMostRows], token[kMostRows], path[kMostRows], next[kMostRows];
   __shared__ float prob[kMostRows], drawn[kDraft ? kMostRows : 1], number_of[kMostRows];
-  __shared__ double m_of[kDraft ? kMostRows : 1], shared_sum[kWaves];
-  __shared__ int complete;
+  __shared__ double m_of[kWay == kDrawn ? kMostRows : 1], shared_sum[kWaves];
+  __shared__ double fresh[kMostSlices];  // sums of slices made by the workgroup that joins
+  __shared__ int complete, last_of[kWaves], found;
   const int part = blockIdx.x % (unsigned)a.parts, b = blockIdx.x / (unsigned)a.parts;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int row0, count, n;
@@ -204,18 +254,31 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
     const int p = parent_of(a.parents, row0, i), t = a.tokens[row0 + i];
     const bool some = p >= 0 && t >= 0 && t < a.V;
     parent[i] = p;
-    token[i] = t;
+    token[i] = some ? t : -1;
     number_of[i] = a.uniform[row0 + i];
     prob[i] = some ? entry(target + (row0 + p) * a.ts + t) : 0.f;
     if constexpr (kDraft) drawn[i] = some ? entry(draft + (row0 + p) * a.ds + t) : 0.f;
   }
+  if (threadIdx.x == 0) path[0] = 0;
   __syncthreads();
 
+  Row<T> row;
+  row.V = a.V;
+  row.count = 0;
+  row.first = 0;
+  row.next = next;
+  row.token = token;
+  row.m = m_of;
+  auto reach = [&](int i) {
+    row.p = target + (row0 + i) * a.ts;
+    row.q = kDraft ? draft + (row0 + i) * a.ds : row.p;
+    row.lead = lead_of(row.p);
+    row.aligned = lead_of(row.q) == row.lead;
+  };
+  reach(0);
   // the walk, the same in all wavefronts
-  int at = 0, taken = 1;
-  double m = 1.0;
-  Left l{m_of, gone, 0};
-  if (threadIdx.x == 0) path[0] = 0;
+  int at = 0, taken = 1, last = 0;
+  double m = 1.0;  // the sum of what is left; of drawn siblings -1 until it is needed
   for (int c = 0; c < n; c += 64) {
     const int mine = c + lane < n ? parent[c + lane] : -1;
     uint64_t open = ~0ull;  // rows of these 64 that are still to come
@@ -226,262 +289,277 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
       open = j - c == 63 ? 0 : ~0ull << (j - c + 1);
       const int x = __builtin_amdgcn_readfirstlane(token[j]);
       double r = mass(prob[j]), q = 1.0;
-      if constexpr (kDraft) {
-        q = mass(drawn[j]);
-        if (l.count > 0) {  // m is that of what is left now
-          const T* pr = target + (row0 + at) * a.ts;
-          const T* qr = draft + (row0 + at) * a.ds;
+      if constexpr (kDraft) q = mass(drawn[j]);
+      if constexpr (kWay == kChosen) {
+        for (int k = 0, i = row.first; k < row.count; ++k, i = next[i])
+          if (token[i] == x) r = 0.0;
+      }
+      if constexpr (kWay == kDrawn) {
+        if (row.count > 0) {
           if (m < 0.0) {
-            // the sum that the last row not taken leaves: by slices of the wavefronts
-            const int each = ((a.V + kWaves - 1) / kWaves + 255) / 256 * 256;
-            const double s = left_sum<T, true>(a, l, pr, qr, min(wave * each, a.V), min((wave + 1) * each, a.V), lane);
+            double s = 0.0;
+            for (int i = wave; i < a.slices; i += kWaves)
+              s += left_sum<T, kWay>(row, (int64_t)i * a.slice - row.lead, a.slice, lane);
             __syncthreads();
             if (lane == 0) shared_sum[wave] = s;
             __syncthreads();
             m = (shared_sum[0] + shared_sum[1]) + (shared_sum[2] + shared_sum[3]);
           }
-          r = left_of<true>(l, r, q);
+          for (int k = 0, i = row.first; k < row.count; ++k, i = next[i])
+            r = fmax((k > 0 && m_of[i] > 0.0 ? r / m_of[i] : r) - q, 0.0);
         }
-      } else {
-        for (int k = 0; k < l.count; ++k)
-          if (gone[k] == x) r = 0.0;
       }
-      const bool take = x >= 0 && x < a.V && number(number_of[j]) * q * m < r;
-      if (take) {
+      if (x >= 0 && number(number_of[j]) * q * m < r) {
         if (threadIdx.x == 0) path[taken] = j;
         ++taken;
         at = j;
         m = 1.0;
-        l.count = 0;
+        row.count = 0;
+        reach(j);
       } else {
-        if constexpr (kDraft) {
-          __syncthreads();  // every wavefront has read what was there
-          if (threadIdx.x == 0) m_of[l.count] = m;
-          __syncthreads();
-          m = -1.0;  // not known yet
-        } else {
-          __syncthreads();
-          if (threadIdx.x == 0) gone[l.count] = x;
-          __syncthreads();
-          m -= r;
-        }
-        ++l.count;
+        // (every wavefront writes these, the same, and none reads them before it has)
+        if (row.count == 0)
+          row.first = j;
+        else
+          next[last] = j;
+        if constexpr (kWay == kDrawn) m_of[j] = m;
+        last = j;
+        __builtin_amdgcn_wave_barrier();
+        m = kDraft ? -1.0 : m - r;
+        ++row.count;
       }
     }
   }
 
-  const T* pr = target + (row0 + at) * a.ts;
-  const T* qr = kDraft ? draft + (row0 + at) * a.ds : pr;
-  const int slices = kWaves * a.parts;
-  double* sums = a.sums + (int64_t)b * slices;
-  auto slice_sum = [&](int s) {
-    const int lo = (int)min((int64_t)s * a.slice, (int64_t)a.V);
-    return left_sum<T, kDraft>(a, l, pr, qr, lo, (int)min((int64_t)lo + a.slice, (int64_t)a.V), lane);
-  };
-  {
-    const int s = part * kWaves + wave;
-    const double sum = slice_sum(s);
-    if (lane == 0)
-      __hip_atomic_store(sums + s, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  // device-scope stores have reached the level that all XCDs share once vmcnt is 0
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (a.parts > 1) {
-    if (wave == 0) {
-      uint64_t* tags = a.tags + (int64_t)b * a.parts;
-      if (lane == 0) __hip_atomic_store(tags + part, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      const bool there = lane >= a.parts ||
-                         __hip_atomic_load(tags + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.call;
-      const bool all = __all(there);
-      if (all && lane < a.parts) __hip_atomic_store(tags + lane, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (lane == 0) complete = all;
-    }
-    __syncthreads();
-    if (!complete) return;
-  }
-
-  // slice s of the running sum that passes x, and what comes before it; if rounding
-  // leaves none, the last one that has any
+  double* sums = a.sums + (int64_t)b * a.slices;
+  const int each = (a.slices + a.parts - 1) / a.parts;
+  int begin = part * each, end = min(begin + each, a.slices);
   const double u = number(number_of[0]);
-  double x = 0.0, before = 0.0;
+  double x = 0.0, start = 0.0;
   int s = -1;
-  for (int attempt = 0; attempt < 2; ++attempt) {
-    double four[4], mine = 0.0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 4 * lane + e;
-      four[e] = i < slices ? __hip_atomic_load(sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0;
-      mine += four[e];
-    }
-    const double upto = wave_scan(mine, lane);
-    const double all = __shfl(upto, 63);
-    if (all > 0.0) {
-      x = u * all;
-      const uint64_t past = __ballot(upto > x), some = __ballot(mine > 0.0);
-      const int from = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
-      // in that lane's four
-      double run = upto - mine, start = run;
-      int e_hit = -1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool hit = past ? run + four[e] > x && e_hit < 0 : four[e] > 0.0;
-        if (hit) e_hit = e, start = run;
-        run += four[e];
+  for (bool joined = false;; joined = true) {
+    for (int i = begin + wave; i < end; i += kWaves) {
+      const double sum = left_sum<T, kWay>(row, (int64_t)i * a.slice - row.lead, a.slice, lane);
+      if (lane == 0) {
+        // (two workgroups may both see that all have come: what one makes after that is its own)
+        if (joined)
+          fresh[i] = sum;
+        else
+          __hip_atomic_store(sums + i, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
-      if (e_hit < 0) {  // passed by the lanes' sums, not by these: the last one that has any
-        double r = upto - mine;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (four[e] > 0.0) e_hit = e, start = r;
-          r += four[e];
-        }
-      }
-      s = 4 * from + __shfl(e_hit, from);
-      before = __shfl(start, from);
-      break;
     }
-    // nothing left: the distribution as it was
-    if (attempt == 1 || l.count == 0) break;
-    l.count = 0;
-    __syncthreads();
-    for (int i = wave; i < slices; i += kWaves) {
-      const double sum = slice_sum(i);
-      if (lane == 0) __hip_atomic_store(sums + i, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    auto sum_of = [&](int i) {
+      return joined ? fresh[i] : __hip_atomic_load(sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    };
+    // device-scope stores have reached the level that all XCDs share once vmcnt is 0
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-  }
-  int found = -1;
-  if (s >= 0) {
-    // its quarter, then the entry
-    const int lo = (int)min((int64_t)s * a.slice, (int64_t)a.V), hi = (int)min((int64_t)lo + a.slice, (int64_t)a.V);
-    const int each = (a.slice / kWaves + 255) / 256 * 256;
-    const double mine = left_sum<T, kDraft>(a, l, pr, qr, min(lo + wave * each, hi), min(lo + (wave + 1) * each, hi), lane);
-    __syncthreads();
-    if (lane == 0) shared_sum[wave] = mine;
-    __syncthreads();
-    int quarter = -1, last = 0;
-    double run = before, start = before, last_start = before;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const double t = shared_sum[w];
-      if (quarter < 0 && run + t > x) quarter = w, start = run;
-      if (t > 0.0) last = w, last_start = run;
-      run += t;
-    }
-    if (quarter < 0) quarter = last, start = last_start;
-    if (wave == 0) {
-      const int end = min(lo + (quarter + 1) * each, hi);
-      int spare = -1;  // the last entry with any mass
-      for (int v0 = lo + quarter * each; v0 < end; v0 += 256) {
-        const int v = v0 + 4 * lane;
-        double r[4] = {0.0, 0.0, 0.0, 0.0};
-        if (v < end) left4<T, kDraft>(a, l, pr, qr, v, r);
-        const double here = (r[0] + r[1]) + (r[2] + r[3]);
-        const double upto = wave_scan(here, lane);
-        const uint64_t past = __ballot(start + upto > x && here > 0.0), some = __ballot(here > 0.0);
-        if (past) {
-          const int from = __builtin_ctzll(past);
-          double t = start + (upto - here);
-          int hit = -1, any = -1;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            t += r[e];
-            if (r[e] > 0.0) any = v + e;
-            if (hit < 0 && r[e] > 0.0 && t > x) hit = v + e;
-          }
-          found = __shfl(hit >= 0 ? hit : any, from);
-          break;
-        }
-        if (some) {
-          int any = -1;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r[e] > 0.0) any = v + e;
-          spare = __shfl(any, 63 - __builtin_clzll(some));
-        }
-        start += __shfl(upto, 63);
+    if (!joined && a.parts > 1) {
+      if (wave == 0) {
+        uint64_t* tags = a.tags + (int64_t)b * a.parts;
+        if (lane == 0) __hip_atomic_store(tags + part, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const bool there = lane >= a.parts ||
+                           __hip_atomic_load(tags + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.call;
+        const bool all = __all(there);
+        if (all && lane < a.parts)
+          __hip_atomic_store(tags + lane, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) complete = all;
       }
-      if (found < 0) found = spare;
+      __syncthreads();
+      if (!complete) return;
     }
+    // the slice in which the running sum passes x, and the sum before it; where rounding leaves
+    // none, the last one that has any
+    double four[4], mine = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) four[e] = 4 * lane + e < a.slices ? sum_of(4 * lane + e) : 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine += four[e];
+    const double upto = wave_scan(mine, lane), all = __shfl(upto, 63);
+    if (all > 0.0) {
+      x = u * all;
+      const uint64_t past = __ballot(upto > x && mine > 0.0), some = __ballot(mine > 0.0);
+      const int from = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+      double run = upto - mine, run_at = run;
+      int hit = -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (four[e] > 0.0 && !(hit >= 0 && run > x)) hit = 4 * lane + e, run_at = run;
+        run += four[e];
+      }
+      s = __shfl(hit, from);
+      start = __shfl(run_at, from);
+      break;
+    }
+    if (joined || row.count == 0) break;
+    row.count = 0;  // nothing is left: the distribution as it was
+    begin = 0, end = a.slices;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) found = -1;
+  if (s >= 0) {
+    // a quarter of 1024 entries for each wavefront
+    const int64_t lo = (int64_t)s * a.slice - row.lead, hi = min(lo + a.slice, (int64_t)a.V);
+    int spare = -1;  // the last entry with any mass
+    for (int64_t c = lo; c < hi; c += kSlice) {
+      const int v = (int)c + 256 * wave + 4 * lane;
+      double tile[1][4];
+      left_at<T, kWay>(row, (int)c + 256 * wave, lane, tile);
+      const double(&r)[4] = tile[0];
+      const double here = (r[0] + r[1]) + (r[2] + r[3]);
+      const double upto = wave_scan(here, lane), sum = __shfl(upto, 63);
+      int any = -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r[e] > 0.0) any = v + e;
+      const uint64_t some = __ballot(any >= 0);
+      __syncthreads();
+      if (lane == 0) shared_sum[wave] = sum;
+      const int wave_last = some ? __shfl(any, 63 - __builtin_clzll(some)) : -1;
+      if (lane == 0) last_of[wave] = wave_last;
+      __syncthreads();
+      int quarter = -1;
+      double before = start;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const double t = shared_sum[w];
+        if (last_of[w] >= 0) spare = last_of[w];
+        if (quarter < 0 && t > 0.0 && start + t > x) quarter = w, before = start;
+        start += t;
+      }
+      if (quarter < 0) continue;
+      if (wave == quarter) {
+        const uint64_t past = __ballot(any >= 0 && before + upto > x);
+        const int from = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+        double t = before + (upto - here);
+        int hit = any;
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          double run = t;
+#pragma unroll
+          for (int i = 0; i <= e; ++i) run += r[i];
+          if (r[e] > 0.0 && run > x) hit = v + e;
+        }
+        hit = __shfl(hit, from);
+        if (lane == 0) found = hit;
+      }
+      spare = -1;
+      break;
+    }
+    __syncthreads();
+    if (spare >= 0 && threadIdx.x == 0) found = spare;
   }
   if (threadIdx.x == 0) a.token[b] = found, a.taken[b] = taken;
   for (int i = threadIdx.x; i < count; i += 256) a.path[row0 + i] = i < taken ? row0 + path[i] : -1;
 }
 
+constexpr int kRowPart = 4096;  // least entries of a row's part: each thread reads 16 at once
+
 // Entry x at v before y at w: larger, or as large and first.
 __device__ inline bool before(float x, int v, float y, int w) { return x > y || (x == y && v < w); }
 
-// The largest entry of a workgroup's slice of a row, the first of equal ones.
+// By the largest entries.  A workgroup finds the largest of its slice of a row, the first
+// of equal ones; the one that comes last of a sequence (tags again) walks through its tree.
 template <typename T>
-__global__ __launch_bounds__(256) void k_row_largest(VerifyArgs a) {
-  __shared__ float best_of[4];
-  __shared__ int at_of[4];
-  const int part = blockIdx.x % (unsigned)a.parts, row = blockIdx.x / (unsigned)a.parts;
-  const T* p = reinterpret_cast<const T*>(a.target) + row * a.ts;
-  const int lo = (int)min((int64_t)part * a.slice, (int64_t)a.V), hi = (int)min((int64_t)lo + a.slice, (int64_t)a.V);
+__global__ __launch_bounds__(256) void k_verify_largest(VerifyArgs a) {
+  __shared__ int parent[kMostRows], token[kMostRows], top[kMostRows], path[kMostRows];
+  __shared__ uint64_t best_of[4], part_best[kFill];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = blockIdx.x / (unsigned)a.parts, b = item / (unsigned)a.r.most;
+  const int part = (int)(blockIdx.x - item * a.parts), mine = (int)(item - b * a.r.most);
+  int row0, count, n;
+  rows_of(a.r, b, row0, count, n);
+  if (mine >= n) {
+    if (mine == 0 && part == 0 && threadIdx.x == 0) a.token[b] = -1, a.taken[b] = 0;
+    return;
+  }
+  const T* p = reinterpret_cast<const T*>(a.target) + (row0 + mine) * a.ts;
+  const int64_t first = (int64_t)part * a.slice - lead_of(p);
+  const int lo = (int)min(first, (int64_t)a.V), hi = (int)min(first + a.slice, (int64_t)a.V);
   float best = -INFINITY;
   int at = kNobody;
-  for (int v = lo + 4 * threadIdx.x; v < hi; v += 1024) {
-    float x[4];
-    load4(p, v, a.V, a.aligned, NAN, x);
+  auto meet = [&](const float (&x)[4], int v) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (before(x[e], v + e, best, at)) best = x[e], at = v + e;
-  }
+  };
+#pragma unroll 1
+  for (int v0 = lo + 256 * wave; v0 < hi; v0 += kRowPart) {
+    float x[4][4];
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const float x = __shfl_xor(best, m);
-    const int v = __shfl_xor(at, m);
+    for (int k = 0; k < 4; ++k) load_tile(p, v0 + 1024 * k, a.V, true, lane, NAN, x[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) meet(x[k], v0 + 1024 * k + 4 * lane);
+  }
+  auto join = [&](float x, int v) {
     if (before(x, v, best, at)) best = x, at = v;
-  }
-  if ((threadIdx.x & 63) == 0) best_of[threadIdx.x >> 6] = best, at_of[threadIdx.x >> 6] = at;
+  };
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) join(__shfl_xor(best, m), __shfl_xor(at, m));
+  if (lane == 0) best_of[wave] = (uint64_t)__float_as_uint(best) << 32 | (uint32_t)at;
   __syncthreads();
+  const int64_t seq = (int64_t)b * a.r.most * a.parts;
+  uint64_t *bests = a.best + seq, *tags = a.tags + seq;
+  const int place = mine * a.parts + part, all = n * a.parts;
   if (threadIdx.x == 0) {
-    for (int w = 1; w < 4; ++w)
-      if (before(best_of[w], at_of[w], best, at)) best = best_of[w], at = at_of[w];
-    a.top[blockIdx.x] = best;
-    a.top_at[blockIdx.x] = at;
-  }
-}
-
-// By the largest entries: the walk of a sequence.
-__global__ __launch_bounds__(256) void k_verify_largest(VerifyArgs a) {
-  __shared__ int parent[kMostRows], token[kMostRows], best[kMostRows], path[kMostRows];
-  const int b = blockIdx.x, lane = threadIdx.x & 63;
-  int row0, count, n;
-  rows_of(a.r, b, row0, count, n);
-  for (int i = threadIdx.x; i < n; i += 256) {
-    parent[i] = parent_of(a.parents, row0, i);
-    token[i] = a.tokens[row0 + i];
-    const int64_t t = (int64_t)(row0 + i) * a.parts;
-    float x = a.top[t];
-    int at = a.top_at[t];
-    for (int k = 1; k < a.parts; ++k)
-      if (before(a.top[t + k], a.top_at[t + k], x, at)) x = a.top[t + k], at = a.top_at[t + k];
-    best[i] = at;
+    for (int w = 1; w < 4; ++w) join(__uint_as_float((uint32_t)(best_of[w] >> 32)), (int)(uint32_t)best_of[w]);
+    __hip_atomic_store(bests + place, (uint64_t)__float_as_uint(best) << 32 | (uint32_t)at, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    // it has reached the level that all XCDs share once vmcnt is 0; then the tag, then the look
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __hip_atomic_store(tags + place, a.call, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
   __syncthreads();
-  int at = 0, taken = n > 0 ? 1 : 0;
+  bool there = true;  // four at once: all <= kFill, or one part of each of at most kMostRows rows
+#pragma unroll
+  for (int k = 0; k < kFill / 256; ++k) {
+    const int i = 256 * k + threadIdx.x;
+    there &= i >= all || __hip_atomic_load(tags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.call;
+  }
+  if (!__syncthreads_and(there)) return;
+#pragma unroll
+  for (int k = 0; k < kFill / 256; ++k) {
+    const int i = 256 * k + threadIdx.x;
+    if (i < all) {
+      part_best[i] = __hip_atomic_load(bests + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(tags + i, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (i < n) {
+      parent[i] = parent_of(a.parents, row0, i);
+      token[i] = a.tokens[row0 + i];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += 256) {
+    best = -INFINITY;
+    at = kNobody;
+    for (int k = 0; k < a.parts; ++k) {
+      const uint64_t w = part_best[i * a.parts + k];
+      join(__uint_as_float((uint32_t)(w >> 32)), (int)(uint32_t)w);
+    }
+    top[i] = at;
+  }
+  __syncthreads();
+  int node = 0, taken = 1;
   if (threadIdx.x == 0) path[0] = 0;
   for (int c = 0; c < n; c += 64) {
-    const int i = c + lane, mine = i < n ? parent[i] : -1, x = i < n ? token[i] : -1;
+    const int i = c + lane, above = i < n ? parent[i] : -1, x = i < n ? token[i] : -1;
     uint64_t open = ~0ull;
     for (;;) {
-      const uint64_t fits = __ballot(i > 0 && mine == at && x == best[at]) & open;
+      const uint64_t fits = __ballot(i > 0 && above == node && x == top[node]) & open;
       if (!fits) break;
       const int j = c + __builtin_ctzll(fits);
       open = j - c == 63 ? 0 : ~0ull << (j - c + 1);
       if (threadIdx.x == 0) path[taken] = j;
       ++taken;
-      at = j;
+      node = j;
     }
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    a.token[b] = n > 0 && best[at] != kNobody ? best[at] : -1;
+    a.token[b] = top[node] != kNobody ? top[node] : -1;
     a.taken[b] = taken;
   }
   for (int i = threadIdx.x; i < count; i += 256) a.path[row0 + i] = i < taken ? row0 + path[i] : -1;
@@ -503,33 +581,37 @@ msq_status rows_view(const int32_t* offset, int32_t batch, int64_t total, int32_
   return MSQ_OK;
 }
 
-// Workgroups that the calls aim at (by chance, by the largest entries), and the most
-// parts of a sequence: its tags are looked at by one wavefront, its slices by four a lane.
-constexpr int kChanceFill = 512, kLargestFill = 1024, kMostParts = 64;
+constexpr int kMostParts = 64;  // of a sequence or row: one wavefront looks at a sequence's tags
 
 struct VerifyPlan {
-  int parts, slice;
+  int parts, slice, slices;
   int64_t blocks;
-  size_t workspace, at;  // at: of the tags, or of the entries' numbers
+  size_t workspace, at;  // at: of the tags
 };
-msq_status plan_verify(const msq_draft& d, VerifyArgs& a, VerifyPlan& p) {
+msq_status plan_verify(const msq_draft& d, Rows& r, VerifyPlan& p) {
   p = VerifyPlan{};
-  const msq_status st = rows_view(d.offset, d.batch, d.total, d.max_count, a.r);
+  const msq_status st = rows_view(d.offset, d.batch, d.total, d.max_count, r);
   if (st != MSQ_OK) return st;
-  if (d.vocab < 1) return MSQ_ERR_SHAPE;
+  if (d.vocab < 1 || d.vocab > 1 << 30) return MSQ_ERR_SHAPE;
   if (d.batch == 0) return MSQ_OK;
-  const int64_t items = d.uniform ? d.batch : d.total, fill = d.uniform ? kChanceFill : kLargestFill;
-  const int64_t most = std::max(items, fill);  // parts of all items, at any size up to this one
-  p.workspace = d.uniform ? (size_t)most * 40 : (size_t)most * 8;
-  p.at = d.uniform ? (size_t)most * 32 : (size_t)most * 4;
-  // parts of at least 1024 entries (a wavefront's slice: a multiple of 256)
-  const int64_t parts = std::clamp<int64_t>(std::min(fill / std::max<int64_t>(items, 1), ((int64_t)d.vocab + 1023) / 1024), 1, kMostParts);
-  const int64_t shares = d.uniform ? 4 * parts : parts, unit = d.uniform ? 256 : 1024;
-  const int64_t slice = ((d.vocab + shares - 1) / shares + unit - 1) / unit * unit;
-  p.parts = (int)parts;
-  p.slice = (int)std::min<int64_t>(slice, 0x7FFFFF00);
-  p.blocks = items * parts;
-  if (p.blocks > kMostThreads / 256 || d.batch > kMostThreads / 256) return MSQ_ERR_SHAPE;
+  r.most = std::max(r.most, 1);
+  const int64_t items = d.uniform ? d.batch : (int64_t)d.batch * r.most;
+  // all parts of calls of any size up to this one are at most `most` (a row may begin three
+  // entries before its first group of four)
+  const int64_t unit = d.uniform ? kSlice : kRowPart;
+  const int64_t most = std::max<int64_t>(items, kFill), groups = ((int64_t)d.vocab + 3 + unit - 1) / unit;
+  p.parts = (int)std::clamp<int64_t>(std::min(kFill / items, groups), 1, kMostParts);
+  if (d.uniform) {
+    p.slice = (int)((groups + kMostSlices - 1) / kMostSlices * kSlice);
+    p.slices = (int)(((int64_t)d.vocab + 3 + p.slice - 1) / p.slice);
+    p.at = (size_t)d.batch * std::min<int64_t>(groups, kMostSlices) * 8;
+  } else {
+    p.slice = (int)((groups + p.parts - 1) / p.parts * unit);
+    p.at = (size_t)most * 8;
+  }
+  p.workspace = p.at + (size_t)most * 8;
+  p.blocks = items * p.parts;
+  if (p.blocks > kMostThreads / 256) return MSQ_ERR_SHAPE;
   return MSQ_OK;
 }
 
@@ -560,9 +642,9 @@ extern "C" msq_status msq_draft_tree(const int32_t* parents, const int32_t* offs
 }
 
 extern "C" size_t msq_verify_draft_workspace_bytes(const msq_draft* d) {
-  VerifyArgs a{};
+  Rows r;
   VerifyPlan p;
-  return d && plan_verify(*d, a, p) == MSQ_OK ? p.workspace : 0;
+  return d && plan_verify(*d, r, p) == MSQ_OK ? p.workspace : 0;
 }
 
 extern "C" msq_status msq_verify_draft(const msq_draft* d, void* workspace, size_t workspace_bytes,
@@ -570,7 +652,7 @@ extern "C" msq_status msq_verify_draft(const msq_draft* d, void* workspace, size
   if (!d) return MSQ_ERR_INVALID_ARG;
   VerifyArgs a{};
   VerifyPlan p;
-  const msq_status st = plan_verify(*d, a, p);
+  const msq_status st = plan_verify(*d, a.r, p);
   if (st != MSQ_OK) return st;
   if (d->dtype != MSQ_DTYPE_BF16 && d->dtype != MSQ_DTYPE_F32) return MSQ_ERR_INVALID_ARG;
   if (d->batch == 0) return MSQ_OK;
@@ -593,28 +675,27 @@ extern "C" msq_status msq_verify_draft(const msq_draft* d, void* workspace, size
   a.token = d->token, a.taken = d->taken, a.path = d->path;
   a.parts = p.parts;
   a.slice = p.slice;
-  a.aligned = d->target_stride % 4 == 0 && aligned_to(d->target, 4 * size) &&
-              (!drawn || (d->draft_stride % 4 == 0 && aligned_to(d->draft, 4 * size)));
+  a.slices = p.slices;
   const dim3 threads(256);
   if (chance) {
     a.sums = reinterpret_cast<double*>(ws);
     a.tags = reinterpret_cast<uint64_t*>(ws + p.at);
     a.call = next_call();
     const dim3 grid((unsigned)p.blocks);
-    if (f32 && drawn) hipLaunchKernelGGL((k_verify_chance<float, true>), grid, threads, 0, stream, a);
-    else if (f32) hipLaunchKernelGGL((k_verify_chance<float, false>), grid, threads, 0, stream, a);
-    else if (drawn) hipLaunchKernelGGL((k_verify_chance<uint16_t, true>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((k_verify_chance<uint16_t, false>), grid, threads, 0, stream, a);
+    auto go = [&](auto t) {
+      using T = decltype(t);
+      if (!drawn) hipLaunchKernelGGL((k_verify_chance<T, kChosen>), grid, threads, 0, stream, a);
+      else if (!d->parents) hipLaunchKernelGGL((k_verify_chance<T, kDrawnOne>), grid, threads, 0, stream, a);
+      else hipLaunchKernelGGL((k_verify_chance<T, kDrawn>), grid, threads, 0, stream, a);
+    };
+    f32 ? go(float{}) : go(uint16_t{});
     return hipGetLastError() == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
   }
-  a.top = reinterpret_cast<float*>(ws);
-  a.top_at = reinterpret_cast<int32_t*>(ws + p.at);
-  if (p.blocks > 0) {
-    const dim3 grid((unsigned)p.blocks);
-    if (f32) hipLaunchKernelGGL((k_row_largest<float>), grid, threads, 0, stream, a);
-    else hipLaunchKernelGGL((k_row_largest<uint16_t>), grid, threads, 0, stream, a);
-    if (hipGetLastError() != hipSuccess) return MSQ_ERR_HIP;
-  }
-  hipLaunchKernelGGL(k_verify_largest, dim3((unsigned)d->batch), threads, 0, stream, a);
+  a.best = reinterpret_cast<uint64_t*>(ws);
+  a.tags = reinterpret_cast<uint64_t*>(ws + p.at);
+  a.call = next_call();
+  const dim3 grid((unsigned)p.blocks);
+  if (f32) hipLaunchKernelGGL((k_verify_largest<float>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((k_verify_largest<uint16_t>), grid, threads, 0, stream, a);
   return hipGetLastError() == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
 }

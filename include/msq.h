@@ -632,7 +632,7 @@ typedef struct {
   int64_t total;          /* rows of all sequences, 0 .. 2^31 - 1 */
   int32_t max_count;      /* at least the largest sequence's rows; 0: total / batch with a null
                              offset, else total.  Rows past it or MSQ_DRAFT_MAX_ROWS count as not there */
-  int32_t vocab;          /* entries of a distribution, >= 1 */
+  int32_t vocab;          /* entries of a distribution, 1 .. 2^30 */
   const int32_t *tokens;  /* [total]: the drafted tokens (those of rows 0 are not looked at) */
   const int32_t *parents; /* [total] or null: a chain, the row before */
   const void *target;     /* [total][vocab] of dtype, the large model's entries after each row */
@@ -667,9 +667,9 @@ typedef struct {
  * or NaN as the nearer end or 0; a token outside 0 .. vocab - 1 is not taken.  All
  * arithmetic is fp64.  Rows outside every sequence: path is left as it is.
  * workspace: msq_verify_draft_workspace_bytes, 256-byte aligned, holding anything; calls that
- * share one must be ordered on one stream.  One launch, or by the largest entries two.
- * Asynchronous, and the same results every time.  Errors: MSQ_ERR_INVALID_ARG,
- * MSQ_ERR_SHAPE, MSQ_ERR_BUFFER_TOO_SMALL, MSQ_ERR_HIP. */
+ * share one must be ordered on one stream.  One launch, asynchronous, and the same results
+ * every time.  Errors: MSQ_ERR_INVALID_ARG, MSQ_ERR_SHAPE, MSQ_ERR_BUFFER_TOO_SMALL,
+ * MSQ_ERR_HIP. */
 msq_status msq_verify_draft(const msq_draft *d, void *workspace, size_t workspace_bytes, hipStream_t stream);
 /* Bytes that it needs at most for calls of these sizes (batch, total, max_count, vocab, whether
  * offset, parents, draft and uniform are null) or a smaller vocab or total; 0 for sizes that it refuses. */
