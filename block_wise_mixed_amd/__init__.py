@@ -941,27 +941,42 @@ class Rotary:
     amplitude: float = 1.0
 
     def __post_init__(self):
-        f = self.frequencies
-        if f.dtype is not _torch().float64 or f.dim() != 1 or f.numel() < 8 or f.numel() % 8 or \
-                not f.is_contiguous():
-            raise ValueError("frequencies must be contiguous float64 [dims / 2], dims a multiple of 16")
-        if not np.isfinite(self.amplitude) or self.amplitude == 0:
-            raise ValueError("amplitude must be finite and not 0")
+        self.fields()
 
-    def fields(self, index: int):
-        """Its fields in the C structs, for a call on device `index`."""
-        f = self.frequencies
-        if f.get_device() != index:
-            raise ValueError("frequencies must be on the call's device")
-        return f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0, self.amplitude
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_fields", None)
+
+    def fields(self):
+        """(device, its fields in the C structs, the struct); made anew after a field was set."""
+        if self._fields is None:
+            f = self.frequencies
+            if f.dtype is not _torch().float64 or f.dim() != 1 or f.numel() < 8 or f.numel() % 8 or \
+                    not f.is_contiguous():
+                raise ValueError("frequencies must be contiguous float64 [dims / 2], dims a multiple of 16")
+            if not np.isfinite(self.amplitude) or self.amplitude == 0:
+                raise ValueError("amplitude must be finite and not 0")
+            fields = f.data_ptr(), 2 * f.numel(), 1 if self.interleaved else 0, float(self.amplitude)
+            r = _Rotary()
+            _pack(_ROTARY, r, "frequencies", *fields)
+            object.__setattr__(self, "_fields", (f.get_device(), fields, r))
+        return self._fields
 
 
-def _rotary_out(x, out, out_dtype, name, index):
-    """The tensor that takes x rotated, and its fields."""
+def _rotary_out(x, contiguous, out, out_dtype, name, index):
+    """The tensor that takes x [rows][heads][dim] rotated, with its address, strides and type;
+    contiguous: x is."""
     torch = _torch()
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    elif out.shape != x.shape or out.get_device() != index or (out_dtype is not None and out.dtype != out_dtype):
+        dtype = out_dtype or x.dtype
+        code = _KV_DTYPE.get(dtype)
+        if code is None:
+            code = _kv_dtype(dtype)
+        out = torch.empty_like(x, dtype=dtype) if contiguous else \
+            torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+        dim = x.shape[2]
+        return out, out.data_ptr(), x.shape[1] * dim, dim, code
+    if out.shape != x.shape or out.get_device() != index or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError(f"{name} must have the shape of what is rotated, on its device")
     code = _kv_dtype(out.dtype)
     st, sh, sd = out.stride()
@@ -985,18 +1000,26 @@ def rotary(x, positions, rot: Rotary, out=None, out_dtype=None, stream=None):
     rows, heads, dim = x.shape
     given = x
     x, _, at, st, sh, code = _kv_rows(x, "x", heads, dim, index)
-    if out is given and x is not given:
+    if x is not given and out is given:
         raise ValueError("in place: dims contiguous, strides and address multiples of 16 bytes")
     positions = _kv_index(positions, "positions", rows, index)
-    out, o_at, o_st, o_sh, o_code = _rotary_out(x, out, out_dtype, "out", index)
-    r, v = _Rotary(), _RotaryRows()
-    _ROTARY.pack_into(r, 0, *rot.fields(index))
-    _pack(_ROTARY_ROWS, v, "x", at, st, sh, o_at, o_st, o_sh, code, o_code, heads, dim)
+    device, _, r = rot._fields or rot.fields()
+    if device != index:
+        raise ValueError("the frequencies must be on x's device")
+    out, o_at, o_st, o_sh, o_code = _rotary_out(x, sh == dim and st == heads * dim, out, out_dtype, "out", index)
+    v = _RotaryRows()
+    try:
+        _ROTARY_ROWS.pack_into(v, 0, at, st, sh, o_at, o_st, o_sh, code, o_code, heads, dim)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"x: {e}") from None
     status = load_library().msq_rotary_apply(r, v, positions.data_ptr(), rows,
                                              cuda._cuda_getCurrentRawStream(index))
     if status:
         raise MsqError(status, "msq_rotary_apply")
     return out
+
+
+_NO_QUERIES = (0,) * 10
 
 
 def kv_append(cache: KVCache, k, v, block_table, first, rot: Optional[Rotary] = None, q=None,
@@ -1037,21 +1060,27 @@ def kv_append(cache: KVCache, k, v, block_table, first, rot: Optional[Rotary] = 
         positions = _kv_index(positions, "positions", rows, index)
     if count is not None:
         count = _kv_index(count, "count", s.batch, index)
-    queries = (0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    queries = _NO_QUERIES
     if q is not None:
         if q.dim() != 3 or q.size(0) != rows:
             raise ValueError(f"q must be [{rows}][q_heads][{dim}]")
         given, q_heads = q, q.size(1)
         q, _, q_at, q_st, q_sh, q_code = _kv_rows(q, "q", q_heads, dim, index)
-        if q_out is given and q is not given:
+        if q is not given and q_out is given:
             raise ValueError("in place: dims contiguous, strides and address multiples of 16 bytes")
-        q_out, o_at, o_st, o_sh, o_code = _rotary_out(q, q_out, q_dtype, "q_out", index)
+        q_out, o_at, o_st, o_sh, o_code = _rotary_out(q, q_sh == dim and q_st == q_heads * dim, q_out,
+                                                      q_dtype, "q_out", index)
         queries = (q_at, q_st, q_sh, o_at, o_st, o_sh, q_code, o_code, q_heads, dim)
+    turn = (0, 0, 0, 0.0)
+    if rot is not None:
+        device, turn, _ = rot._fields or rot.fields()
+        if device != index:
+            raise ValueError("the frequencies must be on the cache's device")
     n = _KvNew()
     _pack(_KV_NEW, n, "the rows", k_at, k_st, k_sh, v_at, v_st, v_sh, code, kv_rows,
           0 if source is None else source.data_ptr(), 0 if count is None else count.data_ptr(),
           0 if positions is None else positions.data_ptr(),
-          *((0, 0, 0, 0.0) if rot is None else rot.fields(index)), *queries)
+          *turn, *queries)
     status = load_library().msq_kv_append(desc, s, first.data_ptr(), n,
                                           cuda._cuda_getCurrentRawStream(index))
     if status:
@@ -1100,8 +1129,7 @@ def draft_tree(parents, offset=None, first=None, max_count: int = 0, batch: int 
     if first is not None:
         first = _kv_index(first, "first", batch, index)
     words = max(1, (most + 31) // 32)
-    sets = torch.empty((total, words), dtype=torch.int32, device=parents.device)
-    positions = torch.empty_like(parents)
+    sets, positions = parents.new_empty((total, words)), torch.empty_like(parents)
     status = load_library().msq_draft_tree(
         parents.data_ptr(), 0 if offset is None else offset.data_ptr(), batch, total, max_count,
         0 if first is None else first.data_ptr(), sets.data_ptr(), words, positions.data_ptr(),
@@ -1165,8 +1193,8 @@ def verify_draft(tokens, target, offset=None, parents=None, draft=None, uniform=
             raise ValueError(f"uniform must be float32 [{total}] on target's device")
         uniform = uniform if uniform.is_contiguous() else uniform.contiguous()
     offset, batch, _ = _draft_rows(total, offset, batch, max_count, index)
-    token, taken = (torch.empty(batch, dtype=torch.int32, device=target.device) for _ in range(2))
     path = torch.empty_like(tokens)
+    token, taken = path.new_empty(batch), path.new_empty(batch)
     d = _Draft()
     _pack(_DRAFT, d, "sizes", batch, 0 if offset is None else offset.data_ptr(), total, max_count,
           vocab, tokens.data_ptr(), 0 if parents is None else parents.data_ptr(), target.data_ptr(),

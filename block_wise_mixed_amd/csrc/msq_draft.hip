@@ -600,7 +600,7 @@ msq_status plan_verify(const msq_draft& d, Rows& r, VerifyPlan& p) {
   // entries before its first group of four)
   const int64_t unit = d.uniform ? kSlice : kRowPart;
   const int64_t most = std::max<int64_t>(items, kFill), groups = ((int64_t)d.vocab + 3 + unit - 1) / unit;
-  p.parts = (int)std::clamp<int64_t>(std::min(kFill / items, groups), 1, kMostParts);
+  p.parts = (int)std::clamp<int64_t>(std::min(kFill / items, d.uniform ? (groups + 3) / 4 : groups), 1, kMostParts);
   if (d.uniform) {
     p.slice = (int)((groups + kMostSlices - 1) / kMostSlices * kSlice);
     p.slices = (int)(((int64_t)d.vocab + 3 + p.slice - 1) / p.slice);

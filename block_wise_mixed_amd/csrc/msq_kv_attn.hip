@@ -850,7 +850,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   constexpr int kTerms = kTwo ? 4 : 2;   // a strip's weights: the first terms, then what they leave
   const Place at_wg = place_of(a.c.H, a.nsplit, a.s.batch);
   const int h = at_wg.h, sp = at_wg.part, b = at_wg.low;
-  const int tile_row = a.row_tiles - 1 - at_wg.high;  // the longest rows first
+  // the longest rows first; by sets all are as long, and the last tile may have few rows
+  const int tile_row = kTree ? at_wg.high : a.row_tiles - 1 - at_wg.high;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
   // Blocks of the strips: lane j holds that of the j-th strip of a batch of 64,
