@@ -104,21 +104,16 @@ def build_host_sanitized(out: str, verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False) -> str:
+    from concurrent.futures import ThreadPoolExecutor
     cc = hipcc()
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
-        _compile(cc, src, obj, verbose=verbose)
-        objs.append(obj)
-    _link(cc, objs, LIB)
-    pobjs = []
-    for src in PROBE_SOURCES:
-        obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
-        _compile(cc, src, obj, verbose=verbose)
-        pobjs.append(obj)
-    _link(cc, pobjs, PROBE_LIB)
+    every = SOURCES + PROBE_SOURCES
+    objs = [os.path.join(objdir, os.path.splitext(src)[0] + ".o") for src in every]
+    with ThreadPoolExecutor(max(1, min(len(every), (os.cpu_count() or 1) // 2))) as ex:
+        list(ex.map(lambda so: _compile(cc, so[0], so[1], verbose=verbose), zip(every, objs)))
+    _link(cc, objs[:len(SOURCES)], LIB)
+    _link(cc, objs[len(SOURCES):], PROBE_LIB)
     return LIB
 
 

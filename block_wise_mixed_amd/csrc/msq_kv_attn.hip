@@ -1461,10 +1461,35 @@ size_t most_workspace(const Shape& z, int64_t longest) {
   return most;
 }
 
+// Trees of several row tiles in k_kv_decode: no more parts than the launch joins itself,
+// and none where a sequence is short.  On the GPU alone, 8 heads of 128, us, plan of other
+// calls, 4 parts, 1: 104 rows on 777 tokens 12.5, 10.6, 9.5; on 1500 13.0, 11.4, 12.7; 6000
+// 17.6, 16.8, 36.0; 20000 32.8, 42.1, 132; 480 rows on 777 (2 parts) 14.7, -, 9.6; heads of 64,
+// 104 rows on 777 8.6, 7.2, 7.6; on 1500 9.4, 7.9, 10.0; 6000 12.9, 12.3, 27.2; of 256 (where the launch
+// joins 2) on 777 15.2, -, 15.3.  A call without a launch for the join costs the host 3 us
+// less.  The workspace stays within what other calls of these sizes need.
+constexpr int kTreeTiles = 28, kTreeParts = 4, kTreeJoined = 192;
+void tree_parts(const Shape& z, int64_t tiles, AttnPlan& p) {
+  if (p.waves || z.rows <= kRowTile || p.nsplit == 1) return;
+  int parts = p.nsplit;
+  if (tiles <= kTreeTiles)
+    parts = 1;
+  else if (tiles <= kTreeJoined && parts > kTreeParts && z.tagged_parts() >= kTreeParts &&
+           z.tags_end(kTreeParts) <= p.workspace)
+    parts = kTreeParts;
+  if (parts == p.nsplit) return;
+  p.nsplit = parts;
+  p.span_tiles = (int)((tiles + parts - 1) / parts);
+  p.blocks = z.all(kRowTile) * parts;
+  p.ml_at = z.partials(parts);
+  p.tags_at = parts > 1 ? z.tags_at(parts) : 0;
+  p.workspace = parts > 1 ? z.tags_end(parts) : 0;
+}
+
 // Sizes only; MSQ_OK with blocks == 0 for an empty call.  most: also the most
 // workspace of calls with shorter sequences.
 msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_attn& t, int D,
-                     AttnPlan& p, size_t* most = nullptr) {
+                     AttnPlan& p, size_t* most = nullptr, bool tree = false) {
   p = AttnPlan{};
   if (t.q_heads < 1 || t.q_heads % c.H != 0 || t.window < 0 || t.max_kv_len < 0)
     return MSQ_ERR_SHAPE;
@@ -1526,6 +1551,7 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
     p.workspace = z.tags_end(p.nsplit);
   }
   if (most) *most = std::max(p.workspace, most_workspace(z, longest));
+  if (tree) tree_parts(z, tiles, p);
   return MSQ_OK;
 }
 
@@ -1624,7 +1650,7 @@ msq_status attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const m
       !(t.scale >= 0.f) || !std::isfinite(t.scale))
     return MSQ_ERR_INVALID_ARG;
   AttnPlan p;
-  st = plan_attn(a.c, a.s, t, D, p);
+  st = plan_attn(a.c, a.s, t, D, p, nullptr, kTree);
   if (st != MSQ_OK || p.blocks == 0) return st;
   st = kv_pointers(cache, seqs);
   if (st != MSQ_OK) return st;

@@ -618,9 +618,10 @@ msq_status msq_draft_tree(const int32_t *parents, const int32_t *offset, int32_t
  * (positions up to kv_len - n) and of these, at positions kv_len - n + j, the rows j
  * that its set has (device uint32 [total][words]; rows past 32 * words are in no set);
  * with a window the last window of them all.  Any sets will do, also empty ones and
- * ones without the row itself.  attn->causal must be set.  Plan, workspace and errors
- * as msq_kv_attention's; MSQ_ERR_INVALID_ARG also for null or misaligned sets,
- * MSQ_ERR_SHAPE for words < 1. */
+ * ones without the row itself.  attn->causal must be set.  fp32 results come of queries
+ * and weights of 22 bits (bf16 ones as msq_kv_attention's).  Workspace and errors as
+ * msq_kv_attention's, the plan too but for fewer parts of few rows;
+ * MSQ_ERR_INVALID_ARG also for null or misaligned sets, MSQ_ERR_SHAPE for words < 1. */
 msq_status msq_kv_attention_tree(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const msq_kv_attn *attn,
                                  const uint32_t *sets, int32_t words, void *workspace, size_t workspace_bytes,
                                  hipStream_t stream);
