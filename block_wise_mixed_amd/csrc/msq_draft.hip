@@ -153,9 +153,11 @@ __device__ inline double wave_scan(double x, int lane) {
 // one after another.
 enum Drafts { kChosen, kDrawnOne, kDrawn };
 
-// The row that the walk has reached, and the rows that it has not taken there: count of them
-// from `first` on, each with the next one, its token (kChosen) and the sum m of what was
-// left before it (kDrawn; 1 for the first).
+// The row that the walk has reached, and what it has not taken there.  Of chosen ones count
+// rows from `first` on, each with its token and the next one.  Of drawn ones what is left
+// is max(scale p - share q, 0): what max(r / m - q, 0) has brought to 0 stays 0, so the
+// steps one after another, r / m - q each, come to one multiple of p and one of q
+// (scale / m and share / m + 1), and no row is gone through more than once for a step.
 template <typename T>
 struct Row {
   const T *p, *q;
@@ -163,8 +165,12 @@ struct Row {
   bool aligned;
   int count, first;
   const int *next, *token;
-  const double* m;
+  double scale, share;
 };
+template <typename T>
+__device__ inline double left_of(const Row<T>& row, double p, double q) {
+  return fmax(fma(row.scale, p, -row.share * q), 0.0);
+}
 
 // What is left there of N tiles from v on (v + lead a multiple of 4), all read at once.
 template <typename T, Drafts kWay, int N>
@@ -195,19 +201,11 @@ __device__ inline void left_at(const Row<T>& row, int v, int lane, double (&r)[N
       each([&](double& p, float, int at) { p = t - 4 * lane == at ? 0.0 : p; });
     }
   } else {
-    each([&](double& p, float q, int) { p = fmax(p - mass(q), 0.0); });
-    if constexpr (kWay == kDrawn) {
-#pragma unroll 1
-      for (int k = 1, j = row.first; k < row.count; ++k) {
-        j = row.next[j];
-        const double m = row.m[j] > 0.0 ? row.m[j] : 1.0;
-        each([&](double& p, float q, int) { p = fmax(p / m - mass(q), 0.0); });
-      }
-    }
+    each([&](double& p, float q, int) { p = left_of(row, p, mass(q)); });
   }
 }
 
-// The sum of what is left in the slice from lo on, by one wavefront.  (A kernel's code is fetched
+// A lane's part of the sum of what is left in the slice from lo on.  (A kernel's code is fetched
 // as it goes: with tiles unrolled wherever they are looked at, 50 KB, a call took twice as
 // long as with a tile at a time.)
 constexpr int kSlice = 1024, kMostSlices = 256;
@@ -222,7 +220,7 @@ __device__ inline double left_sum(const Row<T>& row, int64_t lo, int size, int l
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum += (r[k][0] + r[k][1]) + (r[k][2] + r[k][3]);
   }
-  return wave_sum(sum);
+  return sum;
 }
 
 // By chance.  Every workgroup of a sequence walks through its tree: the probabilities of
@@ -231,13 +229,15 @@ __device__ inline double left_sum(const Row<T>& row, int64_t lo, int size, int l
 // up their slices of what is left at the row where the walk ends; the workgroup that
 // comes last (tags as in the cache attention's join) finds the slice in which the
 // running sum passes the number, and the entry in it.
+// Between siblings a workgroup needs the sum of a whole row at once: 16 wavefronts.
+constexpr int waves_of(Drafts way) { return way == kDrawn ? 16 : 4; }
 template <typename T, Drafts kWay>
-__global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
-  constexpr int kWaves = 4;
+__global__ __launch_bounds__(64 * waves_of(kWay)) void k_verify_chance(VerifyArgs a) {
+  constexpr int kWaves = waves_of(kWay), kThreads = 64 * kWaves;
   constexpr bool kDraft = kWay != kChosen;
-  __shared__ int parent[kMostRows], token[kMostRows], path[kMostRows], next[kMostRows];
+  __shared__ int parent[kMostRows], token[kMostRows], path[kMostRows], next[kDraft ? 1 : kMostRows];
   __shared__ float prob[kMostRows], drawn[kDraft ? kMostRows : 1], number_of[kMostRows];
-  __shared__ double m_of[kWay == kDrawn ? kMostRows : 1], shared_sum[kWaves];
+  __shared__ double shared_sum[kWaves];
   __shared__ double fresh[kMostSlices];  // sums of slices made by the workgroup that joins
   __shared__ int complete, last_of[kWaves], found;
   const int part = blockIdx.x % (unsigned)a.parts, b = blockIdx.x / (unsigned)a.parts;
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
   }
   const T* target = reinterpret_cast<const T*>(a.target);
   const T* draft = reinterpret_cast<const T*>(a.draft);
-  for (int i = threadIdx.x; i < n; i += 256) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
     const int p = parent_of(a.parents, row0, i), t = a.tokens[row0 + i];
     const bool some = p >= 0 && t >= 0 && t < a.V;
     parent[i] = p;
@@ -264,16 +264,17 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
 
   Row<T> row;
   row.V = a.V;
-  row.count = 0;
   row.first = 0;
   row.next = next;
   row.token = token;
-  row.m = m_of;
   auto reach = [&](int i) {
     row.p = target + (row0 + i) * a.ts;
     row.q = kDraft ? draft + (row0 + i) * a.ds : row.p;
     row.lead = lead_of(row.p);
     row.aligned = lead_of(row.q) == row.lead;
+    row.count = 0;
+    row.scale = 1.0;
+    row.share = 0.0;
   };
   reach(0);
   // the walk, the same in all wavefronts
@@ -301,12 +302,13 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
             for (int i = wave; i < a.slices; i += kWaves)
               s += left_sum<T, kWay>(row, (int64_t)i * a.slice - row.lead, a.slice, lane);
             __syncthreads();
+            s = wave_sum(s);
             if (lane == 0) shared_sum[wave] = s;
             __syncthreads();
-            m = (shared_sum[0] + shared_sum[1]) + (shared_sum[2] + shared_sum[3]);
+            m = 0.0;
+            for (int w = 0; w < kWaves; ++w) m += shared_sum[w];
           }
-          for (int k = 0, i = row.first; k < row.count; ++k, i = next[i])
-            r = fmax((k > 0 && m_of[i] > 0.0 ? r / m_of[i] : r) - q, 0.0);
+          r = left_of(row, r, q);
         }
       }
       if (x >= 0 && number(number_of[j]) * q * m < r) {
@@ -314,18 +316,22 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
         ++taken;
         at = j;
         m = 1.0;
-        row.count = 0;
         reach(j);
       } else {
-        // (every wavefront writes these, the same, and none reads them before it has)
-        if (row.count == 0)
-          row.first = j;
-        else
-          next[last] = j;
-        if constexpr (kWay == kDrawn) m_of[j] = m;
-        last = j;
-        __builtin_amdgcn_wave_barrier();
-        m = kDraft ? -1.0 : m - r;
+        if constexpr (kDraft) {
+          if (m > 0.0) row.scale /= m, row.share /= m;
+          row.share += 1.0;
+          m = -1.0;
+        } else {
+          // (every wavefront writes this, the same, and none reads it before it has)
+          if (row.count == 0)
+            row.first = j;
+          else
+            next[last] = j;
+          last = j;
+          __builtin_amdgcn_wave_barrier();
+          m -= r;
+        }
         ++row.count;
       }
     }
@@ -339,7 +345,7 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
   int s = -1;
   for (bool joined = false;; joined = true) {
     for (int i = begin + wave; i < end; i += kWaves) {
-      const double sum = left_sum<T, kWay>(row, (int64_t)i * a.slice - row.lead, a.slice, lane);
+      const double sum = wave_sum(left_sum<T, kWay>(row, (int64_t)i * a.slice - row.lead, a.slice, lane));
       if (lane == 0) {
         // (two workgroups may both see that all have come: what one makes after that is its own)
         if (joined)
@@ -393,19 +399,19 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
       break;
     }
     if (joined || row.count == 0) break;
-    row.count = 0;  // nothing is left: the distribution as it was
+    reach(at);  // nothing is left: the distribution as it was
     begin = 0, end = a.slices;
     __syncthreads();
   }
   if (threadIdx.x == 0) found = -1;
   if (s >= 0) {
-    // a quarter of 1024 entries for each wavefront
+    // a tile for each wavefront
     const int64_t lo = (int64_t)s * a.slice - row.lead, hi = min(lo + a.slice, (int64_t)a.V);
     int spare = -1;  // the last entry with any mass
-    for (int64_t c = lo; c < hi; c += kSlice) {
+    for (int64_t c = lo; c < hi; c += 256 * kWaves) {
       const int v = (int)c + 256 * wave + 4 * lane;
-      double tile[1][4];
-      left_at<T, kWay>(row, (int)c + 256 * wave, lane, tile);
+      double tile[1][4] = {{0.0, 0.0, 0.0, 0.0}};
+      if (c + 256 * wave < hi) left_at<T, kWay>(row, (int)c + 256 * wave, lane, tile);
       const double(&r)[4] = tile[0];
       const double here = (r[0] + r[1]) + (r[2] + r[3]);
       const double upto = wave_scan(here, lane), sum = __shfl(upto, 63);
@@ -451,7 +457,7 @@ __global__ __launch_bounds__(256) void k_verify_chance(VerifyArgs a) {
     if (spare >= 0 && threadIdx.x == 0) found = spare;
   }
   if (threadIdx.x == 0) a.token[b] = found, a.taken[b] = taken;
-  for (int i = threadIdx.x; i < count; i += 256) a.path[row0 + i] = i < taken ? row0 + path[i] : -1;
+  for (int i = threadIdx.x; i < count; i += kThreads) a.path[row0 + i] = i < taken ? row0 + path[i] : -1;
 }
 
 constexpr int kRowPart = 4096;  // least entries of a row's part: each thread reads 16 at once
@@ -600,7 +606,10 @@ msq_status plan_verify(const msq_draft& d, Rows& r, VerifyPlan& p) {
   // entries before its first group of four)
   const int64_t unit = d.uniform ? kSlice : kRowPart;
   const int64_t most = std::max<int64_t>(items, kFill), groups = ((int64_t)d.vocab + 3 + unit - 1) / unit;
-  p.parts = (int)std::clamp<int64_t>(std::min(kFill / items, d.uniform ? (groups + 3) / 4 : groups), 1, kMostParts);
+  const int64_t waves = waves_of(!d.draft ? kChosen : d.parents ? kDrawn : kDrawnOne);
+  const int64_t fill = d.uniform ? 4 * kFill / waves : kFill;           // workgroups
+  const int64_t split = d.uniform ? (groups + waves - 1) / waves : groups;  // a slice a wavefront at least
+  p.parts = (int)std::clamp<int64_t>(std::min(fill / items, split), 1, kMostParts);
   if (d.uniform) {
     p.slice = (int)((groups + kMostSlices - 1) / kMostSlices * kSlice);
     p.slices = (int)(((int64_t)d.vocab + 3 + p.slice - 1) / p.slice);
@@ -686,7 +695,7 @@ extern "C" msq_status msq_verify_draft(const msq_draft* d, void* workspace, size
       using T = decltype(t);
       if (!drawn) hipLaunchKernelGGL((k_verify_chance<T, kChosen>), grid, threads, 0, stream, a);
       else if (!d->parents) hipLaunchKernelGGL((k_verify_chance<T, kDrawnOne>), grid, threads, 0, stream, a);
-      else hipLaunchKernelGGL((k_verify_chance<T, kDrawn>), grid, threads, 0, stream, a);
+      else hipLaunchKernelGGL((k_verify_chance<T, kDrawn>), grid, dim3(64 * waves_of(kDrawn)), 0, stream, a);
     };
     f32 ? go(float{}) : go(uint16_t{});
     return hipGetLastError() == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
