@@ -983,6 +983,12 @@ def _rotary_out(x, contiguous, out, out_dtype, name, index):
     per16 = 4 if code else 8
     if out.numel() and (sd != 1 or st % per16 or sh % per16 or out.data_ptr() % 16):
         raise ValueError(f"{name}: dims contiguous, strides and address multiples of 16 bytes")
+    reach = out.shape[2]  # of what a step of the smaller stride has to pass, then of the larger
+    for stride, size in sorted(((st, out.shape[0]), (sh, out.shape[1]))):
+        if size > 1:
+            if stride < reach:
+                raise ValueError(f"{name}'s rows overlap")
+            reach = stride * size
     return out, out.data_ptr(), st, sh, code
 
 

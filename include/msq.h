@@ -562,8 +562,8 @@ typedef struct {
  * 2^32 threads do not do), asynchronous.  rows == 0 is a no-op.  Errors:
  * MSQ_ERR_INVALID_ARG (null or misaligned pointer, unknown dtype, an amplitude that is
  * not finite), MSQ_ERR_SHAPE (heads or head_dim outside the ranges above, dims no
- * positive multiple of 16 or above head_dim, rows negative or past 2^31 - 1),
- * MSQ_ERR_HIP. */
+ * positive multiple of 16 or above head_dim, rows negative or past 2^31 - 1, more than
+ * 2^32 - 1 workgroups of 4096 values), MSQ_ERR_HIP. */
 msq_status msq_rotary_apply(const msq_rotary *rot, const msq_rotary_rows *x, const int32_t *positions,
                             int64_t rows, hipStream_t stream);
 
@@ -589,8 +589,9 @@ typedef struct {
  * source and count, rows that were written before are written again: the drafted tokens
  * that msq_verify_draft keeps (its path and taken) then stand in the cache one after
  * another.  Query rows of sequences with first < 0, past count or outside every
- * sequence are left as they are.  Launches and errors as msq_kv_write and
- * msq_rotary_apply; MSQ_ERR_INVALID_ARG also for queries together with source. */
+ * sequence are left as they are; those of tokens whose block is absent are rotated.
+ * Launches and errors as msq_kv_write and msq_rotary_apply; MSQ_ERR_INVALID_ARG also for
+ * queries together with source, MSQ_ERR_SHAPE for more than 2^31 - 1 workgroups. */
 msq_status msq_kv_append(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
                          const msq_kv_new *rows, hipStream_t stream);
 

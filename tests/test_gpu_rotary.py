@@ -106,6 +106,12 @@ def test_strides_in_place_and_out(msq, dtype):
     to = torch.full((12, 20, 128), 7.0, dtype=torch.float32, device="cuda").transpose(0, 1)
     assert torch.equal(msq.rotary(xt, i32(at), rot, out=to), msq.rotary(xt, i32(at), rot, out_dtype=torch.float32))
     assert msq.rotary(xt[:0], i32([]), rot).shape == (0, 12, 128)
+    for overlapping in (xt[:1].expand(20, 12, 128), xt[:, :1].expand(20, 12, 128), xt.view(-1)[:20 * 128 + 11 * 64]
+                        .as_strided((20, 12, 128), (128, 64, 1))):
+        with pytest.raises(ValueError):
+            msq.rotary(xt, i32(at), rot, out=overlapping)
+    wide = torch.zeros(20, 12, 256, dtype=dtype, device="cuda")[..., :128]
+    assert torch.equal(msq.rotary(xt, i32(at), rot, out=wide), want)
 
 
 def test_inverse_is_the_gradient(msq):
