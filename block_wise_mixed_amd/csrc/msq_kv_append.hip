@@ -5,7 +5,13 @@
 // two own what the call changes in their block and heads, as in msq_kv.hip, and the
 // quantiser is the same.  The turns (cosine and sine of a position) of a block's new
 // tokens are made in LDS, in fp64, and used for all heads of the workgroup; a lane
-// reads the 8 dims it holds and the 8 that these are paired with.
+// reads the 8 dims it holds and the 8 that these are paired with (from L1: HBM sees
+// every value once, 1.00 of what the call has to move by the counters).
+//
+// HBM bound on long runs: 16 sequences of 4097 to 8192 bf16 tokens, 32 query heads on 8 of
+// 128, 2.28 GB in 455 to 473 us, 4.8 to 5.0 TB/s.  A step of 64 fp32 tokens with 64
+// query heads: 7.0 us, a chain of loads (first, table, positions, frequencies) and the fp64
+// turns behind it.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -181,7 +187,9 @@ __global__ __launch_bounds__(1024) void k_kv_append(AppendArgs a) {
       });
 }
 
-// Most LDS for a table of turns (a compute unit has 160 KB).
+// Most LDS for a table of turns (a compute unit has 160 KB).  A table of that size, of blocks of
+// 256 tokens, leaves one workgroup a compute unit and is still ahead of turns made by each lane
+// (16 sequences of 3000 tokens, 4 heads of 256, a head a workgroup: 117 and 154 us).
 constexpr size_t kMostTable = 128 << 10;
 
 template <int D, typename T>
@@ -191,8 +199,11 @@ msq_status launch_append(AppendArgs& a, int64_t lists, bool queries, hipStream_t
   const int waves = strips * (D / (wide || D == 64 ? 64 : 128)), threads = 64 * waves;
   const size_t table = (size_t)std::min(P, a.s.max_count) * a.r.half * sizeof(float2);
   const bool fits = table <= kMostTable;
-  // Heads of a workgroup of keys: more share the turns, fewer fill the GPU.
-  a.heads = fits ? (int)std::clamp<int64_t>(lists * a.c.H / 1024, 1, a.c.H) : 1;
+  // Heads of a workgroup of keys: more share the turns, fewer fill the GPU; as many as leave
+  // 12 wavefronts a compute unit.  Keys and values of 8 heads of 128 in blocks of 64, 1, 2, 4 and 8
+  // heads a workgroup: 16 sequences of 6000 tokens 243, 189, 165, 153 us; one of 2000 11, 14, 20, 32;
+  // 64 of 64 15.0, 15.5, 21.5, 33; 4 heads of 256 in blocks of 256, 16 of 3000, 1, 2, 4: 117, 98, 86.
+  a.heads = fits ? (int)std::clamp<int64_t>(lists * a.c.H * waves / 3072, 1, a.c.H) : 1;
   a.groups = (a.c.H + a.heads - 1) / a.heads;
   int64_t query_sets = 0;
   size_t lds = std::max(fits ? table : 0, (size_t)waves * (wide || D == 64 ? Map<64>::kImage : Map<128>::kImage));

@@ -41,8 +41,10 @@
 // bf16 alone is 1.7e-3.  The second term costs 2 to 4% in k_kv_decode and 18 to 29%
 // in k_kv_prefill (2048 rows of 64 heads on 16000 tokens 941 -> 1215 us).  L of the
 // rounded weights, which cancels some of their rounding: 1.9e-4 -> 1.7e-4 and 1.2e-4 ->
-// 0.7e-4, at 4% of the time of many rows; not taken.  Attention by sets (kTree) has
-// both in two terms where the results are fp32, which are then some 1e-6 away.
+// 0.7e-4, at 4% of the time of many rows; not taken.  Attention by sets has the weights in
+// two terms too where the results are fp32 (kSetsFine), which are then 1e-7 to 1e-6 away;
+// bf16 results, fp32 ones of bf16 and of fp32 queries: 4 trees of 64 on up to 131000 tokens, 64
+// query heads on 8 of 128, 1030, 1410, 1750 us; one of 26 on 751, 32 heads on 8, 9.8, 10.6, 11.8.
 #include <hip/hip_runtime.h>
 #include <unistd.h>
 
@@ -78,6 +80,10 @@ constexpr int kMostParts = 64;     // parts of a row tile's tokens
 constexpr uint32_t kNoScale = 0x72000000;  // 2^101, inverse of less than any scale
 constexpr uint32_t kFaint = 64u << 23;  // 2^64, between the bit patterns of two scales' inverses
 constexpr float kTinyStep = 1e-37f;  // keeps -inf * step from being NaN where a step is 0
+
+// Whether rows see of their call's own tokens those of a set, and for fp32 results go with
+// weights in two f16 terms.
+enum Sets { kNoSets, kSets, kSetsFine };
 
 struct AttnArgs {
   KvCacheView c;
@@ -199,7 +205,6 @@ __device__ inline void query_fragments(const Raw8 (&raw)[N], int f32, half8 (&q)
         q[s][2 * e] = (_Float16)(__uint_as_float(w[e] << 16) * up);
         q[s][2 * e + 1] = (_Float16)(__uint_as_float(w[e] & 0xFFFF0000u) * up);
       }
-      if constexpr (kFine) rest[s] = half8{};
     }
   }
 }
@@ -310,7 +315,12 @@ __device__ inline void row_range(const AttnArgs& a, int len, int n, int i, int& 
 // The same for rows that see, of their call's n rows, those of a set: from lo on, and of
 // the call's own (at positions len - n + j) those that the set has.  A window counts
 // from the end of what a row sees, so lo is the first of the set that it still holds, or
-// as far before the call's rows as the set leaves of it.
+// as far before the call's rows as the set leaves of it.  Only the tiles that hold own rows
+// look at the bits, some n / 32 + 1 of them.  Trees on the 8-bit cache: 30 of up to 33 rows
+// on up to 4063 tokens, 64 query heads on 8 of 128, 128 us, 53 at the matrix rate: 264 rows a
+// head are a tile of 256 and one of 8, which takes half the time of a full one, and
+// the longest sequence alone takes 115 (tiles in the other order, the small first, 142;
+// three of 128 rows 132); 4 of up to 64 on up to 131000 1030, 841 at the matrix rate.
 __device__ inline void tree_range(const AttnArgs& a, int len, int n, int row, int& lo, int& hi) {
   lo = 0;
   hi = min(len, a.s.width << a.c.shift);
@@ -481,10 +491,10 @@ __device__ inline void load_tile(Tile<D>& t, const KvCacheView& c, int id, int h
   for (int i = 0; i < D / 32; ++i) t.v[i] = v[64 * i];
 }
 
-template <int D, bool kFine, bool kTree>
+template <int D, bool kFine, Sets kTree>
 __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
   constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
-  constexpr bool kTwo = kFine && kTree;  // weights in two f16 terms
+  constexpr bool kTwo = kTree == kSetsFine;  // weights in two f16 terms
   constexpr int kStride = D + 4;
   const Place at_wg = place_of(a.c.H, a.nsplit, a.row_tiles);
   const int h = at_wg.h, sp = at_wg.part, tile_row = at_wg.low, b = at_wg.high;
@@ -495,7 +505,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   kv_rows(a.s, b, row0, n);
   const int rows = n * a.G, r0 = tile_row * kRowTile;
   if (r0 >= rows) return;
-  const Parts pt = parts_of<kTree>(a, len, n, r0);
+  const Parts pt = parts_of<kTree != kNoSets>(a, len, n, r0);
   const int lo1 = pt.lo_last, hi0 = pt.hi_first;
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   const int parts = pt.parts;
@@ -840,13 +850,13 @@ struct Prefill {
   }
 };
 
-template <int D, int W, bool kFine, bool kTree>
+template <int D, int W, bool kFine, Sets kTree>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArgs a) {
   using C = Prefill<D, W>;
   constexpr int kStage = C::kStage, kSteps = C::kSteps, kTiles = C::kTiles;
   constexpr int kProducts = C::kProducts, kAhead = C::kAhead, kStrips = C::kStrips;
   constexpr int kRing = 2 * kStrips, kBatch = 64 / kStrips;
-  constexpr bool kTwo = kFine && kTree;  // weights in two f16 terms
+  constexpr bool kTwo = kTree == kSetsFine;  // weights in two f16 terms
   constexpr int kTerms = kTwo ? 4 : 2;   // a strip's weights: the first terms, then what they leave
   const Place at_wg = place_of(a.c.H, a.nsplit, a.s.batch);
   const int h = at_wg.h, sp = at_wg.part, b = at_wg.low;
@@ -869,7 +879,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   kv_rows(a.s, b, row0, n);
   const int rows = n * a.G, r0 = tile_row * C::kRows;
   if (r0 >= rows) return;
-  const Parts pt = parts_of<kTree>(a, len, n, r0);
+  const Parts pt = parts_of<kTree != kNoSets>(a, len, n, r0);
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   if (t0 >= t1 && a.nsplit > 1) return;
   if (t0 != guess) id0 = blocks_at(t0), id1 = blocks_at(t0 + kBatch), id2 = blocks_at(t0 + 2 * kBatch);
@@ -889,7 +899,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   else
     row_range(a, len, n, i, my_lo, my_hi);
   int w_lo, w_hi, w_lo_last, w_hi_first;
-  rows_range<kTree>(a, len, n, over(min(w0, rows - 1), a.G), over(min(w0 + 31, rows - 1), a.G), w_lo, w_hi_first,
+  rows_range<kTree != kNoSets>(a, len, n, over(min(w0, rows - 1), a.G), over(min(w0 + 31, rows - 1), a.G), w_lo, w_hi_first,
                     w_lo_last, w_hi);
   if (w0 >= rows) w_hi = 0;
   // its stages: a0 .. a1 - 1 (none: a0 == a1)
@@ -1555,7 +1565,7 @@ msq_status plan_attn(const KvCacheView& c, const KvSeqsView& s, const msq_kv_att
   return MSQ_OK;
 }
 
-template <int D, bool kFine, bool kTree>
+template <int D, bool kFine, Sets kTree>
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   if (p.waves) {
     auto prefill = [&](auto w) {
@@ -1575,9 +1585,9 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
     // few rows: four wavefronts each (64 rows of 60 parts: 12.1 -> 9.6 us; 4800 rows of 17
     // parts: 34.7 -> 43.1)
     if (rows <= 1024)
-      hipLaunchKernelGGL((k_kv_join<D, 4, kTree>), dim3((unsigned)rows), dim3(256), 0, stream, a, rows);
+      hipLaunchKernelGGL((k_kv_join<D, 4, kTree != kNoSets>), dim3((unsigned)rows), dim3(256), 0, stream, a, rows);
     else
-      hipLaunchKernelGGL((k_kv_join<D, 1, kTree>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, rows);
+      hipLaunchKernelGGL((k_kv_join<D, 1, kTree != kNoSets>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, rows);
   }
   return hipGetLastError();
 }
@@ -1689,13 +1699,20 @@ msq_status attention(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const m
   a.c2 = (t.scale > 0.f ? t.scale : 1.f / std::sqrt((float)D)) * kLog2e;
   a.sets = sets;
   a.words = words;
-  const bool fine = (a.q_f32 || kTree) && a.out_f32;
-  hipError_t e;
-  switch (D) {
-    case 64: e = fine ? launch_attn<64, true, kTree>(a, p, stream) : launch_attn<64, false, kTree>(a, p, stream); break;
-    case 128: e = fine ? launch_attn<128, true, kTree>(a, p, stream) : launch_attn<128, false, kTree>(a, p, stream); break;
-    default: e = fine ? launch_attn<256, true, kTree>(a, p, stream) : launch_attn<256, false, kTree>(a, p, stream); break;
-  }
+  const bool fine = a.q_f32 && a.out_f32;
+  auto launch = [&](auto dims) {
+    constexpr int kD = decltype(dims)::value;
+    if constexpr (kTree) {
+      if (a.out_f32)
+        return fine ? launch_attn<kD, true, kSetsFine>(a, p, stream) : launch_attn<kD, false, kSetsFine>(a, p, stream);
+      return launch_attn<kD, false, kSets>(a, p, stream);
+    } else {
+      return fine ? launch_attn<kD, true, kNoSets>(a, p, stream) : launch_attn<kD, false, kNoSets>(a, p, stream);
+    }
+  };
+  const hipError_t e = D == 64 ? launch(std::integral_constant<int, 64>{})
+                       : D == 128 ? launch(std::integral_constant<int, 128>{})
+                                  : launch(std::integral_constant<int, 256>{});
   return e == hipSuccess ? MSQ_OK : MSQ_ERR_HIP;
 }
 

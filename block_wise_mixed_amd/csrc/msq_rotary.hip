@@ -23,8 +23,11 @@ struct RotaryArgs {
 
 extern __shared__ __align__(16) unsigned char smem_turns[];
 
-// A workgroup takes a few rows of some heads: the turns of a row are made once in LDS,
-// in fp64, and used for all of its heads.
+// A workgroup takes a few rows of some heads, a unit of 16 values a thread: the turns of a row are
+// made once in LDS, in fp64, and used for all of its heads.  HBM bound: 28707 rows of 32 bf16
+// heads of 128, 470 MB in 77 to 81 us, 5.8 to 6.1 TB/s (a large copy runs at 5.1 to 5.2).  With four
+// units a thread, and so fewer, longer workgroups, 162 us; with 64 rows a workgroup 192.  A
+// step of 64 rows of 64 fp32 heads 3.5 us.
 __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a) {
   const unsigned id = a.begin + blockIdx.x, chunk = id / (unsigned)a.parts, part = id - chunk * a.parts;
   const int row0 = (int)chunk * a.each, rows = min(a.each, a.rows - row0);
