@@ -237,8 +237,8 @@ __device__ inline double left_sum(const Row<T>& row, int64_t lo, int size, int l
 // 128000 fp32 entries, 65 MB in 16 to 18 us (12.7 at the copy rate).  Fewer sequences are a
 // chain of some ten loads, stores and waits: one chain of 32000 8.7 us, a chosen tree of 26
 // of 128000 11, 16 of up to 32 16.  Between drawn siblings a compute unit reads both rows,
-// 1 MB for 128000 entries, some 10 us a sibling: 16 trees of 32 153 us, one of 26 21.
-// Between siblings a workgroup needs the sum of a whole row at once: 16 wavefronts.
+// 1 MB for 128000 entries, some 10 us a sibling: 16 trees of 32 153 us, one of 26 21 (with
+// four wavefronts a workgroup and r / m - q for each sibling in turn 756 and 27).
 constexpr int waves_of(Drafts way) { return way == kDrawn ? 16 : 4; }
 template <typename T, Drafts kWay>
 __global__ __launch_bounds__(64 * waves_of(kWay)) void k_verify_chance(VerifyArgs a) {
@@ -434,17 +434,17 @@ __global__ __launch_bounds__(64 * waves_of(kWay)) void k_verify_chance(VerifyArg
       const int wave_last = some ? __shfl(any, 63 - __builtin_clzll(some)) : -1;
       if (lane == 0) last_of[wave] = wave_last;
       __syncthreads();
-      int quarter = -1;
+      int hit_wave = -1;
       double before = start;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const double t = shared_sum[w];
         if (last_of[w] >= 0) spare = last_of[w];
-        if (quarter < 0 && t > 0.0 && start + t > x) quarter = w, before = start;
+        if (hit_wave < 0 && t > 0.0 && start + t > x) hit_wave = w, before = start;
         start += t;
       }
-      if (quarter < 0) continue;
-      if (wave == quarter) {
+      if (hit_wave < 0) continue;
+      if (wave == hit_wave) {
         const uint64_t past = __ballot(any >= 0 && before + upto > x);
         const int from = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
         double t = before + (upto - here);
@@ -632,7 +632,7 @@ msq_status plan_verify(const msq_draft& d, Rows& r, VerifyPlan& p) {
   }
   p.workspace = p.at + (size_t)most * 8;
   p.blocks = items * p.parts;
-  if (p.blocks > kMostThreads / 256) return MSQ_ERR_SHAPE;
+  if (p.blocks > kMostThreads / (64 * (d.uniform ? waves : 4))) return MSQ_ERR_SHAPE;
   return MSQ_OK;
 }
 

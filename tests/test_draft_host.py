@@ -170,6 +170,10 @@ def test_verify_arguments(lib):
         assert run(ws=BASE + 128, n=need, **kw) == INVALID
     assert f(draft(batch=0, offset=None, total=0, token=None, taken=None), None, 0, None) == OK
     assert size(draft(batch=0, offset=None, total=0)) == 0 and size(draft(vocab=0)) == 0
+    # 2^32 - 1 threads of one launch: 1024 a sequence between drawn siblings, else 256
+    for most, kw in ((1 << 22, dict()), (1 << 24, dict(parents=None)), (1 << 24, dict(draft=None))):
+        assert size(draft(batch=most - 1, **kw)) > 0 and size(draft(batch=most, **kw)) == 0
+        assert run(batch=most - 1, ws=None, **kw) == INVALID and run(batch=most, ws=None, **kw) == SHAPE
 
 
 def test_verify_workspace_covers_smaller_calls(lib):
