@@ -939,18 +939,23 @@ class Rotary:
     frequencies: "object"
     interleaved: bool = False
     amplitude: float = 1.0
+    _fields = None
 
     def __post_init__(self):
         self.fields()
+
+    def __getstate__(self):  # copied and stored without the C structs
+        return {name: value for name, value in vars(self).items() if name != "_fields"}
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_fields", None)
 
     def fields(self):
-        """(device, its fields in the C structs, the struct); made anew after a field was set."""
-        if self._fields is None:
-            f = self.frequencies
+        """(device, its fields in the C structs, the struct); made anew after a field was set, and
+        where the frequencies' data was."""
+        f, kept = self.frequencies, self._fields
+        if kept is None or f.data_ptr() != kept[1][0] or 2 * f.numel() != kept[1][1]:
             if f.dtype is not _torch().float64 or f.dim() != 1 or f.numel() < 8 or f.numel() % 8 or \
                     not f.is_contiguous():
                 raise ValueError("frequencies must be contiguous float64 [dims / 2], dims a multiple of 16")
@@ -1009,7 +1014,7 @@ def rotary(x, positions, rot: Rotary, out=None, out_dtype=None, stream=None):
     if x is not given and out is given:
         raise ValueError("in place: dims contiguous, strides and address multiples of 16 bytes")
     positions = _kv_index(positions, "positions", rows, index)
-    device, _, r = rot._fields or rot.fields()
+    device, _, r = rot.fields()
     if device != index:
         raise ValueError("the frequencies must be on x's device")
     out, o_at, o_st, o_sh, o_code = _rotary_out(x, sh == dim and st == heads * dim, out, out_dtype, "out", index)
@@ -1079,7 +1084,7 @@ def kv_append(cache: KVCache, k, v, block_table, first, rot: Optional[Rotary] = 
         queries = (q_at, q_st, q_sh, o_at, o_st, o_sh, q_code, o_code, q_heads, dim)
     turn = (0, 0, 0, 0.0)
     if rot is not None:
-        device, turn, _ = rot._fields or rot.fields()
+        device, turn, _ = rot.fields()
         if device != index:
             raise ValueError("the frequencies must be on the cache's device")
     n = _KvNew()

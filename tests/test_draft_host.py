@@ -1,6 +1,8 @@
 """Refusals and sizes of the entry points for rotary positions and drafted tokens, before any launch (no
 GPU needed)."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 
@@ -214,6 +216,13 @@ def test_binding_refuses(lib):
     r.frequencies = f.float()
     with pytest.raises(ValueError):
         r.fields()
+    r = msq.Rotary(f.clone())              # so do a copy's, and data set from outside
+    twin = copy.deepcopy(r)
+    assert pickle.loads(pickle.dumps(r)).fields()[1][1:] == r.fields()[1][1:]
+    assert twin.fields()[1] == (twin.frequencies.data_ptr(), 64, 0, 1.0) != r.fields()[1]
+    assert twin.fields()[2].freq == twin.frequencies.data_ptr() != r.fields()[2].freq
+    r.frequencies.data = f[:16].clone()
+    assert r.fields()[1] == (r.frequencies.data_ptr(), 32, 0, 1.0) and r.fields()[2].dims == 32
     r = msq.Rotary(f)
     i = lambda *v: torch.tensor(v, dtype=torch.int32)
     x = torch.zeros(2, 2, 64)
