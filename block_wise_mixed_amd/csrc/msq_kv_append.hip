@@ -203,7 +203,7 @@ msq_status launch_append(AppendArgs& a, int64_t lists, bool queries, hipStream_t
   // 12 wavefronts a compute unit.  Keys and values of 8 heads of 128 in blocks of 64, 1, 2, 4 and 8
   // heads a workgroup: 16 sequences of 6000 tokens 243, 189, 165, 153 us; one of 2000 11, 14, 20, 32;
   // 64 of 64 15.0, 15.5, 21.5, 33; 4 heads of 256 in blocks of 256, 16 of 3000, 1, 2, 4: 117, 98, 86.
-  a.heads = fits ? (int)std::clamp<int64_t>(lists * a.c.H * waves / 3072, 1, a.c.H) : 1;
+  a.heads = fits ? (int)std::clamp<int64_t>(lists * a.c.H * waves / (12 * 256), 1, a.c.H) : 1;
   a.groups = (a.c.H + a.heads - 1) / a.heads;
   int64_t query_sets = 0;
   size_t lds = std::max(fits ? table : 0, (size_t)waves * (wide || D == 64 ? Map<64>::kImage : Map<128>::kImage));

@@ -588,8 +588,9 @@ typedef struct {
  * queries.  The keys enter the quantiser as the fp32 results of the rotation.  With
  * source and count, rows that were written before are written again: the drafted tokens
  * that msq_verify_draft keeps (its path and taken) then stand in the cache one after
- * another.  Query rows of sequences with first < 0, past count or outside every
- * sequence are left as they are; those of tokens whose block is absent are rotated.
+ * another.  (A block's scale does not shrink again until the block is begun anew: drafts
+ * that are not kept leave theirs.)  Query rows of sequences with first < 0, past count
+ * or outside every sequence are left as they are; those of tokens whose block is absent are rotated.
  * Launches and errors as msq_kv_write and msq_rotary_apply; MSQ_ERR_INVALID_ARG also for
  * queries together with source, MSQ_ERR_SHAPE for more than 2^31 - 1 workgroups. */
 msq_status msq_kv_append(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const int32_t *first,
