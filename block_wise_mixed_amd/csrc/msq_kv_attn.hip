@@ -317,10 +317,9 @@ __device__ inline void row_range(const AttnArgs& a, int len, int n, int i, int& 
 // from the end of what a row sees, so lo is the first of the set that it still holds, or
 // as far before the call's rows as the set leaves of it.  Only the tiles that hold own rows
 // look at the bits, some n / 32 + 1 of them.  Trees on the 8-bit cache: 30 of up to 33 rows
-// on up to 4063 tokens, 64 query heads on 8 of 128, 128 us, 53 at the matrix rate: 264 rows a
-// head are a tile of 256 and one of 8, which takes half the time of a full one, and
-// the longest sequence alone takes 115 (tiles in the other order, the small first, 142;
-// three of 128 rows 132); 4 of up to 64 on up to 131000 1030, 841 at the matrix rate.
+// on up to 4063 tokens, 64 query heads on 8 of 128, 116 us, 53 at the matrix rate: the longest
+// sequence alone takes 107 (its tokens in two parts, and a launch that joins them, 142; three
+// tiles of 128 rows 132); 4 of up to 64 on up to 131000 1030, 841 at the matrix rate.
 __device__ inline void tree_range(const AttnArgs& a, int len, int n, int row, int& lo, int& hi) {
   lo = 0;
   hi = min(len, a.s.width << a.c.shift);
@@ -491,27 +490,17 @@ __device__ inline void load_tile(Tile<D>& t, const KvCacheView& c, int id, int h
   for (int i = 0; i < D / 32; ++i) t.v[i] = v[64 * i];
 }
 
-template <int D, bool kFine, Sets kTree>
-__global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
-  constexpr int kSteps = D / 32, kTiles = D / 16, kWaves = 4;
+// The rows r0 .. r0 + 15 of sequence b by the kWaves wavefronts of a workgroup, over its part
+// sp, the tiles t0 .. t1 - 1 (kTags: which may have to be joined here).
+template <int D, bool kFine, Sets kTree, int kWaves, bool kTags>
+__device__ __forceinline__ void few_rows(const AttnArgs& a, int h, int b, int tile_row, int sp, int len, int row0, int n,
+                                         int r0, const Parts& pt, int t0, int t1) {
+  constexpr int kSteps = D / 32, kTiles = D / 16;
   constexpr bool kTwo = kTree == kSetsFine;  // weights in two f16 terms
   constexpr int kStride = D + 4;
-  const Place at_wg = place_of(a.c.H, a.nsplit, a.row_tiles);
-  const int h = at_wg.h, sp = at_wg.part, tile_row = at_wg.low, b = at_wg.high;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int len = length_of(a, b);
-  int row0, n;
-  kv_rows(a.s, b, row0, n);
-  const int rows = n * a.G, r0 = tile_row * kRowTile;
-  if (r0 >= rows) return;
-  const Parts pt = parts_of<kTree != kNoSets>(a, len, n, r0);
-  const int lo1 = pt.lo_last, hi0 = pt.hi_first;
-  const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
-  const int parts = pt.parts;
-  // rows that see nothing are left to the first part, or to the join launch
-  if (t0 >= t1 && a.nsplit > 1 && !(a.tags && parts == 0 && sp == 0)) return;
-
+  const int rows = n * a.G, lo1 = pt.lo_last, hi0 = pt.hi_first, parts = pt.parts;
   const int r = min(r0 + col, rows - 1);
   const int i = over(r, a.G), hq = h * a.G + r - i * a.G;
   int my_lo, my_hi;
@@ -709,14 +698,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   const int64_t orow = (int64_t)(row0 + io) * a.Hq + h * a.G + ro - io * a.G;
   const int64_t step = (int64_t)a.s.total * a.Hq;
   const bool mine = r0 + rr < rows;
-  if (a.tags ? parts > 1 : a.nsplit > 1) {
+  if (kTags && a.tags ? parts > 1 : a.nsplit > 1) {
     if (mine) {
       put2(reinterpret_cast<uint64_t*>(a.part_ml + sp * step + orow), m, l, d0 == 0);
       uint64_t* po = reinterpret_cast<uint64_t*>(a.part_o + (sp * step + orow) * D + d0);
 #pragma unroll
       for (int e = 0; e < kPer; e += 2) put2(po + e / 2, x[e], x[e + 1], true);
     }
-    if (!a.tags) return;
+    if (!kTags || !a.tags) return;
     // Join here if this part is the last to come.  The device-scope stores above
     // have reached the level that all XCDs share once vmcnt is 0; only then is
     // the part's tag stored, and the tags are looked at after that, so the part
@@ -787,6 +776,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   if (a.lse && d0 == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
 }
 
+template <int D, bool kFine, Sets kTree>
+__global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
+  const Place at_wg = place_of(a.c.H, a.nsplit, a.row_tiles);
+  const int h = at_wg.h, sp = at_wg.part, tile_row = at_wg.low, b = at_wg.high;
+  const int len = length_of(a, b);
+  int row0, n;
+  kv_rows(a.s, b, row0, n);
+  const int r0 = tile_row * kRowTile;
+  if (r0 >= n * a.G) return;
+  const Parts pt = parts_of<kTree != kNoSets>(a, len, n, r0);
+  const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
+  // rows that see nothing are left to the first part, or to the join launch
+  if (t0 >= t1 && a.nsplit > 1 && !(a.tags && pt.parts == 0 && sp == 0)) return;
+  few_rows<D, kFine, kTree, 4, true>(a, h, b, tile_row, sp, len, row0, n, r0, pt, t0, t1);
+}
+
 // ---- many query rows -------------------------------------------------------
 // Workgroup: wavefronts of 32 query rows of one kv head, over one part of their
 // tokens, a stage of 64 tokens at a time.  S^T = K Q^T (32 x 32 x 16), softmax in
@@ -817,6 +822,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
 // wavefront (1850 -> 2430: past 256 registers every operand is copied between the
 // two files), the row sums as dot products of the rounded weights (1846 ->
 // 1855).
+// Attention by sets: query rows that k_kv_prefill has in few_rows, with all wavefronts of the
+// workgroup, when no more are left of a sequence.  One wavefront of 32 rows, and the others
+// idle, takes most of the time of a full tile: it has no other's instructions to run between its
+// own.  Heads of 128, 8 kv heads with 8 query heads each, us, without and with: 32 sequences of 33 rows on
+// 4063 tokens 227, 187; 36 rows 226, 222; 64 of up to 33 on up to 1000 95, 77; up to 500
+// 65, 56; heads of 64, 33 rows on 4063 131, 108; more than 32 rows are slower that way (38 rows, 48
+// left: 225, 259).
+constexpr int kLastRows = 32;
 template <int D, int W>
 struct Prefill {
   static constexpr int kStrips = 2;                // a stage
@@ -882,6 +895,16 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void k_kv_prefill(AttnArg
   const Parts pt = parts_of<kTree != kNoSets>(a, len, n, r0);
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   if (t0 >= t1 && a.nsplit > 1) return;
+  if constexpr (kTree)
+    if (rows - r0 <= kLastRows) {
+      const int e0 = 2 * t0, e1 = min(2 * t1, (pt.hi + kSpan - 1) / kSpan);
+#pragma unroll 1
+      for (int x = r0; x < rows; x += kRowTile) {
+        if (x > r0) __syncthreads();  // what holds the rows before
+        few_rows<D, kFine, kTree, W, false>(a, h, b, 0, sp, len, row0, n, x, pt, e0, e1);
+      }
+      return;
+    }
   if (t0 != guess) id0 = blocks_at(t0), id1 = blocks_at(t0 + kBatch), id2 = blocks_at(t0 + 2 * kBatch);
 
   // this wavefront's rows (past the end: the last row again, never written)
@@ -1571,7 +1594,7 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
     auto prefill = [&](auto w) {
       using C = Prefill<D, decltype(w)::value>;
       hipLaunchKernelGGL((k_kv_prefill<D, C::kWaves, kFine, kTree>), dim3((unsigned)p.blocks), dim3(C::kThreads),
-                         C::kLds, stream, a);
+                         std::max<size_t>(C::kLds, kTree ? (size_t)C::kWaves * kRowTile * (D + 4 + 3) * 4 : 0), stream, a);
     };
     if constexpr (D != 256)
       if (p.waves == 8) prefill(std::integral_constant<int, 8>{});

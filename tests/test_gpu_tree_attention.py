@@ -171,6 +171,41 @@ def test_trees_many_rows(msq, D, waves, split):
         attend(msq, p, q, table, lens + [0] * idle, counts_all, window=window, dtype=torch.float32)
 
 
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("D,waves", [(64, 4), (128, 4), (128, 8), (256, 4)])
+def test_last_rows_of_many(msq, D, waves, G, split):
+    """Row tiles of one row, of 16, 17, 32 and 33, alone or behind full ones, in the kernel for many rows: its
+    workgroups take those of up to 32 otherwise."""
+    P, tile = 64, 32 * waves // G
+    n = 2 * tile + 5
+    counts = [n, tile + 1, tile + max(1, 16 // G), tile + 16 // G + 1, tile + 32 // G, tile + 32 // G + 1, 1, 2, 32 // G, 0]
+    c = msq.allocate_kv_cache(1, 1, D, P)
+    plans = [(w, i, msq.kv_attention_plan(c, sum(counts), G, len(counts) + i, w, n)) for w in (12, 20, 40, 64)
+             for i in (0, 5, 20, 50, 100, 200)]
+    plans = [f for f in plans if f[2]["wavefronts"] == waves and f[2]["tile_rows"] == 32 * waves
+             and (f[2]["parts"] > 1) == split]
+    if not plans:
+        pytest.skip("no plan of these sizes")
+    width, idle, plan = plans[0]
+    print("last rows", D, waves, G, width, idle, plan, flush=True)
+    rng = np.random.default_rng(D + waves + G)
+    longest = width * P - n
+    lens = [b + m for b, m in zip([longest, longest - 70, 0, 33, longest - 1, 300, 200, longest, 64, 100], counts)]
+    table, blocks = scattered(rng, lens, P)
+    table = np.concatenate([table, np.full((len(lens), width - table.shape[1]), -1)], 1)
+    table[1, 2] = -1  # an absent block
+    p = Pair(msq, blocks, 1, D, P, seed=D, fill=float("nan"))
+    p.write(table, [0] * len(lens), lens)
+    table = np.concatenate([table, np.full((idle, width), -1)])
+    q = rng.normal(size=(sum(counts), G, D))
+    rest = [np.zeros((0, 0), bool)] * idle
+    for sets, window in (([T.ancestors(random_tree(rng, m)) for m in counts], 0),
+                         ([rng.random((m, m)) < 0.3 for m in counts], 40)):
+        for dtype, out in ((torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.bfloat16, torch.float32)):
+            attend(msq, p, q, table, lens + [0] * idle, sets + rest, dtype=dtype, out=out, window=window)
+
+
 @pytest.mark.parametrize("D,G", [(64, 1), (128, 16), (256, 3)])
 def test_any_sets(msq, D, G):
     """Sets that are no trees: empty ones, ones without the row itself, of later rows; a cache that holds
