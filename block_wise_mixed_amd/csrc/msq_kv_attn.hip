@@ -44,7 +44,7 @@
 // 0.7e-4, at 4% of the time of many rows; not taken.  Attention by sets has the weights in
 // two terms too where the results are fp32 (kSetsFine), which are then 1e-7 to 1e-6 away;
 // bf16 results, fp32 ones of bf16 and of fp32 queries: 4 trees of 64 on up to 131000 tokens, 64
-// query heads on 8 of 128, 1030, 1410, 1750 us; one of 26 on 751, 32 heads on 8, 9.8, 10.6, 11.8.
+// query heads on 8 of 128, 1030, 1410, 1750 us; one of 26 on 751, 32 heads on 8, 8.7, 9.2, 10.2.
 #include <hip/hip_runtime.h>
 #include <unistd.h>
 
@@ -453,7 +453,7 @@ extern __shared__ __align__(16) unsigned char smem_kv[];
 
 // ---- few query rows --------------------------------------------------------
 // Workgroup: 16 query rows (new tokens x the heads of one kv head) and one
-// part of their tokens; its four wavefronts take the part's tiles of 32
+// part of their tokens; its four wavefronts (by sets also eight) take the part's tiles of 32
 // tokens in turn, straight from HBM into registers (the cache order is the
 // operand order), the next tile's loads in flight during the current one's
 // products.  S^T = K Q^T (16 x 16 x 32, tokens down, rows across), whose
@@ -776,8 +776,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int h, int b, int ti
   if (a.lse && d0 == 0) a.lse[orow] = l == 0.f ? -INFINITY : kLn2 * (m + log2_fast(l));
 }
 
-template <int D, bool kFine, Sets kTree>
-__global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
+template <int D, bool kFine, Sets kTree, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : kWaves == 8 ? 2 : D == 128 ? 3 : 4) void k_kv_decode(AttnArgs a) {
   const Place at_wg = place_of(a.c.H, a.nsplit, a.row_tiles);
   const int h = at_wg.h, sp = at_wg.part, tile_row = at_wg.low, b = at_wg.high;
   const int len = length_of(a, b);
@@ -789,7 +789,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void k_kv_dec
   const int t0 = pt.first + sp * pt.span, t1 = min(t0 + pt.span, pt.end);
   // rows that see nothing are left to the first part, or to the join launch
   if (t0 >= t1 && a.nsplit > 1 && !(a.tags && pt.parts == 0 && sp == 0)) return;
-  few_rows<D, kFine, kTree, 4, true>(a, h, b, tile_row, sp, len, row0, n, r0, pt, t0, t1);
+  few_rows<D, kFine, kTree, kWaves, true>(a, h, b, tile_row, sp, len, row0, n, r0, pt, t0, t1);
 }
 
 // ---- many query rows -------------------------------------------------------
@@ -1346,6 +1346,7 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int rows) {
 // ---- host ------------------------------------------------------------------
 struct AttnPlan {
   int waves;  // of k_kv_prefill; 0: k_kv_decode
+  bool wide;  // of k_kv_decode: eight wavefronts, not four
   int tile_rows, tile_tokens, row_tiles, nsplit, span_tiles;
   int64_t blocks;     // workgroups of the attention launch
   size_t workspace, ml_at, tags_at;  // tags_at 0: the parts are joined by a launch of their own
@@ -1501,22 +1502,33 @@ size_t most_workspace(const Shape& z, int64_t longest) {
 // 104 rows on 777 8.6, 7.2, 7.6; on 1500 9.4, 7.9, 10.0; 6000 12.9, 12.3, 27.2; of 256 (where the launch
 // joins 2) on 777 15.2, -, 15.3.  A call without a launch for the join costs the host 3 us
 // less.  The workspace stays within what other calls of these sizes need.
-constexpr int kTreeTiles = 28, kTreeParts = 4, kTreeJoined = 192;
+// Eight wavefronts a workgroup, one a compute unit, where that leaves as many wavefronts at
+// work in fewer parts (not of heads of 256: registers): more of the join is in LDS and a
+// wavefront has fewer tiles one after another.  With four, eight: 104 rows on 777 9.4, 8.6; on 1500 11.9,
+// 10.3; 6000 17.4, 14.8; 20000 32.9, 31.5; 32 rows on 100000 56.9, 40.0; 4 trees of 104 rows on 1500 17.3,
+// 12.4; 10000 45.2, 42.6; heads of 64, 104 rows on 777 7.6, 6.7; on 6000 12.8, 11.6; up to kWideTiles tiles
+// they start later than they save: 104 rows on 200 6.0, 6.5; on 300 6.8, 6.7.
+constexpr int kTreeTiles = 28, kTreeParts = 4, kTreeJoined = 192, kWideTiles = 8;
 void tree_parts(const Shape& z, int64_t tiles, AttnPlan& p) {
-  if (p.waves || z.rows <= kRowTile || p.nsplit == 1) return;
-  int parts = p.nsplit;
+  if (p.waves || z.rows <= kRowTile) return;
+  const int64_t items = z.all(kRowTile);
+  int64_t parts = p.nsplit;
   if (tiles <= kTreeTiles)
     parts = 1;
   else if (tiles <= kTreeJoined && parts > kTreeParts && z.tagged_parts() >= kTreeParts &&
            z.tags_end(kTreeParts) <= p.workspace)
     parts = kTreeParts;
+  const int64_t wide = std::min({parts, 256 / items, (tiles + 7) / 8});
+  if (z.D != 256 && tiles > kWideTiles && wide > 0 && 2 * wide >= parts) p.wide = true, parts = wide;
   if (parts == p.nsplit) return;
-  p.nsplit = parts;
+  const size_t most = p.workspace;
+  p.nsplit = (int)parts;
   p.span_tiles = (int)((tiles + parts - 1) / parts);
-  p.blocks = z.all(kRowTile) * parts;
+  p.blocks = items * parts;
   p.ml_at = z.partials(parts);
-  p.tags_at = parts > 1 ? z.tags_at(parts) : 0;
-  p.workspace = parts > 1 ? z.tags_end(parts) : 0;
+  const bool tagged = parts > 1 && parts <= z.tagged_parts() && z.tags_end(parts) <= most;
+  p.tags_at = tagged ? z.tags_at(parts) : 0;
+  p.workspace = tagged ? z.tags_end(parts) : z.workspace(parts);
 }
 
 // Sizes only; MSQ_OK with blocks == 0 for an empty call.  most: also the most
@@ -1600,8 +1612,15 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& p, hipStream_t stream)
       if (p.waves == 8) prefill(std::integral_constant<int, 8>{});
     if (p.waves == 4) prefill(std::integral_constant<int, 4>{});
   } else {
-    const size_t lds = 4 * kRowTile * (D + 4 + 3) * 4;
-    hipLaunchKernelGGL((k_kv_decode<D, kFine, kTree>), dim3((unsigned)p.blocks), dim3(256), lds, stream, a);
+    auto decode = [&](auto w) {
+      constexpr int kWaves = decltype(w)::value;
+      const size_t lds = kWaves * kRowTile * (D + 4 + 3) * 4;
+      hipLaunchKernelGGL((k_kv_decode<D, kFine, kTree, kWaves>), dim3((unsigned)p.blocks), dim3(64 * kWaves), lds,
+                         stream, a);
+    };
+    if constexpr (kTree != kNoSets && D != 256)
+      if (p.wide) decode(std::integral_constant<int, 8>{});
+    if (!p.wide) decode(std::integral_constant<int, 4>{});
   }
   if (p.nsplit > 1 && !p.tags_at) {
     const int rows = a.s.batch * a.s.max_count * a.Hq;

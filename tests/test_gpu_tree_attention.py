@@ -171,6 +171,30 @@ def test_trees_many_rows(msq, D, waves, split):
         attend(msq, p, q, table, lens + [0] * idle, counts_all, window=window, dtype=torch.float32)
 
 
+@pytest.mark.parametrize("D,H,G,before,counts", [
+    (64, 1, 4, [300, 256, 10], [9, 26, 5]), (128, 2, 4, [2500, 700], [26, 3]), (64, 2, 3, [6100, 31, 4000], [17, 0, 6]),
+    (128, 1, 8, [21000, 5], [3, 4]), (64, 1, 5, [30000], [7]), (128, 8, 8, [900, 1300, 33], [33, 26, 40])])
+def test_rows_on_middle_lengths(msq, D, H, G, before, counts):
+    """Row tiles in one part, in parts joined inside the launch and by a launch of their own, each twice with
+    a workspace that holds what the last call left."""
+    P, rng = 64, np.random.default_rng(D + G)
+    lens = [a + n for a, n in zip(before, counts)]
+    table, blocks = scattered(rng, lens, P)
+    table[0, 1] = -1
+    p = Pair(msq, blocks, H, D, P, seed=G, fill=float("nan"))
+    p.write(table, [0] * len(lens), lens)
+    q = rng.normal(size=(sum(counts), H * G, D))
+    most = max(counts)
+    ws = torch.zeros(msq.kv_attention_workspace_bytes(p.gpu, sum(counts), H * G, len(lens), most, table.shape[1] * P),
+                     dtype=torch.uint8, device="cuda")
+    for sets, window in (([T.ancestors(random_tree(rng, n)) for n in counts], 0),
+                         ([rng.random((n, n)) < 0.3 for n in counts], 600)):
+        for dtype, out in ((torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.bfloat16, torch.float32)):
+            once, again = (attend(msq, p, q, table, lens, sets, dtype=dtype, out=out, window=window, workspace=ws)
+                           for _ in range(2))
+            assert torch.equal(once, again)
+
+
 @pytest.mark.parametrize("split", [False, True])
 @pytest.mark.parametrize("G", [1, 8])
 @pytest.mark.parametrize("D,waves", [(64, 4), (128, 4), (128, 8), (256, 4)])
