@@ -622,8 +622,8 @@ msq_status msq_draft_tree(const int32_t *parents, const int32_t *offset, int32_t
  * with a window the last window of them all.  Any sets will do, also empty ones and
  * ones without the row itself.  attn->causal must be set.  fp32 results come of queries
  * and weights of 22 bits (bf16 ones as msq_kv_attention's).  Workspace and errors as
- * msq_kv_attention's, the plan too but for fewer parts of few rows;
- * MSQ_ERR_INVALID_ARG also for null or misaligned sets, MSQ_ERR_SHAPE for words < 1. */
+ * msq_kv_attention's (tokens of more than 16 query rows a kv head may be cut into fewer
+ * parts than there); MSQ_ERR_INVALID_ARG also for null or misaligned sets, MSQ_ERR_SHAPE for words < 1. */
 msq_status msq_kv_attention_tree(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const msq_kv_attn *attn,
                                  const uint32_t *sets, int32_t words, void *workspace, size_t workspace_bytes,
                                  hipStream_t stream);
