@@ -686,8 +686,10 @@ extern "C" msq_status msq_verify_draft(const msq_draft* d, void* workspace, size
       !aligned_to(d->token, 4) || !aligned_to(d->taken, 4) || !aligned_to(d->path, 4) ||
       !aligned_to(d->target, size) || (drawn && !aligned_to(d->draft, size)))
     return MSQ_ERR_INVALID_ARG;
-  if (workspace_bytes < p.workspace) return MSQ_ERR_BUFFER_TOO_SMALL;
-  if (!workspace || !aligned_to(workspace, 256)) return MSQ_ERR_INVALID_ARG;
+  // (without rows no workgroup gets as far as the workspace, and `uniform`, an array of as many numbers
+  // as rows, may be null in either way)
+  if (rows && workspace_bytes < p.workspace) return MSQ_ERR_BUFFER_TOO_SMALL;
+  if (rows && (!workspace || !aligned_to(workspace, 256))) return MSQ_ERR_INVALID_ARG;
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   a.V = d->vocab;
   a.tokens = d->tokens, a.parents = d->parents, a.uniform = d->uniform;

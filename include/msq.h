@@ -669,8 +669,8 @@ typedef struct {
  * Entries that are negative, NaN or infinite count as 0 by chance; a number outside [0, 1]
  * or NaN as the nearer end or 0; a token outside 0 .. vocab - 1 is not taken.  All
  * arithmetic is fp64.  Rows outside every sequence: path is left as it is.
- * workspace: msq_verify_draft_workspace_bytes, 256-byte aligned, holding anything; calls that
- * share one must be ordered on one stream.  One launch, asynchronous, and the same results
+ * workspace: msq_verify_draft_workspace_bytes, 256-byte aligned, holding anything (none without
+ * rows); calls that share one must be ordered on one stream.  One launch, asynchronous, and the same results
  * every time.  Errors: MSQ_ERR_INVALID_ARG, MSQ_ERR_SHAPE, MSQ_ERR_BUFFER_TOO_SMALL,
  * MSQ_ERR_HIP. */
 msq_status msq_verify_draft(const msq_draft *d, void *workspace, size_t workspace_bytes, hipStream_t stream);

@@ -228,3 +228,16 @@ def test_one_workspace_two_graphs_and_a_stream(msq, greedy):
             want = s["call"](stream=side)
             torch.cuda.current_stream().wait_stream(side)
             assert all(torch.equal(a, b) for a, b in zip(s["out"], want)), step
+
+
+@pytest.mark.parametrize("greedy", [False, True])
+def test_no_rows_in_the_workspace_of_more(msq, greedy):
+    """A call without rows fits the workspace of calls with more of them (an empty tensor has no address, so
+    nothing tells the two ways apart), and needs none itself."""
+    B, V = 4, 32000
+    ws = torch.empty(msq.verify_draft_workspace_bytes(20, B, V, greedy=greedy), dtype=torch.uint8, device="cuda")
+    u = None if greedy else torch.zeros(0, device="cuda")
+    for space in (ws, ws[:0]):
+        for kw in (dict(offset=i32([0] * (B + 1))), dict(batch=B)):
+            token, taken, path = msq.verify_draft(i32([]), torch.zeros(0, V, device="cuda"), uniform=u, workspace=space, **kw)
+            assert token.tolist() == [-1] * B and taken.tolist() == [0] * B and path.numel() == 0
