@@ -161,6 +161,12 @@ enum Drafts { kChosen, kDrawnOne, kDrawn };
 // is max(scale p - share q, 0): what max(r / m - q, 0) has brought to 0 stays 0, so the
 // steps one after another, r / m - q each, come to one multiple of p and one of q
 // (scale / m and share / m + 1), and no row is gone through more than once for a step.
+// Both multiples are large where m is small, and what rounding leaves of their difference grows
+// with them: past 2^53 it is more than q, and entries that have nothing left would get some.  So
+// steps are put together up to a scale of kMostScale (1 / scale is the probability that none of
+// these siblings is taken); a step past it begins multiples of its own, of what those before it
+// (`steps` pairs in `step`) leave.
+constexpr double kMostScale = 16.0;
 template <typename T>
 struct Row {
   const T *p, *q;
@@ -168,11 +174,20 @@ struct Row {
   bool aligned;
   int count, first;
   const int *next, *token;
+  int steps;
+  const double2* step;
   double scale, share;
 };
-template <typename T>
-__device__ inline double left_of(const Row<T>& row, double p, double q) {
-  return fmax(fma(row.scale, p, -row.share * q), 0.0);
+// each(f): f(p, q) of all entries that a lane has, p becomes what is left.
+template <typename T, Drafts kWay, typename Each>
+__device__ inline void left_of(const Row<T>& row, Each&& each) {
+#pragma unroll 1
+  for (int k = 0;; ++k) {
+    const bool last = kWay != kDrawn || k >= row.steps;
+    const double2 by = last ? make_double2(row.scale, row.share) : row.step[k];
+    each([&](double& p, double q) { p = fmax(fma(by.x, p, -by.y * q), 0.0); });
+    if (last) break;
+  }
 }
 
 // What is left there of N tiles from v on (v + lead a multiple of 4), all read at once.
@@ -204,7 +219,12 @@ __device__ inline void left_at(const Row<T>& row, int v, int lane, double (&r)[N
       each([&](double& p, float, int at) { p = t - 4 * lane == at ? 0.0 : p; });
     }
   } else {
-    each([&](double& p, float q, int) { p = left_of(row, p, mass(q)); });
+    left_of<T, kWay>(row, [&](auto&& f) {
+      each([&](double& p, float& q, int) {
+        if constexpr (kWay == kDrawn) asm volatile("" : "+v"(q));  // widened anew in each turn: no registers for it
+        f(p, mass(q));
+      });
+    });
   }
 }
 
@@ -248,6 +268,7 @@ __global__ __launch_bounds__(64 * waves_of(kWay)) void k_verify_chance(VerifyArg
   __shared__ float prob[kMostRows], drawn[kDraft ? kMostRows : 1], number_of[kMostRows];
   __shared__ double shared_sum[kWaves];
   __shared__ double fresh[kMostSlices];  // sums of slices made by the workgroup that joins
+  __shared__ double2 step[kWay == kDrawn ? kMostRows : 1];
   __shared__ int complete, last_of[kWaves], found;
   const int part = blockIdx.x % (unsigned)a.parts, b = blockIdx.x / (unsigned)a.parts;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -276,12 +297,14 @@ __global__ __launch_bounds__(64 * waves_of(kWay)) void k_verify_chance(VerifyArg
   row.first = 0;
   row.next = next;
   row.token = token;
+  row.step = step;
   auto reach = [&](int i) {
     row.p = target + (row0 + i) * a.ts;
     row.q = kDraft ? draft + (row0 + i) * a.ds : row.p;
     row.lead = lead_of(row.p);
     row.aligned = lead_of(row.q) == row.lead;
     row.count = 0;
+    row.steps = 0;
     row.scale = 1.0;
     row.share = 0.0;
   };
@@ -317,7 +340,7 @@ __global__ __launch_bounds__(64 * waves_of(kWay)) void k_verify_chance(VerifyArg
             m = 0.0;
             for (int w = 0; w < kWaves; ++w) m += shared_sum[w];
           }
-          r = left_of(row, r, q);
+          left_of<T, kWay>(row, [&](auto&& f) { f(r, q); });
         }
       }
       if (x >= 0 && number(number_of[j]) * q * m < r) {
@@ -328,6 +351,16 @@ __global__ __launch_bounds__(64 * waves_of(kWay)) void k_verify_chance(VerifyArg
         reach(j);
       } else {
         if constexpr (kDraft) {
+          if constexpr (kWay == kDrawn) {
+            if (m > 0.0 && row.count > 0 && !(row.scale <= kMostScale * m)) {
+              // (as with `next`; the last wavefront that read an entry of another row's steps has since
+              // come to the sum above)
+              step[row.steps] = make_double2(row.scale, row.share);
+              __builtin_amdgcn_wave_barrier();
+              ++row.steps;
+              row.scale = 1.0, row.share = 0.0;
+            }
+          }
           if (m > 0.0) row.scale /= m, row.share /= m;
           row.share += 1.0;
           m = -1.0;

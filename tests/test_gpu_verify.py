@@ -241,3 +241,42 @@ def test_no_rows_in_the_workspace_of_more(msq, greedy):
         for kw in (dict(offset=i32([0] * (B + 1))), dict(batch=B)):
             token, taken, path = msq.verify_draft(i32([]), torch.zeros(0, V, device="cuda"), uniform=u, workspace=space, **kw)
             assert token.tolist() == [-1] * B and taken.tolist() == [0] * B and path.numel() == 0
+
+
+def test_siblings_of_nearly_the_target(msq):
+    """A drafter that differs from the target by one unit of one entry and 1e-20 of another: what is left
+    after the first sibling is 1e-20 in all, and every entry where both are equal has nothing."""
+    V, n = 50, 6
+    rng = np.random.default_rng(12)
+    for trial in range(20):
+        p = softmax(rng.normal(size=(1, V))).repeat(n, 0)
+        q = p.copy()
+        p[:, 1] = np.nextafter(q[:, 1], np.float32(0))
+        p[:, 0], q[:, 0] = 1e-20, 0
+        tokens = np.concatenate([[0, 1], rng.integers(2, V, size=n - 2)])
+        u = np.concatenate([[rng.random()], np.ones(n - 1)]).astype(np.float32)
+        token, taken, _ = check(msq, [n], tokens, np.array([-1] + [0] * (n - 1)), torch.from_numpy(p), torch.from_numpy(q), u)
+        assert (token[0], taken[0]) == (0, 1)
+
+
+@pytest.mark.parametrize("V", [2, 3, 8, 50, 9001])
+def test_very_many_siblings(msq, V):
+    """Some hundred siblings of one row, none taken: the entries that the target has most of beside the
+    drafter stay, however small what was left of the first distribution has become.  In turn all of them
+    below the first row, or half of them, then one that is taken, and the others below it."""
+    n = 200
+    rng = np.random.default_rng(V)
+    for trial in range(8):
+        p, q = softmax(rng.normal(size=(1, V)) * 2), softmax(rng.normal(size=(1, V)) * 2)
+        if trial < 2:
+            p[0], q[0] = np.eye(V)[0], 0.5 * np.eye(V)[0] + 0.5 * np.eye(V)[1]
+        share = p[0] / np.maximum(q[0], 1e-9)
+        tokens = np.full(n, int(np.argmin(share)))   # nothing is left of it from the first sibling on
+        u = np.ones(n, np.float32)
+        u[0] = rng.random()
+        parents = np.array([-1] + [0] * (n - 1))
+        if trial % 2:
+            tokens[100], u[100] = int(np.argmax(share)), 0
+            parents[101:] = 100
+        _, taken, _ = check(msq, [n], tokens, parents, torch.from_numpy(p.repeat(n, 0)), torch.from_numpy(q.repeat(n, 0)), u)
+        assert taken[0] == 1 + trial % 2
