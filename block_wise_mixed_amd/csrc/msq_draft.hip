@@ -579,7 +579,9 @@ __global__ __launch_bounds__(256) void k_verify_largest(VerifyArgs a) {
     }
     if (i < n) {
       parent[i] = parent_of(a.parents, row0, i);
-      token[i] = a.tokens[row0 + i];
+      // (kNobody, the largest of a row of NaN, is no token either)
+      const int t = a.tokens[row0 + i];
+      token[i] = t >= 0 && t < a.V ? t : -1;
     }
   }
   __syncthreads();

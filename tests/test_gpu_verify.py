@@ -280,3 +280,13 @@ def test_very_many_siblings(msq, V):
             parents[101:] = 100
         _, taken, _ = check(msq, [n], tokens, parents, torch.from_numpy(p.repeat(n, 0)), torch.from_numpy(q.repeat(n, 0)), u)
         assert taken[0] == 1 + trial % 2
+
+
+def test_largest_of_nothing_takes_no_token(msq):
+    """Below a row of NaN no token is taken, whatever its number; nor one past the vocabulary elsewhere."""
+    V = 700
+    x = np.full((3, V), np.nan, np.float32)
+    for t in (2 ** 31 - 1, -1, -2 ** 31, V, 0):
+        token, taken, path = check(msq, [3], np.array([0, t, t]), np.array([-1, 0, 1]), torch.from_numpy(x), None, None)
+        assert token[0] == -1 and taken[0] == 1
+        check(msq, [3], np.array([0, t, t]), np.array([-1, 0, 1]), torch.from_numpy(np.nan_to_num(x)), None, None)
