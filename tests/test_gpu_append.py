@@ -182,3 +182,55 @@ def test_rows_left_alone_and_graph(msq):
         n = int(first[0]) + 3
         for x, w in zip(msq.kv_read(cache, table, i32([0] * 3), total=3 * n), msq.kv_read(other, table, i32([0] * 3), total=3 * n)):
             assert torch.equal(x, w), step
+
+
+def heads_a_workgroup(D, P, H, batch, most, width):
+    """Heads that a workgroup of keys takes, by the rule at launch_append (msq_kv_append.hip)."""
+    strips, lists = P // 32, batch * min((most + P - 2) // P + 1, width)
+    waves = strips * (D // (64 if D == 64 or (most >= 16 and strips * (D // 64) <= 16) else 128))
+    return min(max(lists * H * waves // (12 * 256), 1), H)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,P,H,batch,tokens,part,interleaved", [
+    (64, 32, 7, 256, 40, 64, False), (128, 64, 5, 64, 100, 96, True), (128, 128, 7, 40, 200, 128, False),
+    (256, 64, 5, 48, 90, 256, False), (128, 64, 5, 700, 9, 128, False)])
+def test_heads_of_a_workgroup(msq, D, P, H, batch, tokens, part, interleaved, dtype):
+    """Keys whose workgroups take from one to all of the heads one after another, the last of them fewer: the
+    blocks that a call may reach (its max_count, which may be larger than any sequence) make that
+    many workgroups.  Rows from a block's start, and behind earlier ones whose codes move."""
+    rng = np.random.default_rng(D + P + H)
+    width = 64
+    rot = msq.Rotary(msq.rotary_frequencies(part), interleaved)
+    f = rot.frequencies.cpu().numpy()
+    lens = [int(n) for n in rng.integers(tokens // 2, tokens + 1, size=batch)]
+    more = [int(n) for n in rng.integers(0, tokens + 1, size=batch)]
+    table, blocks = scattered(rng, [a + b for a, b in zip(lens, more)], P)
+    table = np.concatenate([table, np.full((batch, width - table.shape[1]), -1)], 1)
+    p = Pair(msq, blocks, H, D, P, seed=D)
+    writes = []
+    for first, counts, spread in (([0] * batch, lens, 1.0), (lens, more, 3.0)):
+        k, kt = rounded(p.tokens(sum(counts), spread), dtype)
+        v, vt = rounded(p.tokens(sum(counts), spread), dtype)
+        off = offsets(counts)
+        at = np.concatenate([np.arange(n) + s for s, n in zip(first, counts)])
+        p.ref.write(R.rotate(k, at, f, interleaved), v, table, first, off)
+        writes.append((kt, vt, i32(first), i32(off), max(counts)))
+    met, want = set(), None
+    held = lambda: (p.gpu.k_codes, p.gpu.v_codes, p.gpu.k_scale, p.gpu.v_scale)
+    for blocks_reached in (0, 2, 4, 6, 8, 12, 17, 26, 34, 64):
+        mosts = [max(w[4], min(blocks_reached * P, len(w[0]))) if tokens >= 16 else w[4] for w in writes]
+        heads = [heads_a_workgroup(D, P, H, batch, most, width) for most in mosts]
+        print(f"heads D={D} P={P} of {H}: {heads} at max_count {mosts}", flush=True)
+        for t in held():
+            t.fill_(7)
+        for (kt, vt, first, off, _), most in zip(writes, mosts):
+            msq.kv_append(p.gpu, kt, vt, i32(table), first, rot, offset=off, max_count=most)
+        if want is None:
+            p.check()  # against the oracle; the others against this one
+            want = [t.clone() for t in held()]
+        assert all(torch.equal(a, b) for a, b in zip(held(), want))
+        met.update(heads)
+        if tokens < 16:
+            break
+    assert any(1 < n < H and H % n for n in met), met
