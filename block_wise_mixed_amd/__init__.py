@@ -233,6 +233,8 @@ def load_library():
     lib.msq_kv_attention.argtypes = [cache_p, seqs_p, attn_p, vp, sz, vp]
     lib.msq_kv_attention.restype = ctypes.c_int
     i32 = ctypes.c_int32
+    lib.msq_kv_attention_tree_plan.argtypes = [cache_p, seqs_p, attn_p, ctypes.POINTER(_KvPlan)]
+    lib.msq_kv_attention_tree_plan.restype = ctypes.c_int
     lib.msq_kv_attention_tree.argtypes = [cache_p, seqs_p, attn_p, vp, i32, vp, sz, vp]
     lib.msq_kv_attention_tree.restype = ctypes.c_int
     lib.msq_rotary_apply.argtypes = [ctypes.POINTER(_Rotary), ctypes.POINTER(_RotaryRows), vp, i64, vp]
@@ -824,15 +826,16 @@ def kv_attention_workspace_bytes(cache: KVCache, rows: int, q_heads: int, batch:
 
 def kv_attention_plan(cache: KVCache, rows: int, q_heads: int, batch: int, table_entries: int,
                       max_count: int = 0, max_kv_len: int = 0, causal: bool = True, window: int = 0,
-                      ragged: bool = True) -> dict:
-    """How kv_attention runs a call of these sizes (msq_kv_attention_plan): tile_rows and
-    wavefronts of its kernel's workgroups, the parts that a tile's tokens are split into, join
-    ("none", "inside" the launch or by a "launch" of its own) and workspace_bytes.  Arguments as
-    of kv_attention; ragged: whether it is given an offset."""
+                      ragged: bool = True, tree: bool = False) -> dict:
+    """How kv_attention runs a call of these sizes (msq_kv_attention_plan, for a call by sets
+    msq_kv_attention_tree_plan): tile_rows and wavefronts of its kernel's workgroups, the parts that
+    a tile's tokens are split into, join ("none", "inside" the launch or by a "launch" of its own)
+    and workspace_bytes.  Arguments as of kv_attention; ragged, tree: whether it is given an offset, sets."""
     s, a = _kv_sizes(rows, q_heads, batch, table_entries, max_count, max_kv_len, causal, window, ragged)
     plan = _KvPlan()
-    _check(load_library().msq_kv_attention_plan(cache._desc or cache.descriptor(), s, a, plan),
-           "msq_kv_attention_plan")
+    lib = load_library()
+    call = lib.msq_kv_attention_tree_plan if tree else lib.msq_kv_attention_plan
+    _check(call(cache._desc or cache.descriptor(), s, a, plan), "msq_kv_attention_plan")
     return dict(tile_rows=plan.tile_rows, wavefronts=plan.wavefronts, parts=plan.parts,
                 join=("none", "inside", "launch")[plan.join], workspace_bytes=plan.workspace_bytes)
 

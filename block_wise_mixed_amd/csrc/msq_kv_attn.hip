@@ -1653,23 +1653,37 @@ uint64_t next_call() {
 
 using namespace msq;
 
-extern "C" msq_status msq_kv_attention_plan(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
-                                            const msq_kv_attn* attn, msq_kv_plan* plan) {
-  if (!attn || !plan) return MSQ_ERR_INVALID_ARG;
+namespace {
+
+msq_status attention_plan(const msq_kv_cache* cache, const msq_kv_seqs* seqs, const msq_kv_attn* attn, bool tree,
+                          msq_kv_plan* plan) {
+  if (!attn || !plan || (tree && !attn->causal)) return MSQ_ERR_INVALID_ARG;
   KvCacheView c;
   KvSeqsView s;
   AttnPlan p;
   msq_status st = kv_views(cache, seqs, c, s);
-  if (st == MSQ_OK) st = plan_attn(c, s, *attn, cache->head_dim, p);
+  if (st == MSQ_OK) st = plan_attn(c, s, *attn, cache->head_dim, p, nullptr, tree);
   if (st != MSQ_OK) return st;
   *plan = msq_kv_plan{};
   if (p.blocks == 0) return MSQ_OK;
   plan->tile_rows = p.tile_rows;
-  plan->wavefronts = p.waves ? p.waves : 4;
+  plan->wavefronts = p.waves ? p.waves : p.wide ? 8 : 4;
   plan->parts = p.nsplit;
   plan->join = p.nsplit == 1 ? 0 : p.tags_at ? 1 : 2;
   plan->workspace_bytes = p.workspace;
   return MSQ_OK;
+}
+
+}  // namespace
+
+extern "C" msq_status msq_kv_attention_plan(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
+                                            const msq_kv_attn* attn, msq_kv_plan* plan) {
+  return attention_plan(cache, seqs, attn, false, plan);
+}
+
+extern "C" msq_status msq_kv_attention_tree_plan(const msq_kv_cache* cache, const msq_kv_seqs* seqs,
+                                                 const msq_kv_attn* attn, msq_kv_plan* plan) {
+  return attention_plan(cache, seqs, attn, true, plan);
 }
 
 extern "C" size_t msq_kv_attention_workspace_bytes(const msq_kv_cache* cache,

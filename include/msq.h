@@ -627,6 +627,10 @@ msq_status msq_draft_tree(const int32_t *parents, const int32_t *offset, int32_t
 msq_status msq_kv_attention_tree(const msq_kv_cache *cache, const msq_kv_seqs *seqs, const msq_kv_attn *attn,
                                  const uint32_t *sets, int32_t words, void *workspace, size_t workspace_bytes,
                                  hipStream_t stream);
+/* The plan of such a call, as msq_kv_attention_plan (tiles of 16 rows may have 8 wavefronts
+ * here; MSQ_ERR_INVALID_ARG also without causal). */
+msq_status msq_kv_attention_tree_plan(const msq_kv_cache *cache, const msq_kv_seqs *seqs,
+                                      const msq_kv_attn *attn, msq_kv_plan *plan);
 
 /* One verification. */
 typedef struct {

@@ -317,3 +317,68 @@ def test_rows_left_alone_streams_and_graph(msq):
         assert torch.equal(kept[2:50], sets[2:50])
         assert torch.equal(y[2:50], call()[2:50]), step
         sets = kept
+
+
+def planned(msq, D, shapes, want):
+    """The first (counts, heads a group, idle sequences, table entries) whose call by sets has the plan (tile rows,
+    wavefronts, join) that is wanted."""
+    c = msq.allocate_kv_cache(1, 1, D, 64, device="cpu")
+    for counts, G in shapes:
+        for width in (4, 8, 16, 20, 40, 64, 256, 1024, 4096):
+            for idle in (0, 4, 10, 30, 60, 75, 100, 165, 200, 255, 300):
+                plan = msq.kv_attention_plan(c, sum(counts), G, len(counts) + idle, width, max(counts), tree=True)
+                if (plan["tile_rows"], plan["wavefronts"], plan["join"]) == want:
+                    print("planned", D, want, counts, G, idle, width, plan, flush=True)
+                    return counts, G, idle, width
+    pytest.fail(f"no plan with {want}")
+
+
+def attend_planned(msq, D, counts, G, idle, width, lens):
+    """Calls of these sizes, of every type, by sets of trees and any others, each twice in one workspace."""
+    P, rng = 64, np.random.default_rng(D + sum(counts) + width)
+    table, blocks = scattered(rng, lens, P)
+    table = np.concatenate([table, np.full((len(lens), width - table.shape[1]), -1)], 1)
+    p = Pair(msq, blocks, 1, D, P, seed=D, fill=float("nan"))
+    p.write(table, [0] * len(lens), lens)
+    table[0, 1] = -1  # an absent block
+    table = np.concatenate([table, np.full((idle, width), -1)])
+    q = rng.normal(size=(sum(counts), G, D))
+    rest, lens = [np.zeros((0, 0), bool)] * idle, lens + [0] * idle
+    # (the workspace of such calls, with a plan's own need within it)
+    need = msq.kv_attention_workspace_bytes(p.gpu, sum(counts), G, len(lens), max(counts), width * P)
+    assert msq.kv_attention_plan(p.gpu, sum(counts), G, len(lens), width, max(counts), tree=True)["workspace_bytes"] <= need
+    ws = torch.full((max(need, 256),), 255, dtype=torch.uint8, device="cuda")
+    for sets in ([T.ancestors(random_tree(rng, n)) for n in counts], [rng.random((n, n)) < 0.3 for n in counts]):
+        for dtype, out in ((torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.bfloat16, torch.float32)):
+            once, again = (attend(msq, p, q, table, lens, sets + rest, dtype=dtype, out=out, workspace=ws) for _ in range(2))
+            assert torch.equal(once, again)
+
+
+ONE, INSIDE, MORE = "none", "inside", "launch"
+FEW, SOME = [([3], 4)], [([26, 5], 4), ([70, 64, 33], 4), ([150], 4), ([40], 1), ([512, 300], 4)]
+PLANS = [(D, 16, 4, join, shapes) for D in (64, 128, 256) for join in (ONE, INSIDE, MORE) for shapes in (FEW, SOME)] + \
+        [(D, 16, 8, join, SOME) for D in (64, 128) for join in (ONE, INSIDE, MORE)] + \
+        [(D, 32 * W, W, join, SOME) for D, W in ((64, 4), (64, 8), (128, 4), (128, 8), (256, 4)) for join in (ONE, MORE)]
+
+
+@pytest.mark.parametrize("D,tile,waves,join,shapes", PLANS)
+def test_every_plan(msq, D, tile, waves, join, shapes):
+    """Every kernel, workgroup and join that a call by sets can have, named by its plan."""
+    counts, G, idle, width = planned(msq, D, shapes, (tile, waves, join))
+    lens = [min(width * 64, max(n, m)) for n, m in zip((2900, 1200, 90), counts)]
+    attend_planned(msq, D, counts, G, idle, width, lens)
+
+
+@pytest.mark.parametrize("join", [ONE, MORE])
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("D,waves", [(64, 4), (64, 8), (128, 4), (128, 8), (256, 4)])
+def test_last_rows_of_every_tile(msq, D, waves, G, join):
+    """As test_last_rows_of_many, for every kernel for many rows, unsplit and split: none may go unfound."""
+    tile = 32 * waves // G
+    n = 2 * tile + 5
+    counts = [n, tile + 1, tile + max(1, 16 // G), tile + 16 // G + 1, tile + 32 // G, tile + 32 // G + 1, 1, 2, 32 // G, 0]
+    shapes = [(counts, G), ([counts[3], counts[4]], G), ([counts[1]], G), ([counts[5]], G)]  # (few sequences: more parts)
+    counts, _, idle, width = planned(msq, D, shapes, (32 * waves, waves, join))
+    longest = min(width * 64, 2600)
+    lens = [min(longest, b) for b in (longest, longest - 70, max(counts), 33 + n, longest - 1, 300 + n, 200, longest, 64, 100)]
+    attend_planned(msq, D, counts, G, idle, width, lens[:len(counts)])

@@ -48,3 +48,27 @@ def test_binding_plan():
     assert msq.kv_attention_plan(c, 4, 32, 4, 1, ragged=False)["join"] == "none"
     with pytest.raises(msq.MsqError):
         msq.kv_attention_plan(c, 4, 30, 4, 1)
+
+
+def test_tree_plan(lib):
+    f, p = lib.msq_kv_attention_tree_plan, msq._KvPlan()
+    assert f(None, seqs(), attn(), p) == INVALID and f(cache(), None, attn(), p) == INVALID
+    assert f(cache(), seqs(), None, p) == INVALID and f(cache(), seqs(), attn(), None) == INVALID
+    assert f(cache(), seqs(), attn(causal=0), p) == INVALID
+    assert f(cache(head_dim=96), seqs(), attn(), p) == UNSUP and f(cache(), seqs(), attn(q_heads=12), p) == SHAPE
+    assert f(cache(), seqs(total=0), attn(), p) == OK
+    assert (p.tile_rows, p.wavefronts, p.parts, p.join, p.workspace_bytes) == (0, 0, 0, 0, 0)
+    # a tree of 26 of one sequence: eight wavefronts, in one part on 751 tokens, in some on 1500
+    one = dict(batch=1, total=26, max_count=26)
+    for width, parts, join in ((13, 1, 0), (24, 4, 1)):
+        assert f(cache(), seqs(table_width=width, **one), attn(), p) == OK
+        assert (p.tile_rows, p.wavefronts, p.join) == (16, 8, join) and 1 <= p.parts <= parts
+    # within what the size query gives, and as calls without sets where there are no more than 16 rows of a head
+    for batch in (1, 3, 40):
+        for most in (1, 4, 26, 64, 300):
+            for width in (1, 5, 30, 200, 3000):
+                s = seqs(batch=batch, total=batch * most, max_count=most, table_width=width)
+                other, need = plan_of(lib, cache(), s, attn()), lib.msq_kv_attention_workspace_bytes(cache(), s, attn())
+                assert f(cache(), s, attn(), p) == OK and p.workspace_bytes <= need
+                if most * 4 <= 16 or other.tile_rows > 16:
+                    assert bytes(p) == bytes(other)
